@@ -69,8 +69,9 @@ extern "C" {
 #define MOE_API
 #endif
 
-/* Element types. */
-enum { MOE_F16 = 1, MOE_BF16 = 2, MOE_F32 = 3 };
+/* Element types.  MOE_E4M3 (8-bit float, 4 exponent and 3 mantissa bits, largest
+ * value 448) is taken by the norm's output and by the key/value cache only. */
+enum { MOE_F16 = 1, MOE_BF16 = 2, MOE_F32 = 3, MOE_E4M3 = 4 };
 
 /* Status codes. */
 typedef enum {
@@ -248,6 +249,125 @@ MOE_API moe_status_t moe_decode_forward_noalloc(const moe_cfg_t* cfg, const void
  * partials. */
 MOE_API moe_status_t moe_sum_partials(const float* partials, int32_t n_parts, int64_t n, const void* residual,
                                       int32_t residual_dtype, void* out, int32_t out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder layer around the block: the norm before
+ * attention and before the block, the rotation and append of new keys and
+ * values to a paged cache, and the attention of one new token per sequence
+ * over that cache.  Conventions as above; strides are in elements, the
+ * innermost dimension is contiguous, every sum and softmax statistic is fp32.
+ * ------------------------------------------------------------------------ */
+
+/* RMS norm with the residual's addition, per row t of T:
+ *   h = x[t] (+ residual[t])                      fp32
+ *   residual_out[t] = h rounded to dtype          (optional)
+ *   y = h / sqrt(mean(h^2) + eps) * weight        (of the unrounded h)
+ *   out[t] = y rounded to dtype, or, with out_dtype MOE_E4M3,
+ *   out[t][c] = e4m3(y[c] / s), s = max(max |y|, 2^-96) / 448 over the row
+ *   (group = 0) or over each `group` columns; scales[t][.] receives s.
+ * A NaN in a row makes the row NaN, its scales included.  Sizes: T >= 0,
+ * 1 <= H <= 32768 and any row strides >= H; rows whose pointers and strides
+ * are multiples of 16 bytes with H % 8 == 0 take the wide loads.  group is 0
+ * or a power of two from 16 to 256, and then needs those wide rows (H need
+ * not be a multiple of it).  residual_out may be residual or x, and out may
+ * be x, with the same strides (in place); no other overlap. */
+typedef struct moe_norm {
+  const void* x;         /* [T, H] dtype                                     */
+  const void* residual;  /* [T, H] dtype, or NULL                            */
+  const void* weight;    /* [H] dtype                                        */
+  void* out;             /* [T, H] out_dtype                                 */
+  void* residual_out;    /* [T, H] dtype, or NULL (NULL if residual is)      */
+  float* scales;         /* [T, group ? ceil(H / group) : 1], MOE_E4M3 only  */
+  int64_t x_stride, residual_stride, out_stride, residual_out_stride; /* between rows */
+  int32_t T, H;
+  int32_t dtype;     /* MOE_F16 or MOE_BF16                                  */
+  int32_t out_dtype; /* dtype or MOE_E4M3                                    */
+  int32_t group;
+  float eps;
+} moe_norm_t;
+
+MOE_API moe_status_t moe_add_rmsnorm(const moe_norm_t* n, void* stream);
+
+/* A paged key/value cache: token j of a sequence lives in slot j % page_size
+ * of the page its block table names.  Strides tell the order of pages, tokens
+ * and heads (each a multiple of 16 bytes); a page may hold its tokens or its
+ * heads outermost. */
+typedef struct moe_kv_cache {
+  void* k;
+  void* v;
+  const float* k_scale; /* [n_kv_heads], value = stored * scale; MOE_E4M3 only, */
+  const float* v_scale; /* NULL = 1                                              */
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int32_t n_pages, page_size, n_kv_heads;
+  int32_t head_dim; /* multiple of 8 (16 for MOE_E4M3) up to 256             */
+  int32_t dtype;    /* the new tensors' dtype, or MOE_E4M3                   */
+} moe_kv_cache_t;
+
+/* Rotation of new queries and keys, and append of keys and values: per token
+ * t and head, in fp32,
+ *   u = q or k head; with norm weights first u = u / sqrt(mean(u^2) + eps) * w
+ *   for i < rot_dim / 2, with a = positions[t] * inv_freq[i] and (i, j) =
+ *   (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved:
+ *     u_i, u_j = u_i cos a - u_j sin a, u_j cos a + u_i sin a
+ *   q_out[t] = u rounded to dtype; k and v go to cache slot slots[t] / page_size,
+ *   slots[t] % page_size, rounded to the cache's dtype (MOE_E4M3: divided by the
+ *   head's scale, saturated at +-448).
+ * Angles are reduced exactly (64-bit fractions of a turn), so far positions
+ * (up to 2^31) lose nothing.  A negative slot stores nothing (padding; q_out is
+ * still written); a slot past the cache stores nothing and is recorded in the
+ * status word of ws (MOE_ERR_DEVICE from moe_query_status).  Tokens that share
+ * a slot leave either's values.  rot_dim is even, <= head_dim (0: no rotation),
+ * and a multiple of 16 unless interleaved; q and k heads of stride multiples
+ * of 16 bytes.  q_out may be q (in place).  ws: any workspace of this library
+ * (only its status word is used). */
+typedef struct moe_rope {
+  const void* q; /* [T, n_q_heads, head_dim] dtype                           */
+  const void* k; /* [T, n_kv_heads, head_dim]                                */
+  const void* v; /* [T, n_kv_heads, head_dim]                                */
+  void* q_out;   /* [T, n_q_heads, head_dim]                                 */
+  const int64_t* positions; /* [T], |position| < 2^31                        */
+  const int64_t* slots;     /* [T]                                           */
+  const float* inv_freq;    /* [rot_dim / 2], radians per position           */
+  const void* q_norm_w;     /* [head_dim] dtype, both or neither             */
+  const void* k_norm_w;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+  int32_t T, n_q_heads, rot_dim, dtype, interleaved;
+  float eps;
+} moe_rope_t;
+
+MOE_API moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_rope_t* r, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* Attention of one new token per sequence b of B over its cached tokens
+ * j in [max(0, len - window), len), len = seq_lens[b] (window 0: all):
+ *   s_j = scale * q . k_j ;  p = softmax(s) ;  out = sum_j p_j v_j ;
+ *   lse = ln sum_j exp(s_j)                         (optional, fp32)
+ * for query head h over key/value head h / (n_q_heads / n_kv_heads).  A
+ * sequence of length 0 gives zeros and lse = -infinity.  Only tokens inside the
+ * range are read, so unused table entries and unwritten slots may hold
+ * anything.  A page id outside the cache drops its tokens, and a length below 0
+ * or past the table is clamped; both are recorded in ws (MOE_ERR_DEVICE from
+ * moe_query_status).  Several new tokens of one sequence are several rows whose
+ * table rows repeat and whose lengths count up.
+ * One launch; results do not depend on timing (parts join in a fixed order).
+ * ws: moe_attention_workspace_bytes(), zero-filled once; not shared by calls
+ * that can run at the same time. */
+typedef struct moe_attention {
+  const void* q;              /* [B, n_q_heads, head_dim] dtype              */
+  void* out;                  /* [B, n_q_heads, head_dim] dtype              */
+  float* lse;                 /* [B, n_q_heads] or NULL                      */
+  const int32_t* block_table; /* [B, max_pages]                              */
+  const int32_t* seq_lens;    /* [B]                                         */
+  int64_t q_seq_stride, q_head_stride, out_seq_stride, out_head_stride, table_stride;
+  int32_t B, n_q_heads, max_pages, window, dtype;
+  float scale;
+} moe_attention_t;
+
+MOE_API size_t moe_attention_workspace_bytes(const moe_kv_cache_t* cache, int32_t n_q_heads);
+MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws,
+                                         size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read and clear the device status word of `ws`
  * (ws == NULL: the word in the built-in array of moe_decode_forward_noalloc on

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -21,7 +22,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 
-MOE_F16, MOE_BF16, MOE_F32 = 1, 2, 3
+MOE_F16, MOE_BF16, MOE_F32, MOE_E4M3 = 1, 2, 3, 4
 _DT = {MOE_F16: torch.float16, MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
 _DT_CODE = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
@@ -32,7 +33,8 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
 EXPORTS = ("moe_abi_version", "moe_workspace_bytes", "moe_workspace_init", "moe_router_topk",
            "moe_decode_forward", "moe_grouped_forward", "moe_query_status", "moe_last_error",
            "moe_get_stats", "moe_reset_stats", "moe_set_wait_timeout_ns", "moe_test_wait_timeout",
-           "moe_decode_forward_noalloc", "moe_sum_partials")
+           "moe_decode_forward_noalloc", "moe_sum_partials", "moe_add_rmsnorm", "moe_rope_append",
+           "moe_attention_workspace_bytes", "moe_paged_attention")
 
 
 class MoeError(RuntimeError):
@@ -127,6 +129,11 @@ def _load():
         "moe_test_wait_timeout": ([vp, sz, vp], ctypes.c_int),
         "moe_decode_forward_noalloc": ([cfgp, vp, vp, vp, vp, vp, vp, vp, moe_topk_t, vp, vp], ctypes.c_int),
         "moe_sum_partials": ([vp, i32, ctypes.c_int64, vp, i32, vp, i32, vp], ctypes.c_int),
+        # the structs below travel as packed bytes (struct.Struct with C alignment)
+        "moe_add_rmsnorm": ([ctypes.c_char_p, vp], ctypes.c_int),
+        "moe_rope_append": ([ctypes.c_char_p, ctypes.c_char_p, vp, sz, vp], ctypes.c_int),
+        "moe_attention_workspace_bytes": ([ctypes.c_char_p, i32], sz),
+        "moe_paged_attention": ([ctypes.c_char_p, ctypes.c_char_p, vp, sz, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -303,6 +310,194 @@ def moe_sum_partials(partials, out, residual=None, stream=None):
         rdt = _DT_CODE[residual.dtype]
     _check(_load().moe_sum_partials(_ptr(partials), partials.shape[0], n, _ptr(residual), rdt, _ptr(out),
                                     _DT_CODE[out.dtype], _stream(stream)))
+
+
+# ------------------------------------------- the layer's attention half
+# Packed forms of moe_norm_t, moe_kv_cache_t, moe_rope_t and moe_attention_t.
+_NORM_T = struct.Struct("@6P4q5if")
+_CACHE_T = struct.Struct("@4P6q5i0q")
+_ROPE_T = struct.Struct("@9P8q5if0q")
+_ATTN_T = struct.Struct("@5P5q5if0q")
+
+
+def _launch_stream(device, stream):
+    """The raw stream a call on tensors of `device` goes to."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is {torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _need_strided(t, name, shape, dtype, device):
+    """Like _need, but any strides with a contiguous last dimension."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=None, group=0, eps=1e-6, stream=None):
+    """RMS norm of ``x (+ residual)`` [T, H] times ``weight`` [H] into ``out``:
+    x's dtype, or float8_e4m3fn with ``scales`` [T, 1] (one per row) or
+    [T, ceil(H / group)].  ``residual_out`` receives the rounded sum (may be
+    ``residual`` itself).  Rows may be strided; see include/moe.h."""
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, H]")
+    T, H = shape = x.shape
+    dt, dev = x.dtype, x.device
+    if dt not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x: dtype {dt}, expected float16 or bfloat16")
+    e4m3 = out.dtype is torch.float8_e4m3fn
+    _need_strided(x, "x", shape, dt, dev)
+    _need_strided(weight, "weight", (H,), dt, dev)
+    _need_strided(out, "out", shape, out.dtype if e4m3 else dt, dev)
+    r = ro = s = rs = ros = 0
+    if residual is not None:
+        _need_strided(residual, "residual", shape, dt, dev)
+        r, rs = residual.data_ptr(), residual.stride(0) if T > 1 else H
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out without residual")
+        _need_strided(residual_out, "residual_out", shape, dt, dev)
+        ro, ros = residual_out.data_ptr(), residual_out.stride(0) if T > 1 else H
+    if (scales is not None) != e4m3:
+        raise ValueError("scales goes with a float8_e4m3fn out, and only with it")
+    if e4m3:
+        if group < 0:
+            raise ValueError("group must be >= 0")
+        _need(scales, "scales", (T, -(-H // group) if group else 1), torch.float32, dev)
+        s = scales.data_ptr()
+    code = _DT_CODE[dt]
+    args = _NORM_T.pack(x.data_ptr(), r, weight.data_ptr(), out.data_ptr(), ro, s,
+                        x.stride(0) if T > 1 else H, rs, out.stride(0) if T > 1 else H, ros,
+                        T, H, code, MOE_E4M3 if e4m3 else code, group, eps)
+    rc = _load().moe_add_rmsnorm(args, _launch_stream(dev, stream))
+    if rc:
+        _check(rc)
+
+
+class MoeKvCache:
+    """A paged key/value cache as the library takes it: ``k`` and ``v``
+    [n_pages, page_size, n_kv_heads, head_dim] in float16, bfloat16 or
+    float8_e4m3fn (then with optional fp32 ``k_scale`` and ``v_scale`` per
+    kv head).  Any order of pages, tokens and heads in memory (permuted views
+    are fine) with contiguous rows.  Holds the tensors; checked once here."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4:
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected [pages, page, kv heads, head_dim]")
+        if k.dtype not in (torch.float16, torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"k: dtype {k.dtype}, expected float16, bfloat16 or float8_e4m3fn")
+        _need_strided(k, "k", k.shape, k.dtype, k.device)
+        _need_strided(v, "v", k.shape, k.dtype, k.device)
+        e4m3 = k.dtype is torch.float8_e4m3fn
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                if not e4m3:
+                    raise ValueError(f"{name} goes with a float8_e4m3fn cache only")
+                _need(t, name, (k.shape[2],), torch.float32, k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        if max(self.n_pages, self.page_size, self.n_kv_heads) > 0x7fffffff:
+            raise ValueError("cache sizes must be below 2^31")
+        self._c = _CACHE_T.pack(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                                0 if v_scale is None else v_scale.data_ptr(), *k.stride()[:3], *v.stride()[:3],
+                                self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
+                                MOE_E4M3 if e4m3 else _DT_CODE[k.dtype])
+
+
+def moe_attention_workspace_bytes(cache: MoeKvCache, n_q_heads: int) -> int:
+    return int(_load().moe_attention_workspace_bytes(cache._c, int(n_q_heads)))
+
+
+def alloc_attention_workspace(cache: MoeKvCache, n_q_heads: int) -> torch.Tensor:
+    """A zero-filled, 256-byte aligned workspace for moe_paged_attention (any
+    batch and lengths) and moe_rope_append on this cache."""
+    n = moe_attention_workspace_bytes(cache, n_q_heads)
+    if n == 0:
+        raise MoeError(1, "n_q_heads must be a positive multiple of the cache's kv heads")
+    ws = torch.zeros(n + 256, dtype=torch.uint8, device=cache.device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n]
+
+
+def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_out, ws, q_norm_w=None, k_norm_w=None,
+                    eps=1e-6, interleaved=False, stream=None):
+    """Rotates new ``q`` [T, Hq, D] (into ``q_out``) and ``k`` [T, Hkv, D] by
+    ``positions`` [T] int64 and ``inv_freq`` [rot_dim / 2] fp32, after a per-head
+    RMS norm when ``q_norm_w`` and ``k_norm_w`` [D] are given, and stores k and v
+    in the cache's ``slots`` [T] int64 (page * page_size + place; negative:
+    not stored)."""
+    T, hq, D = q.shape
+    dt, dev = q.dtype, q.device
+    if dt not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q: dtype {dt}, expected float16 or bfloat16")
+    kv = (T, cache.n_kv_heads, cache.head_dim)
+    _need_strided(q, "q", (T, hq, cache.head_dim), dt, dev)
+    _need_strided(k, "k", kv, dt, dev)
+    _need_strided(v, "v", kv, dt, dev)
+    _need_strided(q_out, "q_out", (T, hq, D), dt, dev)
+    _need(positions, "positions", (T,), torch.int64, dev)
+    _need(slots, "slots", (T,), torch.int64, dev)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq: expected [rot_dim / 2]")
+    _need(inv_freq, "inv_freq", inv_freq.shape, torch.float32, dev)
+    if cache.device != dev:
+        raise ValueError(f"cache: on {cache.device}, expected {dev}")
+    if ws.device != dev:
+        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    qn = kn = 0
+    if q_norm_w is not None or k_norm_w is not None:
+        if q_norm_w is None or k_norm_w is None:
+            raise ValueError("q_norm_w and k_norm_w go together")
+        _need_strided(q_norm_w, "q_norm_w", (D,), dt, dev)
+        _need_strided(k_norm_w, "k_norm_w", (D,), dt, dev)
+        qn, kn = q_norm_w.data_ptr(), k_norm_w.data_ptr()
+    args = _ROPE_T.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), positions.data_ptr(),
+                        slots.data_ptr(), inv_freq.data_ptr(), qn, kn, *q.stride()[:2], *k.stride()[:2],
+                        *v.stride()[:2], *q_out.stride()[:2], T, hq, 2 * inv_freq.shape[0], _DT_CODE[dt],
+                        1 if interleaved else 0, eps)
+    rc = _load().moe_rope_append(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
+    if rc:
+        _check(rc)
+
+
+def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, scale=None, window=0, lse=None,
+                        stream=None):
+    """Attention of one new token per sequence: ``q`` [B, Hq, D] over the
+    ``seq_lens`` [B] int32 cached tokens that ``block_table`` [B, max_pages]
+    int32 places, into ``out`` [B, Hq, D] (and ``lse`` [B, Hq] fp32).  ``scale``
+    defaults to D ** -0.5; ``window`` > 0 keeps the last ``window`` tokens."""
+    B, hq, D = shape = q.shape
+    dt, dev = q.dtype, q.device
+    if dt not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q: dtype {dt}, expected float16 or bfloat16")
+    _need_strided(q, "q", (B, hq, cache.head_dim), dt, dev)
+    _need_strided(out, "out", shape, dt, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [B, max_pages]")
+    _need_strided(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
+    _need(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if lse is not None:
+        _need(lse, "lse", (B, hq), torch.float32, dev)
+    if cache.device != dev:
+        raise ValueError(f"cache: on {cache.device}, expected {dev}")
+    if ws.device != dev:
+        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    args = _ATTN_T.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(),
+                        seq_lens.data_ptr(), *q.stride()[:2], *out.stride()[:2], block_table.stride(0),
+                        B, hq, block_table.shape[1], window, _DT_CODE[dt], D ** -0.5 if scale is None else scale)
+    rc = _load().moe_paged_attention(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
+    if rc:
+        _check(rc)
 
 
 def cfg_from_workload(wl, out_dtype=None, flags=0) -> MoeCfg:

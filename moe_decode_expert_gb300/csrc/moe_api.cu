@@ -341,10 +341,13 @@ moe_status_t moe_query_status(void* ws, void* stream) {
     return check_launch("cudaMemcpy(clear status)");
   static const char* names[] = {"ok", "timeout waiting for router logits", "timeout waiting for activations",
                                 "timeout waiting for a bulk copy", "expert id out of range",
-                                "test wait ran out"};
-  const char* what = hdr[0] < 6 ? names[hdr[0]] : "unknown";
+                                "test wait ran out", "cache slot out of range (token)",
+                                "page id out of range (sequence)", "sequence length out of range (sequence)"};
+  const char* what = hdr[0] <= kDevBadLength ? names[hdr[0]] : "unknown";
   if (hdr[0] == kDevBadExpert)
     return set_error(MOE_ERR_DEVICE, "device check: %s (pair %u)", what, hdr[1]);
+  if (hdr[0] >= kDevBadSlot && hdr[0] <= kDevBadLength)
+    return set_error(MOE_ERR_DEVICE, "device check: %s %u", what, hdr[1]);
   return set_error(MOE_ERR_TIMEOUT, "device wait: %s (CTA %u)", what, hdr[1]);
 }
 

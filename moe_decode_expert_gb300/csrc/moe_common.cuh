@@ -25,6 +25,9 @@ enum : uint32_t {
   kDevTimeoutCopy = 3,    // a bulk copy never completed
   kDevBadExpert = 4,      // an expert id outside [0, E)
   kDevTimeoutTest = 5,    // the test hook's wait ran out (expected)
+  kDevBadSlot = 6,        // a cache slot past the last page
+  kDevBadPage = 7,        // a page id outside the cache
+  kDevBadLength = 8,      // a sequence length below 0 or past the block table
 };
 
 // Control block at offset 0 of every workspace (256 bytes).

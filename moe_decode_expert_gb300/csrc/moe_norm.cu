@@ -1,0 +1,254 @@
+// moe_norm.cu — RMS norm with the residual's addition, 16-bit or e4m3 output.
+//
+//   h = x (+ r);  r_out = rn(h);  y = h * rsqrt(mean(h^2) + eps) * w;
+//   out = rn(y), or q = e4m3(y / s) with s = max(max|y|, 2^-96) / 448 per row
+//   or per group of columns.
+//
+// One pass: a row's h values stay in registers between the reduction and the
+// output, so every input is read once.  max|y| = rsqrt(..) * max|h w|, so the
+// sum of squares and the row's largest magnitude come out of one reduction.
+// Magnitudes are reduced as unsigned bit patterns: their order is that of the
+// floats, with NaN above infinity, so a NaN reaches the row's scale.
+
+#include <cuda_fp8.h>
+
+#include "moe_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 1.26217744835361888865876570445e-29f;  // 2^-96
+
+enum { kOutSame = 0, kOutRow = 1, kOutGroup = 2 };
+
+__device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
+  if (dt == MOE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Scale of a row or group from its largest |y| (kept NaN if that is NaN).
+__device__ __forceinline__ float scale_of(float amax) {
+  return __fdiv_rn(amax < kAmaxFloor ? kAmaxFloor : amax, kE4m3Max);
+}
+
+// VEC elements (8: one 16-byte load, 1: any alignment) NV times per thread.
+// WARP: a warp per row; else a CTA per row.
+template <int DT, int VEC, int NV, int OUT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nthr = WARP ? 32 : blockDim.x;
+  const int tid = WARP ? lane : threadIdx.x;
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (row >= a.T) return;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.x_stride;
+  const uint16_t* r = static_cast<const uint16_t*>(a.residual) + row * a.residual_stride;
+  const uint16_t* w = static_cast<const uint16_t*>(a.weight);
+  uint16_t* ro = static_cast<uint16_t*>(a.residual_out) + row * a.residual_out_stride;
+  const bool res = a.residual != nullptr, res_out = a.residual_out != nullptr;
+
+  float h[NV * VEC], wf[NV * VEC];
+  if constexpr (VEC == 8) {
+    uint4 xv[NV], rv[NV], wv[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * nthr + tid) * 8;
+      xv[v] = rv[v] = wv[v] = make_uint4(0, 0, 0, 0);
+      if (c < a.H) {
+        xv[v] = ld_ordered16(x + c);
+        if (res) rv[v] = ld_ordered16(r + c);
+        wv[v] = ld_ordered16(w + c);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float xf[8], rf[8], w8[8];
+      unpack8<DT>(xv[v], xf);
+      unpack8<DT>(rv[v], rf);
+      unpack8<DT>(wv[v], w8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[v * 8 + j] = res ? xf[j] + rf[j] : xf[j];
+        wf[v * 8 + j] = w8[j];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = v * nthr + tid;
+      h[v] = wf[v] = 0.0f;
+      if (c < a.H) {
+        h[v] = load_scalar<DT>(x, c);
+        if (res) h[v] += load_scalar<DT>(r, c);
+        wf[v] = load_scalar<DT>(w, c);
+      }
+    }
+  }
+
+  float sum = 0.0f;
+  uint32_t mx = 0u;
+#pragma unroll
+  for (int i = 0; i < NV * VEC; ++i) {
+    sum = fmaf(h[i], h[i], sum);
+    if (OUT == kOutRow) mx = max(mx, __float_as_uint(h[i] * wf[i]) & 0x7fffffffu);
+  }
+  sum = warp_sum(sum);
+  if (OUT == kOutRow) mx = __reduce_max_sync(0xffffffffu, mx);
+  if constexpr (!WARP) {
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_max[warp] = mx;
+    }
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    sum = warp_sum(lane < nw ? s_sum[lane] : 0.0f);
+    if (OUT == kOutRow) mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+  }
+  const float rstd = __frcp_rn(sqrtf(__fdiv_rn(sum, static_cast<float>(a.H)) + a.eps));
+
+  float inv = 1.0f;
+  if (OUT == kOutRow) {
+    const float s = scale_of(__uint_as_float(mx) * rstd);
+    inv = __frcp_rn(s);
+    if (tid == 0) a.scales[row] = s;
+  }
+
+  uint8_t* o8 = static_cast<uint8_t*>(a.out) + row * a.out_stride;
+  uint16_t* o16 = static_cast<uint16_t*>(a.out) + row * a.out_stride;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if constexpr (VEC == 8) {
+      const int c = (v * nthr + tid) * 8;
+      const bool in = c < a.H;
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = h[v * 8 + j] * rstd * wf[v * 8 + j];
+      if (in && res_out) {
+        const float* p = h + v * 8;
+        *reinterpret_cast<uint4*>(ro + c) =
+            make_uint4(pack2(DT, p[0], p[1]), pack2(DT, p[2], p[3]), pack2(DT, p[4], p[5]), pack2(DT, p[6], p[7]));
+      }
+      if (OUT == kOutSame) {
+        if (in)
+          *reinterpret_cast<uint4*>(o16 + c) =
+              make_uint4(pack2(DT, y[0], y[1]), pack2(DT, y[2], y[3]), pack2(DT, y[4], y[5]), pack2(DT, y[6], y[7]));
+      } else {
+        if (OUT == kOutGroup) {
+          // group / 8 neighbouring lanes hold a group (groups start at
+          // multiples of their size, and so do those lanes)
+          uint32_t g = 0u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g = max(g, __float_as_uint(y[j]) & 0x7fffffffu);
+          for (int o = 1; o < (a.group >> 3); o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+          const float s = scale_of(__uint_as_float(g));
+          inv = __frcp_rn(s);
+          if (in && (c % a.group) == 0)
+            a.scales[row * ((a.H + a.group - 1) / a.group) + c / a.group] = s;
+        }
+        if (in)
+          *reinterpret_cast<uint2*>(o8 + c) = make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                                         e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+      }
+    } else {
+      const int c = v * nthr + tid;
+      if (c < a.H) {
+        const float y = h[v] * rstd * wf[v];
+        if (res_out) store_out(ro, c, h[v], DT);
+        if (OUT == kOutSame)
+          store_out(o16, c, y, DT);
+        else
+          o8[c] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3));
+      }
+    }
+  }
+}
+
+template <int DT, int VEC, int NV, int OUT, bool WARP>
+moe_status_t launch(const moe_norm_t& n, int threads, cudaStream_t st) {
+  const unsigned grid = WARP ? static_cast<unsigned>((static_cast<int64_t>(n.T) + threads / 32 - 1) / (threads / 32))
+                             : static_cast<unsigned>(n.T);
+  if (launch_pdl(norm_kernel<DT, VEC, NV, OUT, WARP>, dim3(grid), dim3(threads), 0, st, n) != cudaSuccess)
+    return check_launch("norm_kernel");
+  stat_kernels(1);
+  return MOE_OK;
+}
+
+template <int DT, int OUT>
+moe_status_t dispatch(const moe_norm_t& n, bool wide, cudaStream_t st) {
+  if (!wide) {
+    if constexpr (OUT != kOutGroup) {
+      if (n.H <= 4 * 1024) {
+        const int thr = ((n.H + 3) / 4 + 31) / 32 * 32;
+        return launch<DT, 1, 4, OUT, false>(n, thr, st);
+      }
+      return launch<DT, 1, 32, OUT, false>(n, 1024, st);
+    }
+  }
+  const int vecs = (n.H + 7) / 8;
+  const int nv = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+  const int thr = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+  if (nv == 1) return launch<DT, 8, 1, OUT, false>(n, thr, st);
+  if (nv == 2) return launch<DT, 8, 2, OUT, false>(n, thr, st);
+  return launch<DT, 8, 4, OUT, false>(n, thr, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_add_rmsnorm(const moe_norm_t* n, void* stream) {
+  if (!n) return set_error(MOE_ERR_INVALID_ARG, "moe_norm_t is NULL");
+  if (n->T < 0 || n->H < 1) return set_error(MOE_ERR_INVALID_ARG, "T must be >= 0 and H >= 1");
+  if (n->H > 32768) return set_error(MOE_ERR_UNSUPPORTED, "H must be <= 32768");
+  if (n->dtype != MOE_F16 && n->dtype != MOE_BF16)
+    return set_error(MOE_ERR_UNSUPPORTED, "dtype must be MOE_F16 or MOE_BF16");
+  if (n->out_dtype != n->dtype && n->out_dtype != MOE_E4M3)
+    return set_error(MOE_ERR_UNSUPPORTED, "out_dtype must equal dtype or be MOE_E4M3");
+  const bool e4m3 = n->out_dtype == MOE_E4M3;
+  if (n->group != 0 && (!e4m3 || n->group < 16 || n->group > 256 || (n->group & (n->group - 1))))
+    return set_error(MOE_ERR_INVALID_ARG, "group must be 0, or with MOE_E4M3 a power of two from 16 to 256");
+  if (!(n->eps >= 0.0f)) return set_error(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!n->residual && n->residual_out) return set_error(MOE_ERR_INVALID_ARG, "residual_out given without residual");
+  if (n->T == 0) return MOE_OK;
+  if (!n->x || !n->weight || !n->out) return set_error(MOE_ERR_INVALID_ARG, "x / weight / out is NULL");
+  if (e4m3 != (n->scales != nullptr)) return set_error(MOE_ERR_INVALID_ARG, "scales goes with MOE_E4M3, and only with it");
+  if (n->x_stride < n->H || n->out_stride < n->H || (n->residual && n->residual_stride < n->H) ||
+      (n->residual_out && n->residual_out_stride < n->H))
+    return set_error(MOE_ERR_INVALID_ARG, "row strides must be at least H");
+  const uintptr_t p16 = reinterpret_cast<uintptr_t>(n->x) | reinterpret_cast<uintptr_t>(n->residual) |
+                        reinterpret_cast<uintptr_t>(n->weight) | reinterpret_cast<uintptr_t>(n->residual_out) |
+                        (e4m3 ? 0 : reinterpret_cast<uintptr_t>(n->out));
+  if ((p16 & 1u) || (reinterpret_cast<uintptr_t>(n->scales) & 3u))
+    return set_error(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+  const int64_t strides = n->x_stride | n->out_stride | (n->residual ? n->residual_stride : 0) |
+                          (n->residual_out ? n->residual_out_stride : 0);
+  const bool wide = n->H % 8 == 0 && (p16 & 15u) == 0 && (reinterpret_cast<uintptr_t>(n->out) & 7u) == 0 &&
+                    (strides & 7) == 0;
+  if (n->group && !wide)
+    return set_error(MOE_ERR_UNSUPPORTED, "group scales need H %% 8 == 0 and 16-byte aligned rows");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int out = !e4m3 ? kOutSame : n->group ? kOutGroup : kOutRow;
+  if (n->dtype == MOE_BF16)
+    return out == kOutSame  ? dispatch<MOE_BF16, kOutSame>(*n, wide, st)
+           : out == kOutRow ? dispatch<MOE_BF16, kOutRow>(*n, wide, st)
+                            : dispatch<MOE_BF16, kOutGroup>(*n, wide, st);
+  return out == kOutSame  ? dispatch<MOE_F16, kOutSame>(*n, wide, st)
+         : out == kOutRow ? dispatch<MOE_F16, kOutRow>(*n, wide, st)
+                          : dispatch<MOE_F16, kOutGroup>(*n, wide, st);
+}
