@@ -320,27 +320,51 @@ _ROPE_T = struct.Struct("@9P8q5if0q")
 _ATTN_T = struct.Struct("@5P5q5if0q")
 
 
-def _launch_stream(device, stream):
-    """The raw stream a call on tensors of `device` goes to."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, not {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is {torch.cuda.current_device()}")
+# A decode step makes these calls dozens of times per token and their kernels
+# take a few microseconds, so their checks are single comparisons and the
+# current stream is asked for as a number.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_FLOATS = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
+
+
+def _launch_stream(index, stream):
+    """The raw stream a call on tensors of CUDA device `index` goes to."""
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if index != _current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _need_strided(t, name, shape, dtype, device):
-    """Like _need, but any strides with a contiguous last dimension."""
+def _explain(t, name, shape, dtype, index):
+    """Raises for the first thing wrong with an argument (contiguous rows asked for)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected {f'cuda:{index}' if index >= 0 else 'cpu'}")
+    raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _rows(t, name, shape, dtype, index):
+    """Strides of a tensor of this shape, type and device with contiguous rows."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
+        _explain(t, name, shape, dtype, index)
+    return st
+
+
+def _flat(t, name, shape, dtype, index):
+    """Address of a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _explain(t, name, shape, dtype, index)
+    return t.data_ptr()
 
 
 def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=None, group=0, eps=1e-6, stream=None):
@@ -348,37 +372,37 @@ def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=Non
     x's dtype, or float8_e4m3fn with ``scales`` [T, 1] (one per row) or
     [T, ceil(H / group)].  ``residual_out`` receives the rounded sum (may be
     ``residual`` itself).  Rows may be strided; see include/moe.h."""
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, H]")
-    T, H = shape = x.shape
-    dt, dev = x.dtype, x.device
-    if dt not in (torch.float16, torch.bfloat16):
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected [T, H]")
+    T, H = shape
+    code = _FLOATS.get(dt)
+    if code is None:
         raise ValueError(f"x: dtype {dt}, expected float16 or bfloat16")
     e4m3 = out.dtype is torch.float8_e4m3fn
-    _need_strided(x, "x", shape, dt, dev)
-    _need_strided(weight, "weight", (H,), dt, dev)
-    _need_strided(out, "out", shape, out.dtype if e4m3 else dt, dev)
+    xs = _rows(x, "x", shape, dt, dev)[0]
+    os_ = _rows(out, "out", shape, out.dtype if e4m3 else dt, dev)[0]
+    _rows(weight, "weight", (H,), dt, dev)
     r = ro = s = rs = ros = 0
     if residual is not None:
-        _need_strided(residual, "residual", shape, dt, dev)
-        r, rs = residual.data_ptr(), residual.stride(0) if T > 1 else H
+        rs = _rows(residual, "residual", shape, dt, dev)[0]
+        r = residual.data_ptr()
     if residual_out is not None:
         if residual is None:
             raise ValueError("residual_out without residual")
-        _need_strided(residual_out, "residual_out", shape, dt, dev)
-        ro, ros = residual_out.data_ptr(), residual_out.stride(0) if T > 1 else H
+        ros = _rows(residual_out, "residual_out", shape, dt, dev)[0]
+        ro = residual_out.data_ptr()
+    if T == 1:  # a single row's stride says nothing
+        xs = os_ = rs = ros = H
     if (scales is not None) != e4m3:
         raise ValueError("scales goes with a float8_e4m3fn out, and only with it")
     if e4m3:
         if group < 0:
             raise ValueError("group must be >= 0")
-        _need(scales, "scales", (T, -(-H // group) if group else 1), torch.float32, dev)
-        s = scales.data_ptr()
-    code = _DT_CODE[dt]
-    args = _NORM_T.pack(x.data_ptr(), r, weight.data_ptr(), out.data_ptr(), ro, s,
-                        x.stride(0) if T > 1 else H, rs, out.stride(0) if T > 1 else H, ros,
-                        T, H, code, MOE_E4M3 if e4m3 else code, group, eps)
-    rc = _load().moe_add_rmsnorm(args, _launch_stream(dev, stream))
+        s = _flat(scales, "scales", (T, -(-H // group) if group else 1), torch.float32, dev)
+    args = _NORM_T.pack(x.data_ptr(), r, weight.data_ptr(), out.data_ptr(), ro, s, xs, rs, os_, ros, T, H, code,
+                        MOE_E4M3 if e4m3 else code, group, eps)
+    rc = (_lib or _load()).moe_add_rmsnorm(args, _launch_stream(dev, stream))
     if rc:
         _check(rc)
 
@@ -395,17 +419,18 @@ class MoeKvCache:
             raise ValueError(f"k: shape {tuple(k.shape)}, expected [pages, page, kv heads, head_dim]")
         if k.dtype not in (torch.float16, torch.bfloat16, torch.float8_e4m3fn):
             raise ValueError(f"k: dtype {k.dtype}, expected float16, bfloat16 or float8_e4m3fn")
-        _need_strided(k, "k", k.shape, k.dtype, k.device)
-        _need_strided(v, "v", k.shape, k.dtype, k.device)
+        dev = k.get_device()
+        _rows(k, "k", k.shape, k.dtype, dev)
+        _rows(v, "v", k.shape, k.dtype, dev)
         e4m3 = k.dtype is torch.float8_e4m3fn
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 if not e4m3:
                     raise ValueError(f"{name} goes with a float8_e4m3fn cache only")
-                _need(t, name, (k.shape[2],), torch.float32, k.device)
+                _flat(t, name, (k.shape[2],), torch.float32, dev)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self._dev = k.dtype, k.device, dev
         if max(self.n_pages, self.page_size, self.n_kv_heads) > 0x7fffffff:
             raise ValueError("cache sizes must be below 2^31")
         self._c = _CACHE_T.pack(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
@@ -436,36 +461,35 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
     RMS norm when ``q_norm_w`` and ``k_norm_w`` [D] are given, and stores k and v
     in the cache's ``slots`` [T] int64 (page * page_size + place; negative:
     not stored)."""
-    T, hq, D = q.shape
-    dt, dev = q.dtype, q.device
-    if dt not in (torch.float16, torch.bfloat16):
+    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    code = _FLOATS.get(dt)
+    if code is None:
         raise ValueError(f"q: dtype {dt}, expected float16 or bfloat16")
-    kv = (T, cache.n_kv_heads, cache.head_dim)
-    _need_strided(q, "q", (T, hq, cache.head_dim), dt, dev)
-    _need_strided(k, "k", kv, dt, dev)
-    _need_strided(v, "v", kv, dt, dev)
-    _need_strided(q_out, "q_out", (T, hq, D), dt, dev)
-    _need(positions, "positions", (T,), torch.int64, dev)
-    _need(slots, "slots", (T,), torch.int64, dev)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq: expected [rot_dim / 2]")
-    _need(inv_freq, "inv_freq", inv_freq.shape, torch.float32, dev)
-    if cache.device != dev:
-        raise ValueError(f"cache: on {cache.device}, expected {dev}")
-    if ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, expected {dev}")
+    D = cache.head_dim
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"q: shape {tuple(shape)}, expected [T, heads, {D}]")
+    T, hq, _ = shape
+    kv = (T, cache.n_kv_heads, D)
+    qs = _rows(q, "q", shape, dt, dev)
+    ks = _rows(k, "k", kv, dt, dev)
+    vs = _rows(v, "v", kv, dt, dev)
+    os_ = _rows(q_out, "q_out", shape, dt, dev)
+    pos = _flat(positions, "positions", (T,), torch.int64, dev)
+    slot = _flat(slots, "slots", (T,), torch.int64, dev)
+    n_freq = inv_freq.numel()
+    freq = _flat(inv_freq, "inv_freq", (n_freq,), torch.float32, dev)
+    if cache._dev != dev or ws.get_device() != dev:
+        raise ValueError(f"cache on {cache.device} and ws on {ws.device}, expected both on {q.device}")
     qn = kn = 0
     if q_norm_w is not None or k_norm_w is not None:
         if q_norm_w is None or k_norm_w is None:
             raise ValueError("q_norm_w and k_norm_w go together")
-        _need_strided(q_norm_w, "q_norm_w", (D,), dt, dev)
-        _need_strided(k_norm_w, "k_norm_w", (D,), dt, dev)
-        qn, kn = q_norm_w.data_ptr(), k_norm_w.data_ptr()
-    args = _ROPE_T.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), positions.data_ptr(),
-                        slots.data_ptr(), inv_freq.data_ptr(), qn, kn, *q.stride()[:2], *k.stride()[:2],
-                        *v.stride()[:2], *q_out.stride()[:2], T, hq, 2 * inv_freq.shape[0], _DT_CODE[dt],
+        qn = _flat(q_norm_w, "q_norm_w", (D,), dt, dev)
+        kn = _flat(k_norm_w, "k_norm_w", (D,), dt, dev)
+    args = _ROPE_T.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), pos, slot, freq, qn, kn,
+                        qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], T, hq, 2 * n_freq, code,
                         1 if interleaved else 0, eps)
-    rc = _load().moe_rope_append(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
+    rc = (_lib or _load()).moe_rope_append(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
     if rc:
         _check(rc)
 
@@ -476,26 +500,25 @@ def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, sc
     ``seq_lens`` [B] int32 cached tokens that ``block_table`` [B, max_pages]
     int32 places, into ``out`` [B, Hq, D] (and ``lse`` [B, Hq] fp32).  ``scale``
     defaults to D ** -0.5; ``window`` > 0 keeps the last ``window`` tokens."""
-    B, hq, D = shape = q.shape
-    dt, dev = q.dtype, q.device
-    if dt not in (torch.float16, torch.bfloat16):
+    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    code = _FLOATS.get(dt)
+    if code is None:
         raise ValueError(f"q: dtype {dt}, expected float16 or bfloat16")
-    _need_strided(q, "q", (B, hq, cache.head_dim), dt, dev)
-    _need_strided(out, "out", shape, dt, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table: expected [B, max_pages]")
-    _need_strided(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
-    _need(seq_lens, "seq_lens", (B,), torch.int32, dev)
-    if lse is not None:
-        _need(lse, "lse", (B, hq), torch.float32, dev)
-    if cache.device != dev:
-        raise ValueError(f"cache: on {cache.device}, expected {dev}")
-    if ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, expected {dev}")
-    args = _ATTN_T.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(),
-                        seq_lens.data_ptr(), *q.stride()[:2], *out.stride()[:2], block_table.stride(0),
-                        B, hq, block_table.shape[1], window, _DT_CODE[dt], D ** -0.5 if scale is None else scale)
-    rc = _load().moe_paged_attention(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
+    D = cache.head_dim
+    if len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"q: shape {tuple(shape)}, expected [B, heads, {D}]")
+    B, hq, _ = shape
+    qs = _rows(q, "q", shape, dt, dev)
+    os_ = _rows(out, "out", shape, dt, dev)
+    pages = block_table.shape[-1] if block_table.dim() else 0
+    bs = _rows(block_table, "block_table", (B, pages), torch.int32, dev)
+    lens = _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    lse_p = 0 if lse is None else _flat(lse, "lse", (B, hq), torch.float32, dev)
+    if cache._dev != dev or ws.get_device() != dev:
+        raise ValueError(f"cache on {cache.device} and ws on {ws.device}, expected both on {q.device}")
+    args = _ATTN_T.pack(q.data_ptr(), out.data_ptr(), lse_p, block_table.data_ptr(), lens, qs[0], qs[1], os_[0], os_[1],
+                        bs[0], B, hq, pages, window, code, D ** -0.5 if scale is None else scale)
+    rc = (_lib or _load()).moe_paged_attention(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
     if rc:
         _check(rc)
 

@@ -22,6 +22,8 @@
 // shared memory, filled by cp.async two slots ahead; only a part's end meets
 // at a CTA barrier.
 
+#include <atomic>
+
 #include "moe_common.cuh"
 #include "moe_kv.h"
 
@@ -742,7 +744,15 @@ template <int QT, bool F8, int DP, int NT>
 moe_status_t launch(const AttnArgs& g, int grid, cudaStream_t st) {
   using S = Shape<QT, F8, DP, NT>;
   const auto kernel = paged_attention_kernel<QT, F8, DP, NT>;
-  if (raise_smem_limit(kernel, S::kSmem) != cudaSuccess) return check_launch("paged_attention_kernel attributes");
+  // the limit of a kernel is raised once per device: asking costs microseconds
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return check_launch("cudaGetDevice");
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(raised.load(std::memory_order_acquire) & bit)) {
+    if (raise_smem_limit(kernel, S::kSmem) != cudaSuccess) return check_launch("paged_attention_kernel attributes");
+    raised.fetch_or(bit, std::memory_order_release);
+  }
   if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, st, g) != cudaSuccess)
     return check_launch("paged_attention_kernel");
   stat_kernels(1);
