@@ -33,10 +33,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 3;         // slots of a warp's ring
-constexpr int kMaxCtas = 320;    // partial slots in the workspace: two per CTA
+constexpr int kMaxCtas = 640;    // partial slots in the workspace: two per CTA
 constexpr int kJoin = 16;        // parts joined by one CTA at a time
 constexpr int kMaxGroups = (kMaxCtas + kJoin - 1) / kJoin;
 constexpr int kMinUnits = 4;     // units a CTA takes at least: one per warp
+constexpr int kSlotTarget = 8192;
+constexpr int kCtas64 = 2;
+constexpr int kCtas128 = 2;
+constexpr int kCtas256 = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -55,6 +59,10 @@ struct AttnArgs {
   int32_t hpc;     // query heads of a chunk (<= 8 * NT)
   int32_t group;   // query heads of a kv head
   int32_t max_len; // max_pages * page_size, saturated
+  // token / page_size = umulhi(token, page_mul) >> page_shift (page_mul 0: page_size 1)
+  uint32_t page_mul;
+  int32_t page_shift;
+  int32_t blocks;  // page_size % 16 == 0: 16 neighbouring tokens share a page
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -133,18 +141,20 @@ struct JoinSmem {
 template <int QT, bool F8, int DP, int NT>
 struct Shape {
   static constexpr int kBytes = F8 ? 1 : 2;
-  static constexpr int kU = (8192 / (DP * kBytes)) < 64 ? 8192 / (DP * kBytes) : 64;  // tokens of a unit
+  static constexpr int kFill = kSlotTarget / (DP * kBytes);
+  static constexpr int kU = kFill < 16 ? 16 : kFill < 64 ? kFill : 64;  // tokens of a unit
+  static constexpr int kCtas = DP == 256 ? kCtas256 : DP == 128 ? kCtas128 : kCtas64;  // CTAs of an SM
   static constexpr int kRow = DP * kBytes;                                            // bytes of a row
   static constexpr int kSlot = kU * kRow;
   static constexpr int kCpr = kRow / 16;   // 16-byte chunks of a row
   static constexpr int kMt = kU / 16;      // m tiles of a unit's scores
   static constexpr int kDm = DP / 16;      // m tiles of the output
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kPitch = DP + 4;    // fp32 pitch of a warp's output in the merge: conflict-free
+  static constexpr int kCols = NT == 1 ? 64 : 32;  // output columns the warps merge at a time
+  static constexpr int kPitch = kCols + 4;         // their fp32 pitch: conflict-free
   static constexpr bool kBf16 = !F8 && QT == MOE_BF16;  // type of the matrix products
-  static constexpr int kWarpBytes =
-      kRing * kSlot > kHeads * kPitch * 4 ? kRing * kSlot : kHeads * kPitch * 4;
-  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kMergeAt = kWarps * kRing * kSlot;
+  static constexpr int kSmem = kMergeAt + kWarps * kHeads * kPitch * 4;
 };
 
 // Byte offset of 16-byte chunk c of row r in a slot: chunks are permuted so
@@ -156,24 +166,25 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ ((r >> 1) & 3)) << 4));
 }
 
-struct Line {  // a CTA's share of the line and the line's shape
-  int64_t total;
-  int n;
+// The line of units: CTA c of n takes `each` of them, the first `more` CTAs one
+// more.
+struct Line {
+  int total, n, each, more;
+  __device__ __forceinline__ int start(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ int owner(int x) const {
+    const int wide = more * (each + 1);
+    return x < wide ? static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(each + 1))
+                    : more + static_cast<int>(static_cast<unsigned>(x - wide) / static_cast<unsigned>(each));
+  }
 };
 
-__device__ __forceinline__ int owner(const Line& ln, int64_t x) {
-  return static_cast<int>(((x + 1) * ln.n - 1) / ln.total);
-}
-
 template <int QT, bool F8, int DP, int NT>
-__global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g) {
+__global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) paged_attention_kernel(AttnArgs g) {
   using S = Shape<QT, F8, DP, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
   __shared__ JoinSmem s_join;
-  __shared__ int64_t s_scan[kWarps];
-  __shared__ int64_t s_prefix;
-  __shared__ int s_b, s_flag;
+  __shared__ int s_scan[kWarps], s_b, s_prefix, s_flag;
 
   const moe_attention_t& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -186,54 +197,49 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
   pdl_launch_dependents();
   pdl_wait();
 
-  // A sequence's token range and its units.
-  auto range = [&](int b, int& lo, int& len) {
-    len = a.seq_lens[b];
-    if (len < 0 || len > g.max_len) len = len < 0 ? 0 : g.max_len;
-    lo = a.window > 0 && len > a.window ? len - a.window : 0;
-  };
+  // A sequence's token range and its units (at least one, so that an empty
+  // sequence is written too).
+  auto clamp_len = [&](int len) { return len < 0 ? 0 : min(len, g.max_len); };
+  auto low = [&](int len) { return a.window > 0 && len > a.window ? len - a.window : 0; };
   auto units_of = [&](int lo, int len) { return len > lo ? (len + S::kU - 1) / S::kU - lo / S::kU : 1; };
   auto units = [&](int b) {
-    int lo, len;
-    range(b, lo, len);
-    return units_of(lo, len);
+    const int len = clamp_len(a.seq_lens[b]);
+    return units_of(low(len), len);
   };
 
-  // The line's length, then this CTA's share of it.
+  // The line's length, then this CTA's share of it, then the sequence that
+  // holds its start.  The first kThreads sequences stay in registers.
   const int segs = g.c.n_kv_heads * g.chunks;  // segments of a sequence
-  int64_t sum = 0;
-  for (int b = tid; b < a.B; b += kThreads) sum += units(b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int u0 = tid < a.B ? units(tid) : 0;
+  int sum = u0;
+  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += units(b);
+  sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) s_scan[warp] = sum;
   __syncthreads();
   Line ln;
-  ln.total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) ln.total += s_scan[w];
-  ln.total *= segs;
-  const int64_t most = (ln.total + kMinUnits - 1) / kMinUnits;
-  ln.n = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
+  ln.total = (s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3]) * segs;
+  ln.n = min((ln.total + kMinUnits - 1) / kMinUnits, static_cast<int>(gridDim.x));
   const int cta = blockIdx.x;
   if (cta >= ln.n) return;
-  int64_t p = ln.total * cta / ln.n;
-  const int64_t p_end = ln.total * (cta + 1) / ln.n;
-  // The sequence that holds p: the one whose units, before * segs, reach it.
-  int64_t before = 0;
+  ln.each = static_cast<int>(static_cast<unsigned>(ln.total) / static_cast<unsigned>(ln.n));
+  ln.more = ln.total - ln.each * ln.n;
+  int p = ln.start(cta);
+  const int p_end = ln.start(cta + 1);
+  int before = 0;
   for (int b0 = 0;; b0 += kThreads) {
     const int b = b0 + tid;
-    const int64_t u = b < a.B ? units(b) : 0;
-    int64_t inc = u;
+    const int u = b0 == 0 ? u0 : b < a.B ? units(b) : 0;
+    int inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
     __syncthreads();
     if (lane == 31) s_scan[warp] = inc;
     if (tid == 0) s_b = -1;
     __syncthreads();
-    int64_t ex = before + inc - u;
+    int ex = before + inc - u;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) ex += s_scan[w];
@@ -246,25 +252,146 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
     __syncthreads();
     if (s_b >= 0) break;
   }
-  int b = s_b;
-  int64_t prefix = s_prefix;
+  int b = s_b, prefix = s_prefix;
+  int len = clamp_len(a.seq_lens[b]), lo = low(len), nb = units_of(lo, len);
 
-  uint8_t* ring = smem + warp * S::kWarpBytes;
-  const uint32_t ring_u32 = smem_u32(ring);
+  const uint32_t ring = smem_u32(smem + warp * (kRing * S::kSlot));
+  float* merge = reinterpret_cast<float*>(smem + S::kMergeAt);
   const int D = g.c.head_dim;
-  const uint32_t row_in = static_cast<uint32_t>(D * S::kBytes);  // bytes of a row that exist
+
+  // ------------------------------------------------------------------ loads
+  // This warp's units are places p + warp, p + warp + kWarps, ... of the line.
+  // Their loads run ahead of the arithmetic, across segment ends: a cursor
+  // walks the units to load.
+  constexpr int kRr = (S::kU + 31) / 32;  // rows of a unit per lane
+  constexpr int kStep = 32 / S::kCpr;     // rows of one pass of the warp
+  const int col = lane % S::kCpr, row0 = lane / S::kCpr;
+  const bool col_in = col * 16 < D * S::kBytes;
+  int left = (p_end - p - warp + kWarps - 1) / kWarps;  // units still to load
+  if (p_end - p <= warp) left = 0;
+  int cb = b, cseg = (p - prefix * segs) / nb, cu = p - prefix * segs - cseg * nb + warp;
+  int clen = len, clo = lo, cnb = nb;
+  int next_len = cb + 1 < a.B ? a.seq_lens[cb + 1] : 0;
+  auto settle = [&]() {  // bring the cursor's unit index into its segment
+    while (cu >= cnb) {
+      cu -= cnb;
+      if (++cseg == segs) {
+        cseg = 0;
+        ++cb;
+        clen = clamp_len(next_len);
+        clo = low(clen);
+        cnb = units_of(clo, clen);
+        next_len = cb + 1 < a.B ? a.seq_lens[cb + 1] : 0;
+      }
+    }
+  };
+  auto page_of = [&](int tok) {
+    return g.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(tok), g.page_mul) >> g.page_shift) : tok;
+  };
+  // Where the rows of a unit are: lane l holds rows l (and l + 32); the unit
+  // looked up (n...) is the one after the unit being loaded.
+  int page[kRr], off[kRr], npage[kRr], noff[kRr];
+  int kvh_l = 0, nkvh = 0;  // their kv heads
+  bool have = false, nhave = false, nvalid[kRr];
+  auto look_up = [&]() {
+    nhave = left > 0;
+#pragma unroll
+    for (int r = 0; r < kRr; ++r) npage[r] = -1, noff[r] = 0, nvalid[r] = false;
+    if (!nhave) return;
+    --left;
+    settle();
+    nkvh = g.chunks == 1 ? cseg : cseg / g.chunks;
+    const int32_t* table = a.block_table + cb * a.table_stride;
+#pragma unroll
+    for (int r = 0; r < kRr; ++r) {
+      const int row = lane + 32 * r;
+      // unsigned: the last unit may reach past the largest int
+      const uint32_t tok = static_cast<uint32_t>(clo / S::kU + cu) * S::kU + row;
+      const uint32_t first = g.blocks ? tok | 15u : tok, last = g.blocks ? tok & ~15u : tok;
+      nvalid[r] = row < S::kU && tok >= static_cast<uint32_t>(clo) && tok < static_cast<uint32_t>(clen);
+      // rows beside those that count are placed too where a block shares a page
+      if (row < S::kU && first >= static_cast<uint32_t>(clo) && last < static_cast<uint32_t>(clen)) {
+        const int idx = page_of(static_cast<int>(tok));
+        noff[r] = static_cast<int>(tok) - idx * g.c.page_size;
+        npage[r] = table[idx];
+        if (static_cast<uint32_t>(npage[r]) >= static_cast<uint32_t>(g.c.n_pages)) {
+          npage[r] = -1;
+          report_error(ctrl, kDevBadPage, static_cast<uint32_t>(cb));
+        }
+      }
+    }
+    cu += kWarps;
+  };
+  // Issue one unit's rows of K or V into `slot`; rows that do not count (and
+  // columns past head_dim) become zeros without being read.
+  auto issue = [&](const void* base, int64_t ps, int64_t ts, int64_t hs, uint32_t slot, uint64_t vm) {
+    const uint8_t* at = static_cast<const uint8_t*>(base) + kvh_l * hs * S::kBytes + col * 16;
+    if (g.blocks) {
+      // 16 rows on one page: one address, then steps
+#pragma unroll
+      for (int bl = 0; bl < S::kU / 16; ++bl) {
+        const int pg = __shfl_sync(0xffffffffu, page[bl >> 1], (bl & 1) * 16);
+        const int of = __shfl_sync(0xffffffffu, off[bl >> 1], (bl & 1) * 16);
+        const uint32_t bits = col_in ? static_cast<uint32_t>(vm >> (bl * 16 + row0)) : 0u;
+        const uint8_t* src = at + (max(pg, 0) * ps + (of + row0) * ts) * S::kBytes;
+#pragma unroll
+        for (int i = 0; i < 16 / kStep; ++i)
+          cp16_or_zero(slot + swz<S::kCpr>(bl * 16 + i * kStep + row0, col), src + i * kStep * ts * S::kBytes,
+                       ((bits >> (i * kStep)) & 1u) << 4);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kU / kStep; ++i) {
+        const int r = i * kStep + row0;
+        const int pg = __shfl_sync(0xffffffffu, page[i * kStep / 32], r & 31);
+        const int of = __shfl_sync(0xffffffffu, off[i * kStep / 32], r & 31);
+        const bool in = ((vm >> r) & 1) && col_in;
+        cp16_or_zero(slot + swz<S::kCpr>(r, col), at + (in ? (pg * ps + of * ts) * S::kBytes : 0), in ? 16u : 0u);
+      }
+    }
+  };
+  uint64_t vm0 = 0, vm1 = 0;  // tokens of the unit in hand and of the next that count
+  auto issue_k = [&](uint32_t slot) {
+    vm0 = vm1;
+    vm1 = 0;
+    have = nhave;
+    if (have) {
+      kvh_l = nkvh;
+#pragma unroll
+      for (int r = 0; r < kRr; ++r) {
+        page[r] = npage[r];
+        off[r] = noff[r];
+        vm1 |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, nvalid[r] && page[r] >= 0)) << (32 * r);
+      }
+      issue(g.c.k, g.c.k_page_stride, g.c.k_token_stride, g.c.k_head_stride, slot, vm1);
+      look_up();
+    }
+    cp_commit();
+  };
+  auto issue_v = [&](uint32_t slot) {
+    if (have) issue(g.c.v, g.c.v_page_stride, g.c.v_token_stride, g.c.v_head_stride, slot, vm1);
+    cp_commit();
+  };
+  int slot = 0;  // ring slot in hand
+  auto slot_at = [&](int ahead) {
+    int s = slot + ahead;
+    if (s >= kRing) s -= kRing;
+    return ring + s * S::kSlot;
+  };
+  look_up();
+  issue_k(slot_at(0));
+  issue_v(slot_at(1));
+  issue_k(slot_at(2));  // now vm0 is the first unit's mask, vm1 the second's
+  int turn = warp;      // line places before this warp's next unit, from p on
 
   while (p < p_end) {
     // -------------------------------------------------- the part [ub, ue)
-    int lo, len;
-    range(b, lo, len);
-    const int nb = units_of(lo, len);
-    const int64_t local = p - prefix * segs;
-    const int seg = static_cast<int>(local / nb);
-    const int ub = static_cast<int>(local - static_cast<int64_t>(seg) * nb);
-    const int ue = static_cast<int>(p_end - p < nb - ub ? ub + (p_end - p) : nb);
-    const int64_t seg_start = p - ub;
-    const int kvh = seg / g.chunks, chunk = seg - kvh * g.chunks;
+    const int local = p - prefix * segs;
+    const int seg = static_cast<int>(static_cast<unsigned>(local) / static_cast<unsigned>(nb));
+    const int ub = local - seg * nb;
+    const int ue = min(nb, ub + p_end - p);
+    const int seg_start = p - ub;
+    const int kvh = g.chunks == 1 ? seg : seg / g.chunks, chunk = seg - kvh * g.chunks;
     const int heads = min(g.hpc, g.group - chunk * g.hpc);  // query heads of this segment
     const int h0 = kvh * g.group + chunk * g.hpc;
     if (tid == 0) {
@@ -331,94 +458,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    // ------------------------------------------------------------- loads
-    constexpr int kRr = (S::kU + 31) / 32;  // rows of a unit per lane
-    const int first_unit = lo / S::kU;
-    const int mine = ue - ub > warp ? (ue - ub - warp + kWarps - 1) / kWarps : 0;
-    const uint8_t* kb = static_cast<const uint8_t*>(g.c.k) + kvh * g.c.k_head_stride * S::kBytes;
-    const uint8_t* vb = static_cast<const uint8_t*>(g.c.v) + kvh * g.c.v_head_stride * S::kBytes;
-    const int32_t* table = a.block_table + b * a.table_stride;
-    // Where the rows of one unit are: lane l holds rows l (and l + 32).
-    int page[kRr], off[kRr];
-    int npage[kRr], noff[kRr];
-    auto look_up = [&](int i) {  // rows of this warp's unit i -> npage, noff
-#pragma unroll
-      for (int r = 0; r < kRr; ++r) {
-        const int row = lane + 32 * r;
-        const int64_t tok64 = static_cast<int64_t>(first_unit + ub + warp + i * kWarps) * S::kU + row;
-        npage[r] = -1;
-        noff[r] = 0;
-        if (i < mine && row < S::kU && tok64 >= lo && tok64 < len) {
-          const int tok = static_cast<int>(tok64);
-          const int idx = tok / g.c.page_size;
-          noff[r] = tok - idx * g.c.page_size;
-          npage[r] = table[idx];
-          if (static_cast<uint32_t>(npage[r]) >= static_cast<uint32_t>(g.c.n_pages)) {
-            npage[r] = -1;
-            report_error(ctrl, kDevBadPage, static_cast<uint32_t>(b));
-          }
-        }
-      }
-    };
-    // Issue one unit's rows of K or V into `slot`.
-    auto issue = [&](const uint8_t* base, int64_t ps, int64_t ts, uint32_t slot) {
-#pragma unroll
-      for (int i = 0; i < S::kSlot / 512; ++i) {
-        const int ch = i * 32 + lane;
-        const int row = ch / S::kCpr, col = ch % S::kCpr;
-        constexpr int kStep = 32 / S::kCpr;  // rows of one pass of the warp
-        const int pg = __shfl_sync(0xffffffffu, page[i * kStep / 32], row & 31);
-        const int of = __shfl_sync(0xffffffffu, off[i * kStep / 32], row & 31);
-        const bool in = pg >= 0 && static_cast<uint32_t>(col * 16) < row_in;
-        const uint8_t* src = base + (in ? (pg * ps + of * ts) * S::kBytes + col * 16 : 0);
-        cp16_or_zero(slot + swz<S::kCpr>(row, col), src, in ? 16u : 0u);
-      }
-    };
-    uint64_t vm0 = 0, vm1 = 0;  // tokens of the unit in hand and of the next that count
-    auto advance = [&](int i) {  // take up unit i: its rows and mask; look up i + 1
-      uint64_t vm = 0;
-#pragma unroll
-      for (int r = 0; r < kRr; ++r) {
-        page[r] = npage[r];
-        off[r] = noff[r];
-        vm |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, page[r] >= 0)) << (32 * r);
-      }
-      vm0 = vm1;
-      vm1 = vm;
-      look_up(i + 1);
-    };
-    auto issue_k = [&](int i, uint32_t slot) {
-      if (i < mine) {
-        advance(i);
-        issue(kb, g.c.k_page_stride, g.c.k_token_stride, slot);
-      } else {
-        vm0 = vm1;
-        vm1 = 0;
-      }
-      cp_commit();
-    };
-    auto issue_v = [&](int i, uint32_t slot) {
-      if (i < mine) issue(vb, g.c.v_page_stride, g.c.v_token_stride, slot);
-      cp_commit();
-    };
-
-    int slot = 0;  // ring slot in hand
-    auto slot_at = [&](int ahead) {
-      int s = slot + ahead;
-      if (s >= kRing) s -= kRing;
-      return ring_u32 + s * S::kSlot;
-    };
-    look_up(0);
-    issue_k(0, slot_at(0));
-    issue_v(0, slot_at(1));
-    issue_k(1, slot_at(2));  // now vm0 is unit 0's mask, vm1 unit 1's
-
     // ----------------------------------------------------------- compute
     const int kr = (lane & 7) + 8 * ((lane >> 3) & 1);  // K row of this lane's matrix
     const int kc = lane >> 4;                           // and its chunk
     const int vr = F8 ? (lane & 7) + 8 * ((lane >> 3) & 1) : (lane & 7) + 8 * (lane >> 4);
     const int vc = F8 ? lane >> 4 : (lane >> 3) & 1;
-    for (int i = 0; i < mine; ++i) {
+    for (; turn < ue - ub; turn += kWarps) {
       const uint64_t vm = vm0;
       cp_wait<kRing - 1>();
       __syncwarp();
@@ -463,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
             for (int j = 0; j < 4; ++j) s[mt][nt][j] += acc2[nt][j];
       }
       __syncwarp();
-      issue_v(i + 1, slot_at(0));
+      issue_v(slot_at(0));
       if (++slot == kRing) slot = 0;
 
       // softmax step: new reference, weights, sums
@@ -567,16 +612,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
         }
       }
       __syncwarp();
-      issue_k(i + 2, slot_at(0));
+      issue_k(slot_at(0));
       if (++slot == kRing) slot = 0;
     }
-    cp_wait<0>();
-    __syncwarp();
+    turn -= ue - ub;
 
     // ------------------------------------------------ the four warps meet
-    float* mine_o = reinterpret_cast<float*>(ring);  // [head][kPitch]
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float t = l[nt][j];
@@ -588,16 +631,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
           s_l[warp][nt * 8 + 2 * tq + j] = t;
         }
       }
-#pragma unroll
-      for (int dm = 0; dm < S::kDm; ++dm)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int d = dm * 16 + (F8 ? 2 * gr + (j >> 1) : gr + 8 * (j >> 1));
-          mine_o[(nt * 8 + 2 * tq + (j & 1)) * S::kPitch + d] = o[nt][dm][j];
-        }
-    }
-    __syncthreads();
-
     const bool split = ub > 0 || ue < nb;
     const float vscale = F8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.0f;
     constexpr int kQuads = DP / 4;
@@ -615,36 +648,51 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
         a.lse[static_cast<int64_t>(b) * a.n_q_heads + h0 + h] =
             lsum == 0.0f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
     };
-    const int part = cta - (split ? owner(ln, seg_start) : cta);
+    const int part = cta - (split ? ln.owner(seg_start) : cta);
     const int role = part == 0 ? 1 : 0;
     const int my_slot = cta * 2 + role;
-    for (int e = tid; e < heads * kQuads; e += kThreads) {
-      const int h = e / kQuads, d = (e % kQuads) * 4;
-      float mm = s_m[0][h];
+    constexpr int kPasses = DP / S::kCols, kPq = S::kCols / 4;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
-      const float ref = mm == -INFINITY ? 0.0f : mm;
-      float4 v = make_float4(0, 0, 0, 0);
-      float lsum = 0.0f;
+    for (int pass = 0; pass < kPasses; ++pass) {
+      if (pass) __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_m[w][h] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem + w * S::kWarpBytes) + h * S::kPitch + d);
-        v.x = fmaf(f, x.x, v.x);
-        v.y = fmaf(f, x.y, v.y);
-        v.z = fmaf(f, x.z, v.z);
-        v.w = fmaf(f, x.w, v.w);
-        lsum = fmaf(f, s_l[w][h], lsum);
-      }
-      if (!split) {
-        finish(h, d, v, lsum);
-        if (d == 0) finish_lse(h, mm, lsum);
-      } else {
-        *reinterpret_cast<float4*>(parts + (static_cast<int64_t>(my_slot) * S::kHeads + h) * DP + d) = v;
-        if (d == 0) {
-          stats[(my_slot * 16 + h) * 2] = mm;
-          stats[(my_slot * 16 + h) * 2 + 1] = lsum;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int dm = 0; dm < S::kCols / 16; ++dm)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int d = dm * 16 + (F8 ? 2 * gr + (j >> 1) : gr + 8 * (j >> 1));
+            merge[(warp * S::kHeads + nt * 8 + 2 * tq + (j & 1)) * S::kPitch + d] =
+                o[nt][pass * (S::kCols / 16) + dm][j];
+          }
+      __syncthreads();
+      for (int e = tid; e < heads * kPq; e += kThreads) {
+        const int h = e / kPq, dc = (e % kPq) * 4, d = pass * S::kCols + dc;
+        float mm = s_m[0][h];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
+        float4 v = make_float4(0, 0, 0, 0);
+        float lsum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(s_m[w][h] - ref);
+          const float4 x = *reinterpret_cast<const float4*>(merge + (w * S::kHeads + h) * S::kPitch + dc);
+          v.x = fmaf(f, x.x, v.x);
+          v.y = fmaf(f, x.y, v.y);
+          v.z = fmaf(f, x.z, v.z);
+          v.w = fmaf(f, x.w, v.w);
+          lsum = fmaf(f, s_l[w][h], lsum);
+        }
+        if (!split) {
+          finish(h, d, v, lsum);
+          if (d == 0) finish_lse(h, mm, lsum);
+        } else {
+          *reinterpret_cast<float4*>(parts + (static_cast<int64_t>(my_slot) * S::kHeads + h) * DP + d) = v;
+          if (d == 0) {
+            stats[(my_slot * 16 + h) * 2] = mm;
+            stats[(my_slot * 16 + h) * 2 + 1] = lsum;
+          }
         }
       }
     }
@@ -652,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
     // ------------------------------------------- parts of other CTAs join
     if (split) {
       const int first_cta = cta - part;
-      const int n_parts = owner(ln, seg_start + nb - 1) - first_cta + 1;
+      const int n_parts = ln.owner(seg_start + nb - 1) - first_cta + 1;
       const int n_groups = (n_parts + kJoin - 1) / kJoin;
       // Join parts from, from + step, ... (count of them) into the first one's
       // slot, or finish the segment.
@@ -729,19 +777,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attention_kernel(AttnArgs g
         }
       }
     }
-    __syncthreads();  // the rings and the statistics are free again
+    __syncthreads();  // the merge buffer and the statistics are free again
 
     // ---------------------------------------------------- the next segment
     p += ue - ub;
     if (p < p_end && seg == segs - 1 && ue == nb) {
       prefix += nb;
       ++b;
+      len = clamp_len(a.seq_lens[b]);
+      lo = low(len);
+      nb = units_of(lo, len);
     }
   }
+  cp_wait<0>();
 }
 
 template <int QT, bool F8, int DP, int NT>
-moe_status_t launch(const AttnArgs& g, int grid, cudaStream_t st) {
+moe_status_t launch(const AttnArgs& g, cudaStream_t st) {
   using S = Shape<QT, F8, DP, NT>;
   const auto kernel = paged_attention_kernel<QT, F8, DP, NT>;
   // the limit of a kernel is raised once per device: asking costs microseconds
@@ -753,6 +805,7 @@ moe_status_t launch(const AttnArgs& g, int grid, cudaStream_t st) {
     if (raise_smem_limit(kernel, S::kSmem) != cudaSuccess) return check_launch("paged_attention_kernel attributes");
     raised.fetch_or(bit, std::memory_order_release);
   }
+  const int fit = S::kCtas * sm_count(), grid = fit < kMaxCtas ? fit : kMaxCtas;
   if (launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::kSmem, st, g) != cudaSuccess)
     return check_launch("paged_attention_kernel");
   stat_kernels(1);
@@ -760,16 +813,16 @@ moe_status_t launch(const AttnArgs& g, int grid, cudaStream_t st) {
 }
 
 template <int QT, bool F8>
-moe_status_t dispatch(const AttnArgs& g, int nt, int grid, cudaStream_t st) {
+moe_status_t dispatch(const AttnArgs& g, int nt, cudaStream_t st) {
   const int D = g.c.head_dim;
   if (nt == 1) {
-    if (D <= 64) return launch<QT, F8, 64, 1>(g, grid, st);
-    if (D <= 128) return launch<QT, F8, 128, 1>(g, grid, st);
-    return launch<QT, F8, 256, 1>(g, grid, st);
+    if (D <= 64) return launch<QT, F8, 64, 1>(g, st);
+    if (D <= 128) return launch<QT, F8, 128, 1>(g, st);
+    return launch<QT, F8, 256, 1>(g, st);
   }
-  if (D <= 64) return launch<QT, F8, 64, 2>(g, grid, st);
-  if (D <= 128) return launch<QT, F8, 128, 2>(g, grid, st);
-  return launch<QT, F8, 256, 2>(g, grid, st);
+  if (D <= 64) return launch<QT, F8, 64, 2>(g, st);
+  if (D <= 128) return launch<QT, F8, 128, 2>(g, st);
+  return launch<QT, F8, 256, 2>(g, st);
 }
 
 // n tiles of 8 heads of a segment: two when a group has more than 8 heads.
@@ -822,12 +875,18 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.hpc = (g.group + g.chunks - 1) / g.chunks;
   // Tokens are 32-bit numbers; units round a length up by less than 64.
   const int64_t cap = static_cast<int64_t>(a->max_pages) * cache->page_size;
+  // The line of units is counted in 32 bits.
+  if (cap / 16 + 2 > 0x7fffffffll / g.chunks / cache->n_kv_heads / a->B)
+    return set_error(MOE_ERR_UNSUPPORTED, "batch * kv heads * table tokens too large");
+  // ceil(2^(31 + s) / page_size), s = ceil(log2 page_size): exact for 31-bit tokens
+  int sh = 0;
+  while ((1ll << sh) < cache->page_size) ++sh;
+  g.page_mul = sh ? static_cast<uint32_t>(((1ull << (31 + sh)) + cache->page_size - 1) / cache->page_size) : 0u;
+  g.page_shift = sh - 1;
+  g.blocks = cache->page_size % 16 == 0;
   g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
-  // Every CTA is resident at once (two per SM) or waits for nobody.
-  int grid = 2 * sm_count();
-  if (grid > kMaxCtas) grid = kMaxCtas;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f8 = cache->dtype == MOE_E4M3;
-  if (a->dtype == MOE_BF16) return f8 ? dispatch<MOE_BF16, true>(g, nt, grid, st) : dispatch<MOE_BF16, false>(g, nt, grid, st);
-  return f8 ? dispatch<MOE_F16, true>(g, nt, grid, st) : dispatch<MOE_F16, false>(g, nt, grid, st);
+  if (a->dtype == MOE_BF16) return f8 ? dispatch<MOE_BF16, true>(g, nt, st) : dispatch<MOE_BF16, false>(g, nt, st);
+  return f8 ? dispatch<MOE_F16, true>(g, nt, st) : dispatch<MOE_F16, false>(g, nt, st);
 }
