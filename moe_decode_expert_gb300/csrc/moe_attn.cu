@@ -12,7 +12,8 @@
 // lanes that hold its column.  movmatrix turns S^T fragments into P^T ones.
 //
 // Work is split evenly over the CTAs whatever the lengths: the (sequence,
-// kv head, unit of U tokens) triples form one line, and CTA c of n takes the
+// kv head, unit of U tokens) triples form one line, with kVoid empty places
+// before each (sequence, kv head) for its fixed cost, and CTA c of n takes the
 // c-th n-th of it (every CTA finds its place from seq_lens itself).  A (sequence,
 // kv head) that ends up in several CTAs is joined by the last of them to arrive,
 // in groups of kJoin parts and then over the groups, always in the same order:
@@ -36,7 +37,8 @@ constexpr int kRing = 3;         // slots of a warp's ring
 constexpr int kMaxCtas = 640;    // partial slots in the workspace: two per CTA
 constexpr int kJoin = 16;        // parts joined by one CTA at a time
 constexpr int kMaxGroups = (kMaxCtas + kJoin - 1) / kJoin;
-constexpr int kMinUnits = 4;     // units a CTA takes at least: one per warp
+constexpr int kMinUnits = 4;     // places of the line a CTA takes at least: one per warp
+constexpr int kVoid = 4;         // places before a segment's units: its fixed cost, in units
 constexpr int kSlotTarget = 8192;
 constexpr int kCtas64 = 2;
 constexpr int kCtas128 = 2;
@@ -197,22 +199,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
   pdl_launch_dependents();
   pdl_wait();
 
-  // A sequence's token range and its units (at least one, so that an empty
-  // sequence is written too).
+  // A sequence's token range and its places on the line: the void ones, then
+  // its units (at least one, so that an empty sequence is written too).
   auto clamp_len = [&](int len) { return len < 0 ? 0 : min(len, g.max_len); };
   auto low = [&](int len) { return a.window > 0 && len > a.window ? len - a.window : 0; };
-  auto units_of = [&](int lo, int len) { return len > lo ? (len + S::kU - 1) / S::kU - lo / S::kU : 1; };
-  auto units = [&](int b) {
+  auto places_of = [&](int lo, int len) { return kVoid + (len > lo ? (len + S::kU - 1) / S::kU - lo / S::kU : 1); };
+  auto places = [&](int b) {
     const int len = clamp_len(a.seq_lens[b]);
-    return units_of(low(len), len);
+    return places_of(low(len), len);
   };
 
   // The line's length, then this CTA's share of it, then the sequence that
   // holds its start.  The first kThreads sequences stay in registers.
   const int segs = g.c.n_kv_heads * g.chunks;  // segments of a sequence
-  const int u0 = tid < a.B ? units(tid) : 0;
+  const int u0 = tid < a.B ? places(tid) : 0;
   int sum = u0;
-  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += units(b);
+  for (int b = tid + kThreads; b < a.B; b += kThreads) sum += places(b);
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) s_scan[warp] = sum;
   __syncthreads();
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
   int before = 0;
   for (int b0 = 0;; b0 += kThreads) {
     const int b = b0 + tid;
-    const int u = b0 == 0 ? u0 : b < a.B ? units(b) : 0;
+    const int u = b0 == 0 ? u0 : b < a.B ? places(b) : 0;
     int inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -253,26 +255,26 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
     if (s_b >= 0) break;
   }
   int b = s_b, prefix = s_prefix;
-  int len = clamp_len(a.seq_lens[b]), lo = low(len), nb = units_of(lo, len);
+  int len = clamp_len(a.seq_lens[b]), lo = low(len), nb = places_of(lo, len);
 
   const uint32_t ring = smem_u32(smem + warp * (kRing * S::kSlot));
   float* merge = reinterpret_cast<float*>(smem + S::kMergeAt);
   const int D = g.c.head_dim;
 
   // ------------------------------------------------------------------ loads
-  // This warp's units are places p + warp, p + warp + kWarps, ... of the line.
+  // This warp's units are at places p + warp, p + warp + kWarps, ... of the line.
   // Their loads run ahead of the arithmetic, across segment ends: a cursor
   // walks the units to load.
   constexpr int kRr = (S::kU + 31) / 32;  // rows of a unit per lane
   constexpr int kStep = 32 / S::kCpr;     // rows of one pass of the warp
   const int col = lane % S::kCpr, row0 = lane / S::kCpr;
   const bool col_in = col * 16 < D * S::kBytes;
-  int left = (p_end - p - warp + kWarps - 1) / kWarps;  // units still to load
+  int left = (p_end - p - warp + kWarps - 1) / kWarps;  // places still to look at
   if (p_end - p <= warp) left = 0;
   int cb = b, cseg = (p - prefix * segs) / nb, cu = p - prefix * segs - cseg * nb + warp;
   int clen = len, clo = lo, cnb = nb;
   int next_len = cb + 1 < a.B ? a.seq_lens[cb + 1] : 0;
-  auto settle = [&]() {  // bring the cursor's unit index into its segment
+  auto settle = [&]() {  // bring the cursor's place into its segment
     while (cu >= cnb) {
       cu -= cnb;
       if (++cseg == segs) {
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
         ++cb;
         clen = clamp_len(next_len);
         clo = low(clen);
-        cnb = units_of(clo, clen);
+        cnb = places_of(clo, clen);
         next_len = cb + 1 < a.B ? a.seq_lens[cb + 1] : 0;
       }
     }
@@ -294,19 +296,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
   int kvh_l = 0, nkvh = 0;  // their kv heads
   bool have = false, nhave = false, nvalid[kRr];
   auto look_up = [&]() {
-    nhave = left > 0;
+    nhave = false;
+    while (left > 0 && !nhave) {
+      --left;
+      settle();
+      nhave = cu >= kVoid;
+      if (!nhave) cu += kWarps;
+    }
 #pragma unroll
     for (int r = 0; r < kRr; ++r) npage[r] = -1, noff[r] = 0, nvalid[r] = false;
     if (!nhave) return;
-    --left;
-    settle();
     nkvh = g.chunks == 1 ? cseg : cseg / g.chunks;
     const int32_t* table = a.block_table + cb * a.table_stride;
 #pragma unroll
     for (int r = 0; r < kRr; ++r) {
       const int row = lane + 32 * r;
       // unsigned: the last unit may reach past the largest int
-      const uint32_t tok = static_cast<uint32_t>(clo / S::kU + cu) * S::kU + row;
+      const uint32_t tok = static_cast<uint32_t>(clo / S::kU + cu - kVoid) * S::kU + row;
       const uint32_t first = g.blocks ? tok | 15u : tok, last = g.blocks ? tok & ~15u : tok;
       nvalid[r] = row < S::kU && tok >= static_cast<uint32_t>(clo) && tok < static_cast<uint32_t>(clen);
       // rows beside those that count are placed too where a block shares a page
@@ -322,10 +328,33 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
     }
     cu += kWarps;
   };
-  // Issue one unit's rows of K or V into `slot`; rows that do not count (and
-  // columns past head_dim) become zeros without being read.
-  auto issue = [&](const void* base, int64_t ps, int64_t ts, int64_t hs, uint32_t slot, uint64_t vm) {
-    const uint8_t* at = static_cast<const uint8_t*>(base) + kvh_l * hs * S::kBytes + col * 16;
+  uint64_t vm0 = 0, vm1 = 0;  // tokens of the unit in hand and of the next that count
+  bool keys = true;           // what is loaded next: keys, then the same unit's values
+  // Issue the next item, one unit's rows of K or of V, into `slot`; rows that do
+  // not count (and columns past head_dim) become zeros without being read.
+  auto issue = [&](uint32_t slot) {
+    if (keys) {
+      vm0 = vm1;
+      vm1 = 0;
+      have = nhave;
+      kvh_l = nkvh;
+#pragma unroll
+      for (int r = 0; r < kRr; ++r) {
+        page[r] = npage[r];
+        off[r] = noff[r];
+        vm1 |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, nvalid[r] && page[r] >= 0)) << (32 * r);
+      }
+    }
+    if (!have) {
+      keys = !keys;
+      cp_commit();
+      return;
+    }
+    const uint64_t vm = vm1;
+    const int64_t ps = keys ? g.c.k_page_stride : g.c.v_page_stride;
+    const int64_t ts = keys ? g.c.k_token_stride : g.c.v_token_stride;
+    const int64_t hs = keys ? g.c.k_head_stride : g.c.v_head_stride;
+    const uint8_t* at = static_cast<const uint8_t*>(keys ? g.c.k : g.c.v) + kvh_l * hs * S::kBytes + col * 16;
     if (g.blocks) {
       // 16 rows on one page: one address, then steps
 #pragma unroll
@@ -349,28 +378,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
         cp16_or_zero(slot + swz<S::kCpr>(r, col), at + (in ? (pg * ps + of * ts) * S::kBytes : 0), in ? 16u : 0u);
       }
     }
-  };
-  uint64_t vm0 = 0, vm1 = 0;  // tokens of the unit in hand and of the next that count
-  auto issue_k = [&](uint32_t slot) {
-    vm0 = vm1;
-    vm1 = 0;
-    have = nhave;
-    if (have) {
-      kvh_l = nkvh;
-#pragma unroll
-      for (int r = 0; r < kRr; ++r) {
-        page[r] = npage[r];
-        off[r] = noff[r];
-        vm1 |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, nvalid[r] && page[r] >= 0)) << (32 * r);
-      }
-      issue(g.c.k, g.c.k_page_stride, g.c.k_token_stride, g.c.k_head_stride, slot, vm1);
-      look_up();
-    }
     cp_commit();
-  };
-  auto issue_v = [&](uint32_t slot) {
-    if (have) issue(g.c.v, g.c.v_page_stride, g.c.v_token_stride, g.c.v_head_stride, slot, vm1);
-    cp_commit();
+    if (keys) look_up();
+    keys = !keys;
   };
   int slot = 0;  // ring slot in hand
   auto slot_at = [&](int ahead) {
@@ -379,18 +389,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
     return ring + s * S::kSlot;
   };
   look_up();
-  issue_k(slot_at(0));
-  issue_v(slot_at(1));
-  issue_k(slot_at(2));  // now vm0 is the first unit's mask, vm1 the second's
+#pragma unroll 1
+  for (int k = 0; k < kRing; ++k) issue(slot_at(k));  // K, V, K: vm0 is the first unit's mask, vm1 the second's
   int turn = warp;      // line places before this warp's next unit, from p on
 
   while (p < p_end) {
-    // -------------------------------------------------- the part [ub, ue)
+    // ------------------------------------------ the part at places [ub, ue)
     const int local = p - prefix * segs;
     const int seg = static_cast<int>(static_cast<unsigned>(local) / static_cast<unsigned>(nb));
     const int ub = local - seg * nb;
     const int ue = min(nb, ub + p_end - p);
     const int seg_start = p - ub;
+    if (ue <= kVoid) break;  // the share ends before the segment's first unit: it is the next CTA's
     const int kvh = g.chunks == 1 ? seg : seg / g.chunks, chunk = seg - kvh * g.chunks;
     const int heads = min(g.hpc, g.group - chunk * g.hpc);  // query heads of this segment
     const int h0 = kvh * g.group + chunk * g.hpc;
@@ -464,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
     const int vr = F8 ? (lane & 7) + 8 * ((lane >> 3) & 1) : (lane & 7) + 8 * (lane >> 4);
     const int vc = F8 ? lane >> 4 : (lane >> 3) & 1;
     for (; turn < ue - ub; turn += kWarps) {
+      if (ub + turn < kVoid) continue;
       const uint64_t vm = vm0;
       cp_wait<kRing - 1>();
       __syncwarp();
@@ -508,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
             for (int j = 0; j < 4; ++j) s[mt][nt][j] += acc2[nt][j];
       }
       __syncwarp();
-      issue_v(slot_at(0));
+      issue(slot_at(0));
       if (++slot == kRing) slot = 0;
 
       // softmax step: new reference, weights, sums
@@ -612,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
         }
       }
       __syncwarp();
-      issue_k(slot_at(0));
+      issue(slot_at(0));
       if (++slot == kRing) slot = 0;
     }
     turn -= ue - ub;
@@ -631,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
           s_l[warp][nt * 8 + 2 * tq + j] = t;
         }
       }
-    const bool split = ub > 0 || ue < nb;
+    const bool split = ub > kVoid || ue < nb;
     const float vscale = F8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.0f;
     constexpr int kQuads = DP / 4;
     // Write one head's four columns: the finished output.
@@ -648,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
         a.lse[static_cast<int64_t>(b) * a.n_q_heads + h0 + h] =
             lsum == 0.0f ? -INFINITY : (ref + log2f(lsum)) * kLn2;
     };
-    const int part = cta - (split ? ln.owner(seg_start) : cta);
+    const int part = cta - (split ? ln.owner(seg_start + kVoid) : cta);
     const int role = part == 0 ? 1 : 0;
     const int my_slot = cta * 2 + role;
     constexpr int kPasses = DP / S::kCols, kPq = S::kCols / 4;
@@ -786,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<QT, F8, DP, NT>::kCtas)) page
       ++b;
       len = clamp_len(a.seq_lens[b]);
       lo = low(len);
-      nb = units_of(lo, len);
+      nb = places_of(lo, len);
     }
   }
   cp_wait<0>();
@@ -876,7 +887,7 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   // Tokens are 32-bit numbers; units round a length up by less than 64.
   const int64_t cap = static_cast<int64_t>(a->max_pages) * cache->page_size;
   // The line of units is counted in 32 bits.
-  if (cap / 16 + 2 > 0x7fffffffll / g.chunks / cache->n_kv_heads / a->B)
+  if (cap / 16 + 2 + kVoid > 0x7fffffffll / g.chunks / cache->n_kv_heads / a->B)
     return set_error(MOE_ERR_UNSUPPORTED, "batch * kv heads * table tokens too large");
   // ceil(2^(31 + s) / page_size), s = ceil(log2 page_size): exact for 31-bit tokens
   int sh = 0;
