@@ -12,7 +12,7 @@ namespace {
 // n tiles of 8 heads of a segment: two when a group has more than 8 heads.
 int n_tiles(int group) { return group > 8 ? 2 : 1; }
 int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-constexpr int kTeamSegments = 8;
+constexpr int kTeamSegments = 4;
 
 }  // namespace
 }  // namespace moe

@@ -159,11 +159,11 @@ struct Shape {
   // places before a segment's units: its fixed cost, in units
   static constexpr int kVoid = TEAM ? 0 : 4;
   // places of the line a worker takes at least
-  static constexpr int kMinUnits = TEAM ? kTeamMin : 4;
+  static constexpr int kMinUnits = TEAM ? kTeamMin : 12;
   static constexpr int kBytes = F8 ? 1 : 2;
   static constexpr int kFill = (TEAM || DP > 64 ? 8192 : 4096) / (DP * kBytes);
   static constexpr int kU = kFill < 16 ? 16 : kFill < 64 ? kFill : 64;  // tokens of a unit
-  static constexpr int kCtas = TEAM ? 2 : DP == 256 ? kCtas256 : DP == 128 ? kCtas128 : kCtas64;  // CTAs of an SM
+  static constexpr int kCtas = TEAM ? 2 : DP == 256 ? kCtas256 : DP == 128 ? kCtas128 : NT == 1 ? kCtas64 : 3;  // CTAs of an SM
   static constexpr int kRow = DP * kBytes;                                            // bytes of a row
   static constexpr int kSlot = kU * kRow;
   static constexpr int kCpr = kRow / 16;   // 16-byte chunks of a row
@@ -179,7 +179,11 @@ struct Shape {
   static constexpr int kMergeAt = kWarps * kRingBytes;
   static constexpr int kMerge = TEAM ? 0 : kWarps * kHeads * kPitch * 4;
   static constexpr int kCombine = static_cast<int>(sizeof(Combine)) + kThreads * 16;
-  static constexpr int kSmem = kMergeAt + (kMerge > kCombine ? kMerge : kCombine);
+  // what a team CTA receives: its columns and all statistics from every rank
+  static constexpr int kShare = kHeads * DP / 4 / kTeamCtas;  // column quads
+  static constexpr int kReceive = TEAM ? kTeam * (kShare * 16 + 16 * 8) : 0;
+  static constexpr int kMost = kMerge > kCombine ? kMerge : kCombine;
+  static constexpr int kSmem = kMergeAt + (kMost > kReceive ? kMost : kReceive);
   static constexpr int kPart = DP + 4;  // fp32 pitch of a team warp's output in its ring: conflict-free
   static_assert(kHeads * kPart * 4 <= kRingBytes, "a warp's output fits its ring");
 };
@@ -211,26 +215,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ float ld_rank(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void st_rank2(uint32_t a, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
-__device__ __forceinline__ float4 ld_rank4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
+__device__ __forceinline__ void st_rank4(uint32_t a, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
-  return v;
 }
 
 template <int QT, bool F8, int DP, int NT, bool TEAM>
@@ -344,6 +341,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     len = clamp_len(a.seq_lens[b]);
   }
   int lo = low(len), nb = places_of(lo, len);
+  if constexpr (TEAM) cluster_arrive();  // waited for before the first write to another rank
 
   const uint32_t ring = smem_u32(smem + warp * (kRing * S::kSlot));
   float* merge = reinterpret_cast<float*>(smem + S::kMergeAt);
@@ -491,6 +489,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     start_loads(p_end - p, seg, p - prefix * segs - seg * nb);
   }
   int turn = tw;  // line places before this warp's next unit, from p on
+  [[maybe_unused]] bool again = false;  // a team that has combined a segment before
 
   while (p < p_end) {
     // ------------------------------------------ the part at places [ub, ue)
@@ -782,6 +781,27 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
         if (TEAM || e % kQuads == 0) stat(sl)[e / kQuads] = make_float2(ref, lsum);
       }
     };
+    // One column quad of a head over the CTA's four warps, and the head's
+    // reference and sum.
+    auto four_warps = [&](int h, auto quad_at, float2& ml) {
+      ml.x = s_m[0][h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) ml.x = fmaxf(ml.x, s_m[w][h]);
+      const float ref = ml.x == -INFINITY ? 0.0f : ml.x;
+      float4 v = make_float4(0, 0, 0, 0);
+      ml.y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w][h] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(quad_at(w));
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+        ml.y = fmaf(f, s_l[w][h], ml.y);
+      }
+      return v;
+    };
     // Combine `count` partial results in order: stat_of(k, h) gives part k's
     // (reference, sum) of a head, quad_of(k, e) its column quad e.  Few columns
     // are shared out over the threads by parts as well.
@@ -817,31 +837,44 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       const int cols = max(e_hi - e_lo, 1);
       const int ng = max(1, min(kThreads / cols, count));  // threads per column quad
       const int gi = ng > 1 ? tid / cols : 0, e0 = ng > 1 ? tid - gi * cols : tid;
-      constexpr int kAhead = S::kCtas > 2 ? 8 : 16;  // loads in flight per thread, as registers allow
-      for (int e = e_lo + e0; e < e_hi; e += kThreads) {
-        const int h = e / kQuads;
-        float4 v = make_float4(0, 0, 0, 0);
+      // kQ quads by kK parts in flight per thread, as registers allow
+      constexpr int kFew = S::kHeads * kQuads / (TEAM ? S::kTeam : 1) / kThreads;
+      constexpr int kFit = S::kCtas > 2 ? 8 : 32;
+      constexpr int kQ = kFew < 1 ? 1 : kFew > 4 ? 4 : kFew, kK = kFit / kQ < 16 ? kFit / kQ : 16;
+      for (int eb = e_lo + e0; eb < e_hi; eb += kQ * kThreads) {
+        float4 v[kQ];
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) v[i] = make_float4(0, 0, 0, 0);
         if (gi < ng)
-          for (int k0 = gi; k0 < count; k0 += kAhead * ng) {
-            float4 x[kAhead];
+          for (int k0 = gi; k0 < count; k0 += kK * ng) {
+            float4 x[kK][kQ];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-              x[k] = make_float4(0, 0, 0, 0);
-              if (k0 + k * ng < count) x[k] = quad_of(k0 + k * ng, e);
-            }
+            for (int k = 0; k < kK; ++k)
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-              const float f = k0 + k * ng < count ? cb_s.w[k0 + k * ng][h] : 0.0f;
-              v.x = fmaf(f, x[k].x, v.x);
-              v.y = fmaf(f, x[k].y, v.y);
-              v.z = fmaf(f, x[k].z, v.z);
-              v.w = fmaf(f, x[k].w, v.w);
-            }
+              for (int i = 0; i < kQ; ++i) {
+                x[k][i] = make_float4(0, 0, 0, 0);
+                if (k0 + k * ng < count && eb + i * kThreads < e_hi) x[k][i] = quad_of(k0 + k * ng, eb + i * kThreads);
+              }
+#pragma unroll
+            for (int k = 0; k < kK; ++k)
+#pragma unroll
+              for (int i = 0; i < kQ; ++i) {
+                const float f = k0 + k * ng < count ? cb_s.w[k0 + k * ng][((eb + i * kThreads) / kQuads) & 15] : 0.0f;
+                v[i].x = fmaf(f, x[k][i].x, v[i].x);
+                v[i].y = fmaf(f, x[k][i].y, v[i].y);
+                v[i].z = fmaf(f, x[k][i].z, v[i].z);
+                v[i].w = fmaf(f, x[k][i].w, v[i].w);
+              }
           }
-        if (ng == 1)
-          emit(final, sl, e, v, cb_s.m[h], cb_s.l[h]);
-        else
-          cb_x[tid] = v;
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const int e = eb + i * kThreads, h = e / kQuads;
+          if (ng > 1) {
+            if (i == 0) cb_x[tid] = v[0];
+          } else if (e < e_hi) {
+            emit(final, sl, e, v[i], cb_s.m[h], cb_s.l[h]);
+          }
+        }
       }
       if (ng > 1) {
         __syncthreads();
@@ -861,8 +894,8 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     };
 
     if constexpr (TEAM) {
-      // Every warp's output to its ring; then each rank combines its columns
-      // of all the team's warps.
+      // Every warp's output to its ring; the CTA's four in sum to the ranks
+      // that hold the columns; there the eight ranks' in sum.
       float* mine = reinterpret_cast<float*>(smem + warp * S::kRingBytes);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -873,19 +906,46 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
             const int d = dm * 16 + (F8 ? 2 * gr + (j >> 1) : gr + 8 * (j >> 1));
             mine[(nt * 8 + 2 * tq + (j & 1)) * S::kPart + d] = o[nt][dm][j];
           }
-      cluster_sync();
-      combine(
-          S::kTw, !split, my_slot,
-          [&](int k, int h) {
-            return make_float2(ld_rank(at_rank(&s_m[k % kWarps][h], k / kWarps)),
-                               ld_rank(at_rank(&s_l[k % kWarps][h], k / kWarps)));
-          },
-          [&](int k, int e) {
-            const float* at = reinterpret_cast<const float*>(smem + (k % kWarps) * S::kRingBytes) +
-                              (e / kQuads) * S::kPart + (e % kQuads) * 4;
-            return ld_rank4(at_rank(at, k / kWarps));
-          });
-      cluster_sync();  // the rings are free again (and may go)
+      float4* got = reinterpret_cast<float4*>(smem + S::kMergeAt);          // [rank][kShare]
+      float2* got_ml = reinterpret_cast<float2*>(got + S::kTeam * S::kShare);  // [rank][16]
+      // the ranks run, and are done with what they received before
+      if (again) cluster_arrive();
+      again = true;
+      cluster_wait();
+      __syncthreads();
+      for (int e = tid; e < all; e += kThreads) {
+        const int h = e / kQuads;
+        float2 ml;
+        const float4 v = four_warps(h, [&](int w) {
+          return reinterpret_cast<const float*>(smem + w * S::kRingBytes) + h * S::kPart + (e % kQuads) * 4;
+        }, ml);
+        const int to = e / per;
+        st_rank4(at_rank(got + rank * S::kShare + (e - to * per), to), v);
+        st_rank2(at_rank(got_ml + rank * 16 + h, to), ml);
+      }
+      cluster_arrive();
+      cluster_wait();
+      for (int e = e_lo + tid; e < e_hi; e += kThreads) {
+        const int h = e / kQuads;
+        float mm = got_ml[h].x;
+#pragma unroll
+        for (int r = 1; r < S::kTeam; ++r) mm = fmaxf(mm, got_ml[r * 16 + h].x);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
+        float4 v = make_float4(0, 0, 0, 0);
+        float lsum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < S::kTeam; ++r) {
+          const float2 ml = got_ml[r * 16 + h];
+          const float4 x = got[r * S::kShare + e - e_lo];
+          const float f = ex2(ml.x - ref);
+          v.x = fmaf(f, x.x, v.x);
+          v.y = fmaf(f, x.y, v.y);
+          v.z = fmaf(f, x.z, v.z);
+          v.w = fmaf(f, x.w, v.w);
+          lsum = fmaf(f, ml.y, lsum);
+        }
+        emit(!split, my_slot, e, v, mm, lsum);
+      }
     } else {
       constexpr int kPasses = DP / S::kCols, kPq = S::kCols / 4;
 #pragma unroll
@@ -904,23 +964,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
         __syncthreads();
         for (int i = tid; i < heads * kPq; i += kThreads) {
           const int h = i / kPq, dc = (i % kPq) * 4;
-          float mm = s_m[0][h];
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][h]);
-          const float ref = mm == -INFINITY ? 0.0f : mm;
-          float4 v = make_float4(0, 0, 0, 0);
-          float lsum = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(s_m[w][h] - ref);
-            const float4 x = *reinterpret_cast<const float4*>(merge + (w * S::kHeads + h) * S::kPitch + dc);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
-            lsum = fmaf(f, s_l[w][h], lsum);
-          }
-          emit(!split, my_slot, h * kQuads + (pass * S::kCols + dc) / 4, v, mm, lsum);
+          float2 ml;
+          const float4 v = four_warps(h, [&](int w) { return merge + (w * S::kHeads + h) * S::kPitch + dc; }, ml);
+          emit(!split, my_slot, h * kQuads + (pass * S::kCols + dc) / 4, v, ml.x, ml.y);
         }
       }
     }
