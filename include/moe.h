@@ -295,8 +295,8 @@ MOE_API moe_status_t moe_add_rmsnorm(const moe_norm_t* n, void* stream);
 typedef struct moe_kv_cache {
   void* k;
   void* v;
-  const float* k_scale; /* [n_kv_heads], value = stored * scale; MOE_E4M3 only, */
-  const float* v_scale; /* NULL = 1                                              */
+  const float* k_scale; /* [n_kv_heads], value = stored * scale (normal positive */
+  const float* v_scale; /* numbers); MOE_E4M3 only, NULL = 1                     */
   int64_t k_page_stride, k_token_stride, k_head_stride;
   int64_t v_page_stride, v_token_stride, v_head_stride;
   int32_t n_pages, page_size, n_kv_heads;
@@ -317,7 +317,7 @@ typedef struct moe_kv_cache {
  * (up to 2^31) lose nothing.  A negative slot stores nothing (padding; q_out is
  * still written); a slot past the cache stores nothing and is recorded in the
  * status word of ws (MOE_ERR_DEVICE from moe_query_status).  Tokens that share
- * a slot leave either's values.  rot_dim is even, <= head_dim (0: no rotation),
+ * a slot leave either's values.  T <= 2^30; rot_dim is even, <= head_dim (0: no rotation),
  * and a multiple of 16 unless interleaved; q and k heads of stride multiples
  * of 16 bytes.  q_out may be q (in place).  ws: any workspace of this library
  * (only its status word is used). */

@@ -63,11 +63,7 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   // The line of units is counted in 32 bits.
   if (cap / 16 + 2 + 4 > 0x7fffffffll / g.chunks / cache->n_kv_heads / a->B)
     return set_error(MOE_ERR_UNSUPPORTED, "batch * kv heads * table tokens too large");
-  // ceil(2^(31 + s) / page_size), s = ceil(log2 page_size): exact for 31-bit tokens
-  int sh = 0;
-  while ((1ll << sh) < cache->page_size) ++sh;
-  g.page_mul = sh ? static_cast<uint32_t>(((1ull << (31 + sh)) + cache->page_size - 1) / cache->page_size) : 0u;
-  g.page_shift = sh - 1;
+  g.by_page = FastDiv(cache->page_size);
   g.blocks = cache->page_size % 16 == 0;
   g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -66,9 +66,7 @@ struct AttnArgs {
   int32_t hpc;     // query heads of a chunk (<= 8 * NT)
   int32_t group;   // query heads of a kv head
   int32_t max_len; // max_pages * page_size, saturated
-  // token / page_size = umulhi(token, page_mul) >> page_shift (page_mul 0: page_size 1)
-  uint32_t page_mul;
-  int32_t page_shift;
+  FastDiv by_page;
   int32_t blocks;  // page_size % 16 == 0: 16 neighbouring tokens share a page
 };
 
@@ -373,9 +371,6 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       }
     }
   };
-  auto page_of = [&](int tok) {
-    return g.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(tok), g.page_mul) >> g.page_shift) : tok;
-  };
   // Where the rows of a unit are: lane l holds rows l (and l + 32); the unit
   // looked up (n...) is the one after the unit being loaded.
   int page[kRr], off[kRr], npage[kRr], noff[kRr];
@@ -403,7 +398,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       nvalid[r] = row < S::kU && tok >= static_cast<uint32_t>(clo) && tok < static_cast<uint32_t>(clen);
       // rows beside those that count are placed too where a block shares a page
       if (row < S::kU && first >= static_cast<uint32_t>(clo) && last < static_cast<uint32_t>(clen)) {
-        const int idx = page_of(static_cast<int>(tok));
+        const int idx = g.by_page(static_cast<int>(tok));
         noff[r] = static_cast<int>(tok) - idx * g.c.page_size;
         npage[r] = table[idx];
         if (static_cast<uint32_t>(npage[r]) >= static_cast<uint32_t>(g.c.n_pages)) {

@@ -6,6 +6,23 @@
 
 namespace moe {
 
+// n / d for 0 <= n < 2^31 by a multiplication: m = ceil(2^(31 + s) / d) with
+// s = ceil(log2 d) is below 2^32 and exact there.
+struct FastDiv {
+  uint32_t mul = 0;  // 0: d = 1
+  int32_t shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(int32_t d) {
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    mul = s ? static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d) : 0u;
+    shift = s - 1;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift) : n;
+  }
+};
+
 inline bool ptr16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Checks a cache description against the new tensors' dtype.

@@ -1,11 +1,14 @@
 // moe_rope.cu — rotation of new queries and keys, and append of keys and
 // values to a paged cache, with the optional per-head RMS norm before it.
 //
-// A (token, head) item — query, key or value head — takes 8, 16 or 32
-// neighbouring lanes, one 16-byte chunk of 8 elements each: one wide load, the
-// norm's sum by shuffles within the item, the partner half of the rotation by
-// a shuffle, one wide store (8 bytes to an e4m3 cache).  Every element is read
-// and written once.
+// A token's heads are walked by a group of 8, 16 or 32 neighbouring lanes, one
+// 16-byte chunk of 8 elements each: one wide load, the norm's sum by shuffles
+// within the group, the partner half of the rotation by a shuffle, one wide store
+// (8 bytes to an e4m3 cache).  Every element is read and written once.  What
+// belongs to the token (its angles, cache slot) or to the column (norm weights)
+// stays in registers from head to head: with all of it formed per head the
+// kernel was bound by instructions (284 per head and warp; 8192 tokens of 20
+// heads of 256 took 57 us).
 //
 // Angles.  a = pos * f.  f / 2pi is formed as a 64-bit binary fraction of a
 // turn (the 24-bit mantissa of f times the leading 64 bits of 1 / 2pi, shifted
@@ -16,6 +19,8 @@
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "moe_common.cuh"
 #include "moe_kv.h"
 
@@ -23,16 +28,19 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens of a block's items times rot_dim / 2: at least 3 items per token.
-constexpr int kTableMax = 1536;
+constexpr int kTableMax = 1024;  // tokens of a block times rot_dim / 2
+constexpr int kAhead = 4;        // heads loaded ahead
+constexpr int kFill = 4;         // blocks per SM that fill it
 
 struct RopeArgs {
   moe_kv_cache_t c;
   moe_rope_t r;
   Control* ctrl;
-  int32_t heads;    // query + key + value heads of a token
-  int64_t items;    // T * heads
-  int64_t slots;    // n_pages * page_size
+  int32_t heads;   // query + key + value heads of a token
+  int32_t share;   // lane groups that share a token (a power of two)
+  int32_t each;    // heads of a block's token: the block takes heads [y * each, (y + 1) * each)
+  int64_t slots;   // n_pages * page_size
+  FastDiv by_page;
 };
 
 // 1 / 2pi = 0.28be60db9391054a7f09... in base 16: its first 64 fraction bits.
@@ -73,158 +81,163 @@ __device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// LPH lanes per item, NI items per thread.
-template <int DT, int LPH, int NI, bool F8>
+// Blocks along the tokens when `share` of a block's groups share a token.
+inline int64_t r_blocks(const RopeArgs& a, int groups, int share) {
+  const int tokens = groups / share;
+  return (static_cast<int64_t>(a.r.T) + tokens - 1) / tokens;
+}
+
+// LPH lanes per group.
+template <int DT, int LPH, bool F8>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
   __shared__ float2 table[kTableMax];  // [token of the block][frequency]
-  constexpr int kPer = kThreads / LPH;  // items per pass
-  const int tid = threadIdx.x, lane = tid & 31, c = tid % LPH;
   const moe_rope_t& r = a.r;
+  const int tid = threadIdx.x, lane = tid & 31, c = tid % LPH;
+  const int tokens = kThreads / LPH / a.share;  // of a block
+  const int my_tok = tid / LPH / a.share, sub = (tid / LPH) & (a.share - 1);
+  const int t0 = blockIdx.x * tokens, t = t0 + my_tok;
+  const bool live = t < r.T;
   const int D = a.c.head_dim, half = r.rot_dim >> 1, hq = r.n_q_heads, hkv = a.c.n_kv_heads;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kPer * NI);
-  const int t0 = static_cast<int>(first / a.heads);
-  const int rem0 = static_cast<int>(first - static_cast<int64_t>(t0) * a.heads);
+  const int h_lo = blockIdx.y * a.each, h_hi = min(a.heads, h_lo + a.each);
+  const bool col_in = live && c * 8 < D;
   pdl_launch_dependents();
   pdl_wait();
 
-  uint4 raw[NI];
-  int tok[NI], head[NI];
-  int64_t slot[NI];
-  const bool col_in = c * 8 < D;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int k = rem0 + i * kPer + tid / LPH;
-    tok[i] = k / a.heads;  // relative to t0
-    head[i] = k - tok[i] * a.heads;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    slot[i] = -1;
-    if (first + i * kPer + tid / LPH < a.items) {
-      const int64_t t = t0 + tok[i];
-      const void* base;
-      int64_t off;
-      if (head[i] < hq) {
-        base = r.q;
-        off = t * r.q_token_stride + head[i] * r.q_head_stride;
-      } else if (head[i] < hq + hkv) {
-        base = r.k;
-        off = t * r.k_token_stride + (head[i] - hq) * r.k_head_stride;
-      } else {
-        base = r.v;
-        off = t * r.v_token_stride + (head[i] - hq - hkv) * r.v_head_stride;
-      }
-      if (col_in) raw[i] = ld_ordered16(static_cast<const uint16_t*>(base) + off + c * 8);
-      if (head[i] >= hq) slot[i] = r.slots[t];
-    } else {
-      head[i] = -1;
+  // the token's place in the cache
+  int64_t page = -1, off = 0;
+  if (live) {
+    const int64_t s = r.slots[t];
+    if (s >= a.slots) {
+      if (c == 0 && sub == 0 && blockIdx.y == 0) report_error(a.ctrl, kDevBadSlot, static_cast<uint32_t>(t));
+    } else if (s >= 0) {
+      page = a.slots <= 0x7fffffffll ? a.by_page(static_cast<int>(s)) : s / a.c.page_size;
+      off = s - page * a.c.page_size;
     }
   }
-
-  const int last = rem0 + kPer * NI - 1;
-  int ntok = last / a.heads + 1;
-  if (t0 + static_cast<int64_t>(ntok) > r.T) ntok = r.T - t0;
-  for (int i = tid; i < ntok * half; i += kThreads)
-    table[i] = rotation(r.positions[t0 + i / half], r.inv_freq[i % half]);
+  const int ntab = min(tokens, r.T - t0) * half;
+  for (int i = tid; i < ntab; i += kThreads) table[i] = rotation(r.positions[t0 + i / half], r.inv_freq[i % half]);
   __syncthreads();
 
+  // this lane's cosines and sines: of its 8 elements (halves), or of its 4 pairs
+  const int hc = half >> 3;  // chunks of a half
+  const bool turns = r.interleaved ? c * 4 < half : c < 2 * hc;
+  const int partner = (lane & ~(LPH - 1)) + (!turns ? c : c < hc ? c + hc : c - hc);
+  float2 cs[8];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const bool is_q = head[i] >= 0 && head[i] < hq, is_v = head[i] >= hq + hkv;
-    float f[8];
-    unpack8<DT>(raw[i], f);
-    if (r.q_norm_w) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-#pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!is_v && head[i] >= 0 && col_in) {
-        const float rstd = __frcp_rn(sqrtf(__fdiv_rn(ss, static_cast<float>(D)) + r.eps));
-        float w[8];
-        unpack8<DT>(ld_ordered16(static_cast<const uint16_t*>(is_q ? r.q_norm_w : r.k_norm_w) + c * 8), w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
-      }
+  for (int j = 0; j < 8; ++j) {
+    const int p = r.interleaved ? c * 4 + j : (c < hc ? c : c - hc) * 8 + j;
+    cs[j] = make_float2(1.0f, 0.0f);
+    if (live && turns && p < half && !(r.interleaved && j >= 4)) cs[j] = table[my_tok * half + p];
+    if (!r.interleaved && c < hc) cs[j].y = -cs[j].y;  // u_i cos - u_j sin, u_j cos + u_i sin
+  }
+  const float inv_d = __frcp_rn(static_cast<float>(D));
+
+  // Heads r0 .. r1 - 1 of the token's row of heads, of one kind: 0 queries, 1
+  // keys, 2 values.  All groups of a warp make the same number of rounds.
+  auto walk = [&](auto kind, int r0, int r1, const void* in, int64_t in_ts, int64_t in_hs, void* outp, int64_t at,
+                  int64_t out_hs, bool store, const void* norm_w, const float* scales) {
+    constexpr int kKind = decltype(kind)::value;
+    constexpr bool kToF8 = F8 && kKind != 0;
+    const int lo = max(r0, h_lo), hi = min(r1, h_hi);
+    if (lo >= hi) return;
+    const int first = h_lo + (lo - h_lo) / a.share * a.share;
+    const uint16_t* src = static_cast<const uint16_t*>(in) + t * in_ts + c * 8;
+    float w[8];
+    if constexpr (kKind != 2) {
+      uint4 wv = make_uint4(0, 0, 0, 0);
+      if (norm_w && c * 8 < D) wv = ld_ordered16(static_cast<const uint16_t*>(norm_w) + c * 8);
+      unpack8<DT>(wv, w);
     }
-    const float2* cs = table + tok[i] * half;
-    if (r.interleaved) {
-      if (head[i] >= 0 && !is_v) {
+    for (int hb = first; hb < hi; hb += kAhead * a.share) {
+      uint4 raw[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int p = c * 4 + j;
-          if (p < half) {
-            const float2 t = cs[p];
-            const float u = f[2 * j], v = f[2 * j + 1];
-            f[2 * j] = u * t.x - v * t.y;
-            f[2 * j + 1] = v * t.x + u * t.y;
+      for (int i = 0; i < kAhead; ++i) {
+        const int h = hb + i * a.share + sub;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (col_in && h >= lo && h < hi) raw[i] = ld_ordered16(src + (h - r0) * in_hs);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (hb + i * a.share >= hi) break;  // the same for the whole warp
+        const int h = hb + i * a.share + sub;
+        float f[8];
+        unpack8<DT>(raw[i], f);
+        if constexpr (kKind != 2) {
+          if (norm_w) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float rstd = rsqrtf(fmaf(ss, inv_d, r.eps));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
+          }
+          if (r.interleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (c * 4 + j >= half) break;
+              const float u = f[2 * j], v = f[2 * j + 1];
+              f[2 * j] = u * cs[j].x - v * cs[j].y;
+              f[2 * j + 1] = v * cs[j].x + u * cs[j].y;
+            }
+          } else if (half) {
+            float g[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], partner);
+            if (turns) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = f[j] * cs[j].x + g[j] * cs[j].y;
+            }
           }
         }
-      }
-    } else if (half) {
-      const int hc = half >> 3;  // chunks of a half
-      const int src = (lane & ~(LPH - 1)) + (c < hc ? c + hc : c < 2 * hc ? c - hc : c);
-      float g[8];
+        if (!col_in || !store || h < lo || h >= hi) continue;
+        const int64_t to = at + (h - r0) * out_hs + c * 8;
+        if constexpr (kToF8) {
+          const float s8 = scales ? __frcp_rn(scales[h - r0]) : 1.0f;
+          uint32_t q[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], src);
-      if (head[i] >= 0 && !is_v && c < 2 * hc) {
-        const int p = (c < hc ? c : c - hc) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 t = cs[p + j];
-          f[j] = c < hc ? f[j] * t.x - g[j] * t.y : f[j] * t.x + g[j] * t.y;
+          for (int j = 0; j < 4; ++j)
+            q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j] * s8, f[2 * j + 1] * s8),
+                                            __NV_SATFINITE, __NV_E4M3);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(outp) + to) =
+              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(outp) + to) =
+              kKind == 2 ? raw[i]
+                         : make_uint4(pack2(DT, f[0], f[1]), pack2(DT, f[2], f[3]), pack2(DT, f[4], f[5]),
+                                      pack2(DT, f[6], f[7]));
         }
       }
     }
-    if (head[i] < 0 || !col_in) continue;
-    if (is_q) {
-      uint16_t* o = static_cast<uint16_t*>(r.q_out) + (t0 + static_cast<int64_t>(tok[i])) * r.out_token_stride +
-                    head[i] * r.out_head_stride + c * 8;
-      *reinterpret_cast<uint4*>(o) =
-          make_uint4(pack2(DT, f[0], f[1]), pack2(DT, f[2], f[3]), pack2(DT, f[4], f[5]), pack2(DT, f[6], f[7]));
-      continue;
-    }
-    const int64_t s = slot[i];
-    if (s < 0) continue;
-    if (s >= a.slots) {
-      if (c == 0 && a.ctrl) report_error(a.ctrl, kDevBadSlot, static_cast<uint32_t>(t0 + tok[i]));
-      continue;
-    }
-    int64_t page, off;
-    if (a.slots <= 0xffffffffll) {
-      page = static_cast<uint32_t>(s) / static_cast<uint32_t>(a.c.page_size);
-      off = static_cast<uint32_t>(s) % static_cast<uint32_t>(a.c.page_size);
-    } else {
-      page = s / a.c.page_size;
-      off = s % a.c.page_size;
-    }
-    const int hd = is_v ? head[i] - hq - hkv : head[i] - hq;
-    const int64_t at = is_v ? page * a.c.v_page_stride + off * a.c.v_token_stride + hd * a.c.v_head_stride
-                            : page * a.c.k_page_stride + off * a.c.k_token_stride + hd * a.c.k_head_stride;
-    void* cache = is_v ? a.c.v : a.c.k;
-    if constexpr (F8) {
-      const float* sc = is_v ? a.c.v_scale : a.c.k_scale;
-      const float s8 = sc ? sc[hd] : 1.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], s8);
-      uint32_t q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j], f[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at + c * 8) =
-          make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + at + c * 8) =
-          make_uint4(pack2(DT, f[0], f[1]), pack2(DT, f[2], f[3]), pack2(DT, f[4], f[5]), pack2(DT, f[6], f[7]));
-    }
-  }
+  };
+  walk(std::integral_constant<int, 0>(), 0, hq, r.q, r.q_token_stride, r.q_head_stride, r.q_out,
+       t * r.out_token_stride, r.out_head_stride, true, r.q_norm_w, nullptr);
+  walk(std::integral_constant<int, 1>(), hq, hq + hkv, r.k, r.k_token_stride, r.k_head_stride, a.c.k,
+       page * a.c.k_page_stride + off * a.c.k_token_stride, a.c.k_head_stride, page >= 0, r.k_norm_w, a.c.k_scale);
+  walk(std::integral_constant<int, 2>(), hq + hkv, a.heads, r.v, r.v_token_stride, r.v_head_stride, a.c.v,
+       page * a.c.v_page_stride + off * a.c.v_token_stride, a.c.v_head_stride, page >= 0, nullptr, a.c.v_scale);
 }
 
 template <int DT, int LPH, bool F8>
-moe_status_t launch(const RopeArgs& a, cudaStream_t st) {
-  constexpr int kPer = kThreads / LPH;
-  const int64_t grid = (a.items + kPer - 1) / kPer;
-  if (grid > 0x7fffffff) return set_error(MOE_ERR_UNSUPPORTED, "too many (token, head) pairs");
-  if (launch_pdl(rope_append_kernel<DT, LPH, 1, F8>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, a) !=
-      cudaSuccess)
+moe_status_t launch(RopeArgs a, cudaStream_t st) {
+  constexpr int kGroups = kThreads / LPH;
+  // Few tokens: their heads over all groups of a block and over blocks, one head
+  // each.  Many: a group per token walks all its heads, as soon as that fills
+  // kFill blocks per SM; between them, fewer groups share a token.
+  const int64_t fill = kFill * static_cast<int64_t>(sm_count());
+  a.share = kGroups;
+  while (a.share > 1 && (r_blocks(a, kGroups, a.share / 2)) >= fill) a.share >>= 1;
+  int rounds = (a.heads + a.share - 1) / a.share;  // heads of a group
+  const int64_t bx = r_blocks(a, kGroups, a.share);
+  int by = 1;
+  while (by < rounds && bx * by < fill) ++by;
+  rounds = (rounds + by - 1) / by;
+  a.each = rounds * a.share;
+  by = (a.heads + a.each - 1) / a.each;
+  if (bx > 0x7fffffff || by > 65535) return set_error(MOE_ERR_UNSUPPORTED, "too many (token, head) pairs");
+  if (launch_pdl(rope_append_kernel<DT, LPH, F8>, dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by)),
+                 dim3(kThreads), 0, st, a) != cudaSuccess)
     return check_launch("rope_append_kernel");
   stat_kernels(1);
   return MOE_OK;
@@ -267,6 +280,7 @@ extern "C" moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_r
   if ((r->q_token_stride | r->q_head_stride | r->k_token_stride | r->k_head_stride | r->v_token_stride |
        r->v_head_stride | r->out_token_stride | r->out_head_stride) & 7)
     return set_error(MOE_ERR_UNSUPPORTED, "strides of q, k, v and q_out must be multiples of 16 bytes");
+  if (r->T > (1 << 30)) return set_error(MOE_ERR_UNSUPPORTED, "T must be <= 2^30");
   if (static_cast<int64_t>(r->n_q_heads) + 2 * static_cast<int64_t>(cache->n_kv_heads) > (1 << 20))
     return set_error(MOE_ERR_UNSUPPORTED, "too many heads");
   RopeArgs a;
@@ -274,8 +288,8 @@ extern "C" moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_r
   a.r = *r;
   a.ctrl = static_cast<Control*>(ws);
   a.heads = r->n_q_heads + 2 * cache->n_kv_heads;
-  a.items = static_cast<int64_t>(r->T) * a.heads;
   a.slots = static_cast<int64_t>(cache->n_pages) * cache->page_size;
+  a.by_page = FastDiv(cache->page_size);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f8 = cache->dtype == MOE_E4M3;
   if (r->dtype == MOE_BF16) return f8 ? dispatch<MOE_BF16, true>(a, st) : dispatch<MOE_BF16, false>(a, st);
