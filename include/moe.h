@@ -290,7 +290,7 @@ MOE_API moe_status_t moe_add_rmsnorm(const moe_norm_t* n, void* stream);
 
 /* A paged key/value cache: token j of a sequence lives in slot j % page_size
  * of the page its block table names.  Strides tell the order of pages, tokens
- * and heads (each a multiple of 16 bytes); a page may hold its tokens or its
+ * and heads (each a multiple of 16 bytes, from 0 to 2^30 elements); a page may hold its tokens or its
  * heads outermost. */
 typedef struct moe_kv_cache {
   void* k;

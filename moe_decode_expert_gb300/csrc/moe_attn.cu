@@ -64,6 +64,13 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   if (cap / 16 + 2 + 4 > 0x7fffffffll / g.chunks / cache->n_kv_heads / a->B)
     return set_error(MOE_ERR_UNSUPPORTED, "batch * kv heads * table tokens too large");
   g.by_page = FastDiv(cache->page_size);
+  const int64_t size = cache->dtype == MOE_E4M3 ? 1 : 2;
+  g.k_page = static_cast<uint32_t>(cache->k_page_stride * size);
+  g.k_token = static_cast<uint32_t>(cache->k_token_stride * size);
+  g.k_head = static_cast<uint32_t>(cache->k_head_stride * size);
+  g.v_page = static_cast<uint32_t>(cache->v_page_stride * size);
+  g.v_token = static_cast<uint32_t>(cache->v_token_stride * size);
+  g.v_head = static_cast<uint32_t>(cache->v_head_stride * size);
   g.blocks = cache->page_size % 16 == 0;
   g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

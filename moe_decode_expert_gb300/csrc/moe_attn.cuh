@@ -67,6 +67,7 @@ struct AttnArgs {
   int32_t group;   // query heads of a kv head
   int32_t max_len; // max_pages * page_size, saturated
   FastDiv by_page;
+  uint32_t k_page, k_token, k_head, v_page, v_token, v_head;  // the cache's strides in bytes
   int32_t blocks;  // page_size % 16 == 0: 16 neighbouring tokens share a page
 };
 
@@ -432,31 +433,33 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       return;
     }
     const uint64_t vm = vm1;
-    const int64_t ps = keys ? g.c.k_page_stride : g.c.v_page_stride;
-    const int64_t ts = keys ? g.c.k_token_stride : g.c.v_token_stride;
-    const int64_t hs = keys ? g.c.k_head_stride : g.c.v_head_stride;
-    const uint8_t* at = static_cast<const uint8_t*>(keys ? g.c.k : g.c.v) + kvh_l * hs * S::kBytes + col * 16;
+    // 32 by 32 bit products: one instruction each
+    const uint32_t ps = keys ? g.k_page : g.v_page, ts = keys ? g.k_token : g.v_token, hs = keys ? g.k_head : g.v_head;
+    const uint8_t* at = static_cast<const uint8_t*>(keys ? g.c.k : g.c.v) +
+                        static_cast<uint64_t>(static_cast<uint32_t>(kvh_l)) * hs + col * 16;
     if (g.blocks) {
       // 16 rows on one page: one address, then steps
+      at += static_cast<uint64_t>(static_cast<uint32_t>(row0)) * ts;
 #pragma unroll
       for (int bl = 0; bl < S::kU / 16; ++bl) {
-        const int pg = __shfl_sync(0xffffffffu, page[bl >> 1], (bl & 1) * 16);
-        const int of = __shfl_sync(0xffffffffu, off[bl >> 1], (bl & 1) * 16);
+        const uint32_t pg = static_cast<uint32_t>(max(__shfl_sync(0xffffffffu, page[bl >> 1], (bl & 1) * 16), 0));
+        const uint32_t of = static_cast<uint32_t>(__shfl_sync(0xffffffffu, off[bl >> 1], (bl & 1) * 16));
         const uint32_t bits = col_in ? static_cast<uint32_t>(vm >> (bl * 16 + row0)) : 0u;
-        const uint8_t* src = at + (max(pg, 0) * ps + (of + row0) * ts) * S::kBytes;
+        const uint8_t* src = at + static_cast<uint64_t>(pg) * ps + static_cast<uint64_t>(of) * ts;
+        const uint64_t step = static_cast<uint64_t>(ts) * kStep;
 #pragma unroll
-        for (int i = 0; i < 16 / kStep; ++i)
-          cp16_or_zero(slot + swz<S::kCpr>(bl * 16 + i * kStep + row0, col), src + i * kStep * ts * S::kBytes,
-                       ((bits >> (i * kStep)) & 1u) << 4);
+        for (int i = 0; i < 16 / kStep; ++i, src += step)
+          cp16_or_zero(slot + swz<S::kCpr>(bl * 16 + i * kStep + row0, col), src, ((bits >> (i * kStep)) & 1u) << 4);
       }
     } else {
+      const uint64_t bits = col_in ? vm >> row0 : 0u;
 #pragma unroll
       for (int i = 0; i < S::kU / kStep; ++i) {
         const int r = i * kStep + row0;
-        const int pg = __shfl_sync(0xffffffffu, page[i * kStep / 32], r & 31);
-        const int of = __shfl_sync(0xffffffffu, off[i * kStep / 32], r & 31);
-        const bool in = ((vm >> r) & 1) && col_in;
-        cp16_or_zero(slot + swz<S::kCpr>(r, col), at + (in ? (pg * ps + of * ts) * S::kBytes : 0), in ? 16u : 0u);
+        const uint32_t pg = static_cast<uint32_t>(max(__shfl_sync(0xffffffffu, page[i * kStep / 32], r & 31), 0));
+        const uint32_t of = static_cast<uint32_t>(__shfl_sync(0xffffffffu, off[i * kStep / 32], r & 31));
+        const uint8_t* src = at + static_cast<uint64_t>(pg) * ps + static_cast<uint64_t>(of) * ts;
+        cp16_or_zero(slot + swz<S::kCpr>(r, col), src, (static_cast<uint32_t>(bits >> (i * kStep)) & 1u) << 4);
       }
     }
     cp_commit();

@@ -39,6 +39,10 @@ inline moe_status_t check_cache(const moe_kv_cache_t* c, int32_t dtype) {
     return set_error(MOE_ERR_UNSUPPORTED, "cache: head_dim must be a multiple of %d up to 256", lane);
   const int64_t s = c->k_page_stride | c->k_token_stride | c->k_head_stride | c->v_page_stride | c->v_token_stride |
                     c->v_head_stride;
+  const int64_t most = INT32_MAX / 2 + 1;  // 2^30 elements, below 2^32 bytes
+  for (int64_t v : {c->k_page_stride, c->k_token_stride, c->k_head_stride, c->v_page_stride, c->v_token_stride,
+                    c->v_head_stride})
+    if (v < 0 || v > most) return set_error(MOE_ERR_UNSUPPORTED, "cache: strides must be from 0 to 2^30 elements");
   if (s % lane) return set_error(MOE_ERR_UNSUPPORTED, "cache: strides must be multiples of 16 bytes");
   if (!c->k || !c->v) return set_error(MOE_ERR_INVALID_ARG, "cache: k / v is NULL");
   if (!ptr16(c->k) || !ptr16(c->v)) return set_error(MOE_ERR_INVALID_ARG, "cache: k / v is not 16-byte aligned");

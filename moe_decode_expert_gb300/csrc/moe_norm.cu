@@ -39,14 +39,26 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // Scale of a row or group from its largest |y| (kept NaN if that is NaN).
-__device__ __forceinline__ float scale_of(float amax) {
-  return __fdiv_rn(amax < kAmaxFloor ? kAmaxFloor : amax, kE4m3Max);
+__device__ __forceinline__ float scale_of(float amax) { return (amax < kAmaxFloor ? kAmaxFloor : amax) * (1.0f / kE4m3Max); }
+
+// 1 / s to one unit in the last place (s is at least 2^-105 here).
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
 }
+
+// Threads of a block at most: rows of one or two vectors per thread take
+// kThreads, of four or eight 512, scalar ones 1024.
+constexpr int kThreads = 256;
+constexpr int kWarpVecs = 128;  // rows of up to this many vectors: a warp each
+template <int VEC, int NV>
+constexpr int kMaxThreads = VEC == 1 ? 1024 : NV < 4 ? kThreads : 512;
 
 // VEC elements (8: one 16-byte load, 1: any alignment) NV times per thread.
 // WARP: a warp per row; else a CTA per row.
 template <int DT, int VEC, int NV, int OUT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
+__global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel(moe_norm_t a) {
   __shared__ float s_sum[32];
   __shared__ uint32_t s_max[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -62,9 +74,10 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
   uint16_t* ro = static_cast<uint16_t*>(a.residual_out) + row * a.residual_out_stride;
   const bool res = a.residual != nullptr, res_out = a.residual_out != nullptr;
 
-  float h[NV * VEC], wf[NV * VEC];
+  float h[NV * VEC];
+  [[maybe_unused]] uint4 wv[VEC == 8 ? NV : 1];  // weights stay packed
   if constexpr (VEC == 8) {
-    uint4 xv[NV], rv[NV], wv[NV];
+    uint4 xv[NV], rv[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * nthr + tid) * 8;
@@ -77,25 +90,20 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float xf[8], rf[8], w8[8];
+      float xf[8], rf[8];
       unpack8<DT>(xv[v], xf);
       unpack8<DT>(rv[v], rf);
-      unpack8<DT>(wv[v], w8);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[v * 8 + j] = res ? xf[j] + rf[j] : xf[j];
-        wf[v * 8 + j] = w8[j];
-      }
+      for (int j = 0; j < 8; ++j) h[v * 8 + j] = res ? xf[j] + rf[j] : xf[j];
     }
   } else {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = v * nthr + tid;
-      h[v] = wf[v] = 0.0f;
+      h[v] = 0.0f;
       if (c < a.H) {
         h[v] = load_scalar<DT>(x, c);
         if (res) h[v] += load_scalar<DT>(r, c);
-        wf[v] = load_scalar<DT>(w, c);
       }
     }
   }
@@ -103,9 +111,16 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
   float sum = 0.0f;
   uint32_t mx = 0u;
 #pragma unroll
-  for (int i = 0; i < NV * VEC; ++i) {
-    sum = fmaf(h[i], h[i], sum);
-    if (OUT == kOutRow) mx = max(mx, __float_as_uint(h[i] * wf[i]) & 0x7fffffffu);
+  for (int i = 0; i < NV * VEC; ++i) sum = fmaf(h[i], h[i], sum);
+  if (OUT == kOutRow) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float w8[VEC];
+      if constexpr (VEC == 8) unpack8<DT>(wv[v], w8);
+      else w8[0] = v * nthr + tid < a.H ? load_scalar<DT>(w, v * nthr + tid) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) mx = max(mx, __float_as_uint(h[v * VEC + j] * w8[j]) & 0x7fffffffu);
+    }
   }
   sum = warp_sum(sum);
   if (OUT == kOutRow) mx = __reduce_max_sync(0xffffffffu, mx);
@@ -119,12 +134,12 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
     sum = warp_sum(lane < nw ? s_sum[lane] : 0.0f);
     if (OUT == kOutRow) mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
   }
-  const float rstd = __frcp_rn(sqrtf(__fdiv_rn(sum, static_cast<float>(a.H)) + a.eps));
+  const float rstd = rsqrtf(__fdiv_rn(sum, static_cast<float>(a.H)) + a.eps);
 
   float inv = 1.0f;
   if (OUT == kOutRow) {
     const float s = scale_of(__uint_as_float(mx) * rstd);
-    inv = __frcp_rn(s);
+    inv = reciprocal(s);
     if (tid == 0) a.scales[row] = s;
   }
 
@@ -136,8 +151,9 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
       const int c = (v * nthr + tid) * 8;
       const bool in = c < a.H;
       float y[8];
+      unpack8<DT>(wv[v], y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = h[v * 8 + j] * rstd * wf[v * 8 + j];
+      for (int j = 0; j < 8; ++j) y[j] *= h[v * 8 + j] * rstd;
       if (in && res_out) {
         const float* p = h + v * 8;
         *reinterpret_cast<uint4*>(ro + c) =
@@ -156,7 +172,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
           for (int j = 0; j < 8; ++j) g = max(g, __float_as_uint(y[j]) & 0x7fffffffu);
           for (int o = 1; o < (a.group >> 3); o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
           const float s = scale_of(__uint_as_float(g));
-          inv = __frcp_rn(s);
+          inv = reciprocal(s);
           if (in && (c % a.group) == 0)
             a.scales[row * ((a.H + a.group - 1) / a.group) + c / a.group] = s;
         }
@@ -167,7 +183,9 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(moe_norm_t a) {
     } else {
       const int c = v * nthr + tid;
       if (c < a.H) {
-        const float y = h[v] * rstd * wf[v];
+        // The weight comes from L1 again: held in registers beside x and r, its
+        // loads delayed theirs (16384 x 2047: 133 us against 73).
+        const float y = h[v] * rstd * load_scalar<DT>(w, c);
         if (res_out) store_out(ro, c, h[v], DT);
         if (OUT == kOutSame)
           store_out(o16, c, y, DT);
@@ -200,11 +218,18 @@ moe_status_t dispatch(const moe_norm_t& n, bool wide, cudaStream_t st) {
     }
   }
   const int vecs = (n.H + 7) / 8;
-  const int nv = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+  if (vecs <= kWarpVecs) {
+    const int nv = (vecs + 31) / 32;
+    if (nv == 1) return launch<DT, 8, 1, OUT, true>(n, 128, st);
+    if (nv == 2) return launch<DT, 8, 2, OUT, true>(n, 128, st);
+    return launch<DT, 8, 4, OUT, true>(n, 128, st);
+  }
+  const int nv = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : vecs <= 4 * 512 ? 4 : 8;
   const int thr = ((vecs + nv - 1) / nv + 31) / 32 * 32;
   if (nv == 1) return launch<DT, 8, 1, OUT, false>(n, thr, st);
   if (nv == 2) return launch<DT, 8, 2, OUT, false>(n, thr, st);
-  return launch<DT, 8, 4, OUT, false>(n, thr, st);
+  if (nv == 4) return launch<DT, 8, 4, OUT, false>(n, thr, st);
+  return launch<DT, 8, 8, OUT, false>(n, thr, st);
 }
 
 }  // namespace

@@ -27,9 +27,9 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTableMax = 1024;  // tokens of a block times rot_dim / 2
-constexpr int kAhead = 4;        // heads loaded ahead
+constexpr int kThreads = 128;
+constexpr int kTableMax = 512;   // tokens of a block times rot_dim / 2
+constexpr int kAhead = 2;        // heads in hand, and heads loaded ahead
 constexpr int kFill = 4;         // blocks per SM that fill it
 
 struct RopeArgs {
@@ -88,8 +88,8 @@ inline int64_t r_blocks(const RopeArgs& a, int groups, int share) {
 }
 
 // LPH lanes per group.
-template <int DT, int LPH, bool F8>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
+template <int DT, int LPH, bool F8, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
   __shared__ float2 table[kTableMax];  // [token of the block][frequency]
   const moe_rope_t& r = a.r;
   const int tid = threadIdx.x, lane = tid & 31, c = tid % LPH;
@@ -118,18 +118,11 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
   for (int i = tid; i < ntab; i += kThreads) table[i] = rotation(r.positions[t0 + i / half], r.inv_freq[i % half]);
   __syncthreads();
 
-  // this lane's cosines and sines: of its 8 elements (halves), or of its 4 pairs
+  // Which of this lane's elements turn, and with which lane's elements (halves).
   const int hc = half >> 3;  // chunks of a half
-  const bool turns = r.interleaved ? c * 4 < half : c < 2 * hc;
-  const int partner = (lane & ~(LPH - 1)) + (!turns ? c : c < hc ? c + hc : c - hc);
-  float2 cs[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int p = r.interleaved ? c * 4 + j : (c < hc ? c : c - hc) * 8 + j;
-    cs[j] = make_float2(1.0f, 0.0f);
-    if (live && turns && p < half && !(r.interleaved && j >= 4)) cs[j] = table[my_tok * half + p];
-    if (!r.interleaved && c < hc) cs[j].y = -cs[j].y;  // u_i cos - u_j sin, u_j cos + u_i sin
-  }
+  const bool turns = PAIRS ? c * 4 < half : c < 2 * hc;
+  const int partner = (lane & ~(LPH - 1)) + (PAIRS || !turns ? c : c < hc ? c + hc : c - hc);
+  const int pc = partner & (LPH - 1);  // that lane's chunk
   const float inv_d = __frcp_rn(static_cast<float>(D));
 
   // Heads r0 .. r1 - 1 of the token's row of heads, of one kind: 0 queries, 1
@@ -141,58 +134,88 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
     const int lo = max(r0, h_lo), hi = min(r1, h_hi);
     if (lo >= hi) return;
     const int first = h_lo + (lo - h_lo) / a.share * a.share;
-    const uint16_t* src = static_cast<const uint16_t*>(in) + t * in_ts + c * 8;
-    float w[8];
+    const int64_t step = a.share * in_hs, out_step = a.share * out_hs;
+    const uint16_t* src = static_cast<const uint16_t*>(in) + t * in_ts + (first + sub - r0) * in_hs + c * 8;
+    int64_t to = at + (first + sub - r0) * out_hs + c * 8;
+    // A turned element is (its own value times ca + its partner's times cb) *
+    // 1/rms: the norm weights and the angle's sign go into the factors.
+    float ca[8], cb[8];
     if constexpr (kKind != 2) {
-      uint4 wv = make_uint4(0, 0, 0, 0);
-      if (norm_w && c * 8 < D) wv = ld_ordered16(static_cast<const uint16_t*>(norm_w) + c * 8);
-      unpack8<DT>(wv, w);
+      const bool in_d = c * 8 < D;
+      float wp[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ca[j] = wp[j] = 1.0f;
+      if (norm_w && in_d) {
+        unpack8<DT>(ld_ordered16(static_cast<const uint16_t*>(norm_w) + c * 8), ca);
+        unpack8<DT>(ld_ordered16(static_cast<const uint16_t*>(norm_w) + pc * 8), wp);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = PAIRS ? c * 4 + (j >> 1) : (c < hc ? c : c - hc) * 8 + j;
+        cb[j] = 0.0f;
+        if (live && turns && p < half) {
+          const float2 t2 = table[my_tok * half + p];
+          const bool minus = PAIRS ? (j & 1) == 0 : c < hc;
+          ca[j] *= t2.x;
+          cb[j] = (minus ? -t2.y : t2.y) * (PAIRS ? wp[j ^ 1] : wp[j]);
+        }
+      }
     }
-    for (int hb = first; hb < hi; hb += kAhead * a.share) {
-      uint4 raw[kAhead];
+    // kAhead heads in hand, the next kAhead on their way
+    uint4 raw[kAhead], next[kAhead];
+    auto fetch = [&](int hb) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int h = hb + i * a.share + sub;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (col_in && h >= lo && h < hi) raw[i] = ld_ordered16(src + (h - r0) * in_hs);
+        next[i] = make_uint4(0, 0, 0, 0);
+        if (col_in && h >= lo && h < hi) next[i] = ld_ordered16(src);
+        src += step;
       }
+    };
+    fetch(first);
+    for (int hb = first; hb < hi; hb += kAhead * a.share) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
+      fetch(hb + kAhead * a.share);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i, to += out_step) {
         if (hb + i * a.share >= hi) break;  // the same for the whole warp
         const int h = hb + i * a.share + sub;
         float f[8];
         unpack8<DT>(raw[i], f);
         if constexpr (kKind != 2) {
+          float rstd = 1.0f;
           if (norm_w) {
             float ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rstd = rsqrtf(fmaf(ss, inv_d, r.eps));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
+            rstd = rsqrtf(fmaf(ss, inv_d, r.eps));
           }
-          if (r.interleaved) {
+          float g[8];
+          if constexpr (PAIRS) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (c * 4 + j >= half) break;
-              const float u = f[2 * j], v = f[2 * j + 1];
-              f[2 * j] = u * cs[j].x - v * cs[j].y;
-              f[2 * j + 1] = v * cs[j].x + u * cs[j].y;
-            }
+            for (int j = 0; j < 8; ++j) g[j] = f[j ^ 1];
           } else if (half) {
-            float g[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], partner);
-            if (turns) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) f[j] = f[j] * cs[j].x + g[j] * cs[j].y;
-            }
+            uint4 other;
+            other.x = __shfl_sync(0xffffffffu, raw[i].x, partner);
+            other.y = __shfl_sync(0xffffffffu, raw[i].y, partner);
+            other.z = __shfl_sync(0xffffffffu, raw[i].z, partner);
+            other.w = __shfl_sync(0xffffffffu, raw[i].w, partner);
+            unpack8<DT>(other, g);
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= ca[j];
+          if (turns) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (!PAIRS || c * 4 + (j >> 1) < half) f[j] = fmaf(g[j], cb[j], f[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] *= rstd;
         }
         if (!col_in || !store || h < lo || h >= hi) continue;
-        const int64_t to = at + (h - r0) * out_hs + c * 8;
         if constexpr (kToF8) {
           const float s8 = scales ? __frcp_rn(scales[h - r0]) : 1.0f;
           uint32_t q[4];
@@ -219,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
        page * a.c.v_page_stride + off * a.c.v_token_stride, a.c.v_head_stride, page >= 0, nullptr, a.c.v_scale);
 }
 
-template <int DT, int LPH, bool F8>
+template <int DT, int LPH, bool F8, bool PAIRS>
 moe_status_t launch(RopeArgs a, cudaStream_t st) {
   constexpr int kGroups = kThreads / LPH;
   // Few tokens: their heads over all groups of a block and over blocks, one head
@@ -236,18 +259,24 @@ moe_status_t launch(RopeArgs a, cudaStream_t st) {
   a.each = rounds * a.share;
   by = (a.heads + a.each - 1) / a.each;
   if (bx > 0x7fffffff || by > 65535) return set_error(MOE_ERR_UNSUPPORTED, "too many (token, head) pairs");
-  if (launch_pdl(rope_append_kernel<DT, LPH, F8>, dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by)),
+  if (launch_pdl(rope_append_kernel<DT, LPH, F8, PAIRS>, dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by)),
                  dim3(kThreads), 0, st, a) != cudaSuccess)
     return check_launch("rope_append_kernel");
   stat_kernels(1);
   return MOE_OK;
 }
 
-template <int DT, bool F8>
+template <int DT, bool F8, bool PAIRS>
 moe_status_t dispatch(const RopeArgs& a, cudaStream_t st) {
-  if (a.c.head_dim <= 64) return launch<DT, 8, F8>(a, st);
-  if (a.c.head_dim <= 128) return launch<DT, 16, F8>(a, st);
-  return launch<DT, 32, F8>(a, st);
+  if (a.c.head_dim <= 64) return launch<DT, 8, F8, PAIRS>(a, st);
+  if (a.c.head_dim <= 128) return launch<DT, 16, F8, PAIRS>(a, st);
+  return launch<DT, 32, F8, PAIRS>(a, st);
+}
+
+template <int DT>
+moe_status_t dispatch(const RopeArgs& a, cudaStream_t st) {
+  if (a.c.dtype == MOE_E4M3) return a.r.interleaved ? dispatch<DT, true, true>(a, st) : dispatch<DT, true, false>(a, st);
+  return a.r.interleaved ? dispatch<DT, false, true>(a, st) : dispatch<DT, false, false>(a, st);
 }
 
 }  // namespace
@@ -291,7 +320,5 @@ extern "C" moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_r
   a.slots = static_cast<int64_t>(cache->n_pages) * cache->page_size;
   a.by_page = FastDiv(cache->page_size);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool f8 = cache->dtype == MOE_E4M3;
-  if (r->dtype == MOE_BF16) return f8 ? dispatch<MOE_BF16, true>(a, st) : dispatch<MOE_BF16, false>(a, st);
-  return f8 ? dispatch<MOE_F16, true>(a, st) : dispatch<MOE_F16, false>(a, st);
+  return r->dtype == MOE_BF16 ? dispatch<MOE_BF16>(a, st) : dispatch<MOE_F16>(a, st);
 }

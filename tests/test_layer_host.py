@@ -72,7 +72,7 @@ CACHE_REFUSALS = [
     (dict(n_pages=0), 1), (dict(page_size=0), 1), (dict(n_kv_heads=0), 1), (dict(head_dim=0), 1),
     (dict(head_dim=100), 2), (dict(head_dim=264), 2), (dict(cache_dtype=1), 2), (dict(cache_dtype=3), 2),
     (dict(cache_dtype=4, head_dim=72), 2), (dict(cache_k=0), 1), (dict(cache_v=264), 1), (dict(kp=8196), 2),
-    (dict(vt=516), 2), (dict(k_scale=64), 1), (dict(cache_dtype=4, k_scale=66), 1),
+    (dict(vt=516), 2), (dict(vp=-8192), 2), (dict(kp=(1 << 30) + 8), 2), (dict(k_scale=64), 1), (dict(cache_dtype=4, k_scale=66), 1),
 ]
 
 
