@@ -24,7 +24,10 @@ extern "C" size_t moe_attention_workspace_bytes(const moe_kv_cache_t* cache, int
       n_q_heads % cache->n_kv_heads)
     return 0;
   const int nt = n_tiles(n_q_heads / cache->n_kv_heads);
-  return kPartsAt + static_cast<size_t>(kMaxCtas) * 2 * 8 * nt * padded_dim(cache->head_dim) * sizeof(float);
+  const int dp = padded_dim(cache->head_dim);
+  // up to four CTAs per SM at head_dim <= 64, else two
+  const size_t chunks = dp > 64 ? kMaxChunks / 2 : kMaxChunks;
+  return kPartsAt + chunks * 2 * 8 * nt * dp * sizeof(float);
 }
 
 extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws,

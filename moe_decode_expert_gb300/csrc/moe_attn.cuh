@@ -35,26 +35,30 @@ namespace moe {
 namespace {
 
 constexpr int kRing = 3;         // slots of a warp's ring
-constexpr int kMaxCtas = 640;    // partial slots in the workspace: two per CTA
+constexpr int kMaxSms = 160;     // SMs that a launch fills
+constexpr int kMaxCtas = 4 * kMaxSms;
+constexpr int kSmallPer = 2;     // small chunks per CTA of a long line
+constexpr int kMaxChunks = kMaxCtas * (1 + kSmallPer);  // partial slots in the workspace: two per chunk
 constexpr int kTeamCtas = 8;     // CTAs of a team (a cluster), and the most teams
 constexpr int kMaxTeams = 40;
-constexpr int kJoin = 16;        // parts joined by one CTA at a time
-constexpr int kMaxGroups = (kMaxCtas + kJoin - 1) / kJoin;
+constexpr int kMaxParts = 64;    // partial results combined at a time
 constexpr int kTeamMin = 128;
+constexpr int kLong = 256;       // places per CTA from which a line keeps some back
+constexpr int kBack = 20;        // per cent of them
 constexpr int kCtas64 = 4;
 constexpr int kCtas128 = 2;
 constexpr int kCtas256 = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Workspace: control block, join counters [kMaxCtas][4] (teams: [team][8]),
-// partial statistics [kMaxCtas * 2][16][2] fp32 (teams: [team * 2][8][16][2]),
-// partial outputs [kMaxCtas * 2][heads][DP] fp32 (teams: [team * 2][heads][DP]).
+// Workspace: control block, join counters [kMaxChunks][4] (teams: [team][8]) and
+// the number of small chunks taken, partial statistics [kMaxChunks * 2][16][2]
+// fp32 (teams: [team * 2][8][16][2]), partial outputs [chunks * 2][heads][DP] fp32.
 constexpr size_t kCountersAt = 256;
-constexpr size_t kStatsAt = kCountersAt + kMaxCtas * 4 * sizeof(uint32_t);
-constexpr size_t kPartsAt = kStatsAt + kMaxCtas * 2 * 16 * 2 * sizeof(float);
+constexpr size_t kStatsAt = kCountersAt + kMaxChunks * 4 * sizeof(uint32_t) + 256;
+constexpr size_t kPartsAt = kStatsAt + kMaxChunks * 2 * 16 * 2 * sizeof(float);
 static_assert(kPartsAt % 256 == 0, "partials are 256-byte aligned");
-static_assert(kMaxTeams * 8 <= kMaxCtas * 4 && kMaxTeams * 8 <= kMaxCtas, "teams fit where CTAs do");
+static_assert(kMaxTeams * 8 <= kMaxCtas, "teams fit where CTAs do");
 
 }  // namespace
 
@@ -141,12 +145,11 @@ __device__ __forceinline__ uint32_t e4m3_half2(uint32_t two) {
 
 // What a combination of partial results keeps in shared memory (kThreads
 // float4 follow it).
-constexpr int kMaxParts = 40;
+template <int HEADS>
 struct Combine {
-  float w[kMaxParts][16], lp[kMaxParts][16];  // references, then weights; partial sums
-  float m[16], l[16];
+  float w[kMaxParts][HEADS], lp[kMaxParts][HEADS];  // references, then weights; partial sums
+  float m[HEADS], l[HEADS];
 };
-static_assert(kMaxTeams <= kMaxParts && kMaxGroups <= kMaxParts && kJoin <= kMaxParts, "parts of a combination");
 
 // Everything of a kernel that does not depend on its place in the line.
 template <int QT, bool F8, int DP, int NT, bool TEAM>
@@ -163,12 +166,15 @@ struct Shape {
   static constexpr int kFill = (TEAM || DP > 64 ? 8192 : 4096) / (DP * kBytes);
   static constexpr int kU = kFill < 16 ? 16 : kFill < 64 ? kFill : 64;  // tokens of a unit
   static constexpr int kCtas = TEAM ? 2 : DP == 256 ? kCtas256 : DP == 128 ? kCtas128 : NT == 1 ? kCtas64 : 3;  // CTAs of an SM
+  static constexpr int kHeads = 8 * NT;
+  // parts joined at a time: kMaxParts groups hold every chunk of a launch
+  static constexpr int kJoin = DP > 64 ? 32 : 64;
+  static_assert(kJoin <= kMaxParts && kCtas * kMaxSms * (1 + kSmallPer) <= kJoin * kMaxParts, "two levels of joins do");
   static constexpr int kRow = DP * kBytes;                                            // bytes of a row
   static constexpr int kSlot = kU * kRow;
   static constexpr int kCpr = kRow / 16;   // 16-byte chunks of a row
   static constexpr int kMt = kU / 16;      // m tiles of a unit's scores
   static constexpr int kDm = DP / 16;      // m tiles of the output
-  static constexpr int kHeads = 8 * NT;
   static constexpr int kCols = NT == 1 && DP > 64 ? 64 : 32;  // output columns the warps merge at a time
   static constexpr int kPitch = kCols + 4;         // their fp32 pitch: conflict-free
   static constexpr bool kBf16 = !F8 && QT == MOE_BF16;  // type of the matrix products
@@ -177,7 +183,7 @@ struct Shape {
   static constexpr int kRingBytes = kRing * kSlot;  // of a warp
   static constexpr int kMergeAt = kWarps * kRingBytes;
   static constexpr int kMerge = TEAM ? 0 : kWarps * kHeads * kPitch * 4;
-  static constexpr int kCombine = static_cast<int>(sizeof(Combine)) + kThreads * 16;
+  static constexpr int kCombine = static_cast<int>(sizeof(Combine<kHeads>)) + kThreads * 16;
   // what a team CTA receives: its columns and all statistics from every rank
   static constexpr int kShare = kHeads * DP / 4 / kTeamCtas;  // column quads
   static constexpr int kReceive = TEAM ? kTeam * (kShare * 16 + 16 * 8) : 0;
@@ -196,15 +202,21 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ ((r >> 1) & 3)) << 4));
 }
 
-// The line: worker c of n takes `each` of its places, the first `more` workers
-// one more.
+// The line in chunks.  The n workers begin with a chunk each, of `each` places,
+// the first `more` of one more.  A long line keeps its last part back: from
+// `wide` on, chunks of `small` places that CTAs take as they get done, because SMs
+// do not get equal shares of the memory's bandwidth (with equal chunks the last CTA
+// of 304 was done at 96 us where the median was at 82).
 struct Line {
-  int total, n, each, more;  // n: workers (CTAs or teams)
-  __device__ __forceinline__ int start(int c) const { return each * c + min(c, more); }
+  int total, n, each, more, wide, small, chunks;
+  __device__ __forceinline__ int start(int c) const {
+    return c <= n ? each * c + min(c, more) : min(wide + (c - n) * small, total);
+  }
   __device__ __forceinline__ int owner(int x) const {
-    const int wide = more * (each + 1);
-    return x < wide ? static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(each + 1))
-                    : more + static_cast<int>(static_cast<unsigned>(x - wide) / static_cast<unsigned>(each));
+    const int first = more * (each + 1);
+    if (x < first) return static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(each + 1));
+    if (x < wide) return more + static_cast<int>(static_cast<unsigned>(x - first) / static_cast<unsigned>(each));
+    return n + static_cast<int>(static_cast<unsigned>(x - wide) / static_cast<unsigned>(small));
   }
 };
 
@@ -259,93 +271,60 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     return places_of(low(len), len);
   };
 
-  // The line's length, this worker's share of it, and the sequence that holds
-  // the share's start.
+  // The line's length and shape.  Up to 32 sequences: every warp by itself, a
+  // sequence per lane.
   const int segs = g.c.n_kv_heads * g.chunks;  // segments of a sequence
   // the worker, and this CTA's and warp's number in it
-  const int cta = static_cast<int>(blockIdx.x) / S::kTeam;
+  const int worker = static_cast<int>(blockIdx.x) / S::kTeam;
   const int rank = TEAM ? static_cast<int>(cluster_rank()) : 0;
   const int tw = rank * kWarps + warp;
-  Line ln;
-  auto share = [&](int sum) {  // the line's shape from its places before * segs
-    ln.total = sum * segs;
-    ln.n = (ln.total + kMinUnits - 1) / kMinUnits;
-    if constexpr (TEAM) ln.n = max(ln.n, a.B * segs);
-    ln.n = min(ln.n, static_cast<int>(gridDim.x) / S::kTeam);
-    ln.each = static_cast<int>(static_cast<unsigned>(ln.total) / static_cast<unsigned>(ln.n));
-    ln.more = ln.total - ln.each * ln.n;
-  };
-  int b, prefix, len, p, p_end;
+  int my_len = 0, my_u = 0, my_inc = 0;  // a lane's sequence: length, places, places up to its end
+  int sum = 0;
   if (a.B <= 32) {
-    // every warp by itself, a sequence per lane
-    const int my_len = lane < a.B ? clamp_len(a.seq_lens[lane]) : 0;
-    const int u = lane < a.B ? places_of(low(my_len), my_len) : 0;
-    int inc = u;
+    if (lane < a.B) {
+      my_len = clamp_len(a.seq_lens[lane]);
+      my_u = places_of(low(my_len), my_len);
+    }
+    my_inc = my_u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const int v = __shfl_up_sync(0xffffffffu, my_inc, o);
+      if (lane >= o) my_inc += v;
     }
-    share(__shfl_sync(0xffffffffu, inc, 31));
-    if (cta >= ln.n) return;
-    p = ln.start(cta);
-    p_end = ln.start(cta + 1);
-    b = 31 - __clz(__ballot_sync(0xffffffffu, u > 0 && (inc - u) * segs <= p));
-    prefix = __shfl_sync(0xffffffffu, inc - u, b);
-    len = __shfl_sync(0xffffffffu, my_len, b);
+    sum = __shfl_sync(0xffffffffu, my_inc, 31);
   } else {
-    // the first kThreads sequences stay in registers
-    const int u0 = tid < a.B ? places(tid) : 0;
-    int sum = u0;
-    for (int i = tid + kThreads; i < a.B; i += kThreads) sum += places(i);
+    for (int i = tid; i < a.B; i += kThreads) sum += places(i);
     sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) s_scan[warp] = sum;
     __syncthreads();
     sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += s_scan[w];
-    share(sum);
-    if (cta >= ln.n) return;
-    p = ln.start(cta);
-    p_end = ln.start(cta + 1);
-    int before = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-      const int i = b0 + tid;
-      const int u = b0 == 0 ? u0 : i < a.B ? places(i) : 0;
-      int inc = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
-      if (tid == 0) s_b = -1;
-      __syncthreads();
-      int ex = before + inc - u;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) ex += s_scan[w];
-        before += s_scan[w];
-      }
-      if (u > 0 && ex * segs <= p && p < (ex + u) * segs) {
-        s_b = i;
-        s_prefix = ex;
-      }
-      __syncthreads();
-      if (s_b >= 0) break;
-    }
-    b = s_b;
-    prefix = s_prefix;
-    len = clamp_len(a.seq_lens[b]);
   }
-  int lo = low(len), nb = places_of(lo, len);
-  if constexpr (TEAM) cluster_arrive();  // waited for before the first write to another rank
+  Line ln;
+  ln.total = sum * segs;
+  ln.n = (ln.total + kMinUnits - 1) / kMinUnits;
+  if constexpr (TEAM) ln.n = max(ln.n, a.B * segs);
+  ln.n = min(ln.n, static_cast<int>(gridDim.x) / S::kTeam);
+  if (worker >= ln.n) return;
+  ln.each = static_cast<int>(static_cast<unsigned>(ln.total) / static_cast<unsigned>(ln.n));
+  ln.more = ln.total - ln.each * ln.n;
+  ln.wide = ln.total;
+  ln.small = 1;
+  ln.chunks = ln.n;
+  if (!TEAM && ln.each >= kLong) {
+    ln.each -= static_cast<int>(static_cast<unsigned>(ln.each) * kBack / 100u);
+    ln.more = 0;
+    ln.wide = ln.each * ln.n;
+    ln.small = (ln.total - ln.wide + kSmallPer * ln.n - 1) / (kSmallPer * ln.n);
+    ln.chunks = ln.n + (ln.total - ln.wide + ln.small - 1) / ln.small;
+  }
 
   const uint32_t ring = smem_u32(smem + warp * (kRing * S::kSlot));
   float* merge = reinterpret_cast<float*>(smem + S::kMergeAt);
-  Combine& cb_s = *reinterpret_cast<Combine*>(smem + S::kMergeAt);
-  float4* cb_x = reinterpret_cast<float4*>(smem + S::kMergeAt + sizeof(Combine));
+  using Comb = Combine<S::kHeads>;
+  Comb& cb_s = *reinterpret_cast<Comb*>(smem + S::kMergeAt);
+  float4* cb_x = reinterpret_cast<float4*>(smem + S::kMergeAt + sizeof(Comb));
   const int D = g.c.head_dim;
 
   // ------------------------------------------------------------------ loads
@@ -357,6 +336,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   constexpr int kStep = 32 / S::kCpr;     // rows of one pass of the warp
   const int col = lane % S::kCpr, row0 = lane / S::kCpr;
   const bool col_in = col * 16 < D * S::kBytes;
+  int b = 0, prefix = 0, len = 0, lo = 0, nb = 0, p, p_end;
   int left, cb, cseg, cu;  // places still to look at; sequence, segment and place there
   int clen, clo, cnb, next_len;
   auto settle = [&]() {  // bring the cursor's place into its segment
@@ -482,12 +462,58 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
 #pragma unroll 1
     for (int k = 0; k < kRing; ++k) issue(slot_at(k));  // K, V, K: vm0 is the first unit's mask, vm1 the second's
   };
+  [[maybe_unused]] bool again = false;  // a team that has combined a segment before
+  if constexpr (TEAM) cluster_arrive();  // waited for before the first write to another rank
+
+  for (int cta = worker;;) {  // the chunk in hand
+  p = ln.start(cta);
+  p_end = ln.start(cta + 1);
+  // The sequence that holds p: the one whose places, before * segs, reach it.
+  if (a.B <= 32) {
+    b = 31 - __clz(__ballot_sync(0xffffffffu, my_u > 0 && (my_inc - my_u) * segs <= p));
+    prefix = __shfl_sync(0xffffffffu, my_inc - my_u, b);
+    len = __shfl_sync(0xffffffffu, my_len, b);
+  } else {
+    int before = 0;
+    for (int b0 = 0;; b0 += kThreads) {
+      const int i = b0 + tid;
+      const int u = i < a.B ? places(i) : 0;
+      int inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = inc;
+      if (tid == 0) s_b = -1;
+      __syncthreads();
+      int ex = before + inc - u;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) ex += s_scan[w];
+        before += s_scan[w];
+      }
+      if (u > 0 && ex * segs <= p && p < (ex + u) * segs) {
+        s_b = i;
+        s_prefix = ex;
+      }
+      __syncthreads();
+      if (s_b >= 0) break;
+    }
+    b = s_b;
+    prefix = s_prefix;
+    len = clamp_len(a.seq_lens[b]);
+  }
+  lo = low(len);
+  nb = places_of(lo, len);
+  int turn = tw;  // line places before this warp's next unit, from p on
   if constexpr (!TEAM) {
+    keys = true;
+    slot = 0;
     const int seg = (p - prefix * segs) / nb;
     start_loads(p_end - p, seg, p - prefix * segs - seg * nb);
   }
-  int turn = tw;  // line places before this warp's next unit, from p on
-  [[maybe_unused]] bool again = false;  // a team that has combined a segment before
 
   while (p < p_end) {
     // ------------------------------------------ the part at places [ub, ue)
@@ -804,28 +830,29 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     // (reference, sum) of a head, quad_of(k, e) its column quad e.  Few columns
     // are shared out over the threads by parts as well.
     auto combine = [&](int count, bool final, int sl, auto stat_of, auto quad_of) {
-      for (int e = tid; e < count * 16; e += kThreads) {
-        const float2 ml = holds(e & 15) ? stat_of(e >> 4, e & 15) : make_float2(-INFINITY, 0.0f);
-        cb_s.w[e >> 4][e & 15] = ml.x;
-        cb_s.lp[e >> 4][e & 15] = ml.y;
+      for (int e = tid; e < count * S::kHeads; e += kThreads) {
+        const float2 ml = holds(e % S::kHeads) ? stat_of(e / S::kHeads, e % S::kHeads) : make_float2(-INFINITY, 0.0f);
+        cb_s.w[e / S::kHeads][e % S::kHeads] = ml.x;
+        cb_s.lp[e / S::kHeads][e % S::kHeads] = ml.y;
       }
       __syncthreads();
       {
-        // 8 neighbouring lanes per head
-        const int h = (tid >> 3) & 15, sub = tid & 7;
+        // kThreads / kHeads neighbouring lanes per head
+        constexpr int kPer = kThreads / S::kHeads;
+        const int h = tid / kPer, sub = tid % kPer;
         float mm = -INFINITY;
-        for (int k = sub; k < count; k += 8) mm = fmaxf(mm, cb_s.w[k][h]);
+        for (int k = sub; k < count; k += kPer) mm = fmaxf(mm, cb_s.w[k][h]);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        for (int o = 1; o < kPer; o <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         const float ref = mm == -INFINITY ? 0.0f : mm;
         float lsum = 0.0f;
-        for (int k = sub; k < count; k += 8) {
+        for (int k = sub; k < count; k += kPer) {
           const float f = ex2(cb_s.w[k][h] - ref);
           cb_s.w[k][h] = f;
           lsum = fmaf(f, cb_s.lp[k][h], lsum);
         }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+        for (int o = 1; o < kPer; o <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
         if (sub == 0) {
           cb_s.m[h] = mm;
           cb_s.l[h] = lsum;
@@ -857,7 +884,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
             for (int k = 0; k < kK; ++k)
 #pragma unroll
               for (int i = 0; i < kQ; ++i) {
-                const float f = k0 + k * ng < count ? cb_s.w[k0 + k * ng][((eb + i * kThreads) / kQuads) & 15] : 0.0f;
+                const float f = k0 + k * ng < count ? cb_s.w[k0 + k * ng][((eb + i * kThreads) / kQuads) % S::kHeads] : 0.0f;
                 v[i].x = fmaf(f, x[k][i].x, v[i].x);
                 v[i].y = fmaf(f, x[k][i].y, v[i].y);
                 v[i].z = fmaf(f, x[k][i].z, v[i].z);
@@ -997,12 +1024,12 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
         // every rank joins its own columns of the teams' slots
         if (arrive(counters + first * 8 + rank, n_parts)) join(0, 1, n_parts, true);
       } else {
-        const int n_groups = (n_parts + kJoin - 1) / kJoin, from = part / kJoin * kJoin;
-        const int count = min(kJoin, n_parts - from);
+        const int n_groups = (n_parts + S::kJoin - 1) / S::kJoin, from = part / S::kJoin * S::kJoin;
+        const int count = min(S::kJoin, n_parts - from);
         uint32_t* at = counters + (first + from) * 4 + (from == 0 ? 1 : 0);
         if (arrive(at, count)) {
           join(from, 1, count, n_groups == 1);
-          if (n_groups > 1 && arrive(counters + first * 4 + 2, n_groups)) join(0, kJoin, n_groups, true);
+          if (n_groups > 1 && arrive(counters + first * 4 + 2, n_groups)) join(0, S::kJoin, n_groups, true);
         }
       }
     }
@@ -1019,6 +1046,17 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     }
   }
   cp_wait<0>();
+  if (TEAM || ln.chunks == ln.n) break;
+  // the next small chunk, if any is left; the last CTA to find none clears the count
+  __syncthreads();
+  if (tid == 0) s_flag = ln.n + static_cast<int>(atomicAdd(counters + kMaxChunks * 4, 1u));
+  __syncthreads();
+  cta = s_flag;
+  if (cta >= ln.chunks) {
+    if (tid == 0 && cta == ln.chunks + ln.n - 1) counters[kMaxChunks * 4] = 0u;
+    break;
+  }
+  }
 }
 
 template <int QT, bool F8, int DP, int NT, bool TEAM>
@@ -1054,7 +1092,7 @@ moe_status_t launch(const AttnArgs& g, cudaStream_t st) {
       if (teams < 1) return set_error(MOE_ERR_UNSUPPORTED, "the device cannot hold a cluster of the kernel");
       grid = (teams < kMaxTeams ? teams : kMaxTeams) * S::kTeam;
     } else {
-      grid = S::kCtas * sm_count() < kMaxCtas ? S::kCtas * sm_count() : kMaxCtas;
+      grid = S::kCtas * (sm_count() < kMaxSms ? sm_count() : kMaxSms);
     }
     grid_of[dev].store(grid, std::memory_order_release);
   }
