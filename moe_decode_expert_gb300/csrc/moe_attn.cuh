@@ -43,6 +43,7 @@ constexpr int kTeamCtas = 8;     // CTAs of a team (a cluster), and the most tea
 constexpr int kMaxTeams = 40;
 constexpr int kMaxParts = 64;    // partial results combined at a time
 constexpr int kTeamMin = 128;
+constexpr int kSolo = 4;         // units up to which a segment is one warp's
 constexpr int kLong = 256;       // places per CTA from which a line keeps some back
 constexpr int kBack = 20;        // per cent of them
 constexpr int kCtas64 = 4;
@@ -304,8 +305,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   Line ln;
   ln.total = sum * segs;
   ln.n = (ln.total + kMinUnits - 1) / kMinUnits;
-  if constexpr (TEAM) ln.n = max(ln.n, a.B * segs);
-  ln.n = min(ln.n, static_cast<int>(gridDim.x) / S::kTeam);
+  // a worker per segment, as long as there are workers: a segment of one unit
+  // costs several units' time
+  ln.n = min(max(ln.n, a.B * segs), static_cast<int>(gridDim.x) / S::kTeam);
   if (worker >= ln.n) return;
   ln.each = static_cast<int>(static_cast<unsigned>(ln.total) / static_cast<unsigned>(ln.n));
   ln.more = ln.total - ln.each * ln.n;
@@ -328,20 +330,45 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   const int D = g.c.head_dim;
 
   // ------------------------------------------------------------------ loads
-  // This warp's units are at places p + tw, p + tw + kTw, ... of the line.
-  // Their loads run ahead of the arithmetic: a cursor walks the units to load,
-  // across segment ends (a team's within a segment: its rings hold the outputs
+  // The loads of this warp's units run ahead of the arithmetic: a cursor walks
+  // the units to load, across segment ends (a team's within a segment: its rings hold the outputs
   // at the end of one).
   constexpr int kRr = (S::kU + 31) / 32;  // rows of a unit per lane
   constexpr int kStep = 32 / S::kCpr;     // rows of one pass of the warp
   const int col = lane % S::kCpr, row0 = lane / S::kCpr;
   const bool col_in = col * 16 < D * S::kBytes;
   int b = 0, prefix = 0, len = 0, lo = 0, nb = 0, p, p_end;
-  int left, cb, cseg, cu;  // places still to look at; sequence, segment and place there
-  int clen, clo, cnb, next_len;
-  auto settle = [&]() {  // bring the cursor's place into its segment
-    while (cu >= cnb) {
-      cu -= cnb;
+  int cb, cseg, clen, clo, cnb, next_len;  // the cursor's sequence and segment
+  int cu, cue, cstep, cleft;  // its next unit, the end and step there; places left after that part
+  // Which units of a segment's part at places [ub, ue) are this warp's: units
+  // u, u + step, ... below `end`.  A short segment in one piece is one warp's
+  // alone (solo), so that its end needs no barrier and the other warps go on;
+  // else the warps take turns, beginning with another one in each segment.
+  auto mine = [&](int sidx, int places_of_seg, int ub, int ue, int& u, int& end, int& step) {
+    const int u0 = max(ub - kVoid, 0);
+    end = ue - kVoid;
+    if (!TEAM && places_of_seg <= kVoid + kSolo && u0 == 0 && ue == places_of_seg) {
+      u = 0;
+      step = 1;
+      if ((sidx & (kWarps - 1)) != warp) end = 0;
+      return true;
+    }
+    u = u0 + ((tw - sidx) & (S::kTw - 1));
+    step = S::kTw;
+    return false;
+  };
+  auto enter = [&](int ub, int n) {  // the cursor's segment from place ub on, n places left
+    const int ue = min(cnb, ub + n);
+    cleft = n - (ue - ub);
+    mine(cb * segs + cseg, cnb, ub, ue, cu, cue, cstep);
+  };
+  // Where the rows of a unit are: lane l holds rows l (and l + 32); the unit
+  // looked up (n...) is the one after the unit being loaded.
+  int page[kRr], off[kRr], npage[kRr], noff[kRr];
+  int kvh_l = 0, nkvh = 0;  // their kv heads
+  bool have = false, nhave = false, nvalid[kRr];
+  auto look_up = [&]() {
+    while (cu >= cue && cleft > 0) {
       if (++cseg == segs) {
         cseg = 0;
         ++cb;
@@ -350,21 +377,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
         cnb = places_of(clo, clen);
         next_len = cb + 1 < a.B ? a.seq_lens[cb + 1] : 0;
       }
+      enter(0, cleft);
     }
-  };
-  // Where the rows of a unit are: lane l holds rows l (and l + 32); the unit
-  // looked up (n...) is the one after the unit being loaded.
-  int page[kRr], off[kRr], npage[kRr], noff[kRr];
-  int kvh_l = 0, nkvh = 0;  // their kv heads
-  bool have = false, nhave = false, nvalid[kRr];
-  auto look_up = [&]() {
-    nhave = false;
-    while (left > 0 && !nhave) {
-      --left;
-      settle();
-      nhave = cu >= kVoid;
-      if (!nhave) cu += S::kTw;
-    }
+    nhave = cu < cue;
 #pragma unroll
     for (int r = 0; r < kRr; ++r) npage[r] = -1, noff[r] = 0, nvalid[r] = false;
     if (!nhave) return;
@@ -374,7 +389,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     for (int r = 0; r < kRr; ++r) {
       const int row = lane + 32 * r;
       // unsigned: the last unit may reach past the largest int
-      const uint32_t tok = static_cast<uint32_t>(clo / S::kU + cu - kVoid) * S::kU + row;
+      const uint32_t tok = static_cast<uint32_t>(clo / S::kU + cu) * S::kU + row;
       const uint32_t first = g.blocks ? tok | 15u : tok, last = g.blocks ? tok & ~15u : tok;
       nvalid[r] = row < S::kU && tok >= static_cast<uint32_t>(clo) && tok < static_cast<uint32_t>(clen);
       // rows beside those that count are placed too where a block shares a page
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
         }
       }
     }
-    cu += S::kTw;
+    cu += cstep;
   };
   uint64_t vm0 = 0, vm1 = 0;  // tokens of the unit in hand and of the next that count
   bool keys = true;           // what is loaded next: keys, then the same unit's values
@@ -454,9 +469,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   };
   // Start on `n` places from place `u` of segment `seg` of sequence b.
   auto start_loads = [&](int n, int seg, int u) {
-    left = n > tw ? (n - tw + S::kTw - 1) / S::kTw : 0;
-    cb = b, cseg = seg, cu = u + tw;
+    cb = b, cseg = seg;
     clen = len, clo = lo, cnb = nb;
+    enter(u, n);
     next_len = cb + 1 < a.B ? a.seq_lens[cb + 1] : 0;
     look_up();
 #pragma unroll 1
@@ -507,7 +522,6 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   }
   lo = low(len);
   nb = places_of(lo, len);
-  int turn = tw;  // line places before this warp's next unit, from p on
   if constexpr (!TEAM) {
     keys = true;
     slot = 0;
@@ -529,7 +543,6 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     if constexpr (TEAM) {
       keys = true;
       slot = 0;
-      turn = tw;
       start_loads(ue - ub, seg, ub);
     }
     if (tid == 0 && rank == 0) {
@@ -537,6 +550,12 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       if (raw < 0 || raw > g.max_len) report_error(ctrl, kDevBadLength, static_cast<uint32_t>(b));
     }
 
+    int u, u_end, u_step;
+    const bool solo = mine(b * segs + seg, nb, ub, ue, u, u_end, u_step);
+    const float vscale = F8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.0f;
+    float o[NT][S::kDm][4];
+    float m[NT][2], l[NT][2];  // a head's reference (log2) and this lane's share of its sum
+    if (!solo || u < u_end) {
     // Q fragments (the B operand): head gr of an n tile, its elements in the
     // order in which K fragments bring theirs.
     uint32_t qf[NT][DP / 16][2];
@@ -584,8 +603,6 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     }
     const float s2 = a.scale * kLog2e * (F8 && g.c.k_scale ? g.c.k_scale[kvh] : 1.0f);
 
-    float o[NT][S::kDm][4];
-    float m[NT][2], l[NT][2];  // a head's reference (log2) and this lane's share of its sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -601,8 +618,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     const int kc = lane >> 4;                           // and its chunk
     const int vr = F8 ? (lane & 7) + 8 * ((lane >> 3) & 1) : (lane & 7) + 8 * (lane >> 4);
     const int vc = F8 ? lane >> 4 : (lane >> 3) & 1;
-    for (; turn < ue - ub; turn += S::kTw) {
-      if (ub + turn < kVoid) continue;
+    for (; u < u_end; u += u_step) {
       const uint64_t vm = vm0;
       cp_wait<kRing - 1>();
       __syncwarp();
@@ -754,24 +770,68 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       issue(slot_at(0));
       if (++slot == kRing) slot = 0;
     }
-    turn -= ue - ub;
-
-    // ------------------------------------------------ the four warps meet
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float t = l[nt][j];
-        t += __shfl_xor_sync(0xffffffffu, t, 4);
-        t += __shfl_xor_sync(0xffffffffu, t, 8);
-        t += __shfl_xor_sync(0xffffffffu, t, 16);
-        if (gr == 0) {
-          s_m[warp][nt * 8 + 2 * tq + j] = m[nt][j];
-          s_l[warp][nt * 8 + 2 * tq + j] = t;
+        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+        l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+      }
+    if (solo) {
+      // straight from the registers, two neighbouring columns at a time
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int h = nt * 8 + 2 * tq;  // this lane's first head
+        float inv[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          inv[j] = l[nt][j] == 0.0f ? 0.0f : __fdiv_rn(vscale, l[nt][j]);
+          if (gr == 0 && h + j < heads && a.lse)
+            a.lse[static_cast<int64_t>(b) * a.n_q_heads + h0 + h + j] =
+                l[nt][j] == 0.0f ? -INFINITY : (m[nt][j] + log2f(l[nt][j])) * kLn2;
+        }
+        uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_seq_stride + (h0 + h) * a.out_head_stride;
+#pragma unroll
+        for (int dm = 0; dm < S::kDm; ++dm) {
+          const float* v = o[nt][dm];
+          if constexpr (F8) {
+            // rows 2 gr and 2 gr + 1 of either head
+            const int d = dm * 16 + 2 * gr;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (h + j < heads && d < D)
+                *reinterpret_cast<uint32_t*>(out + j * a.out_head_stride + d) =
+                    pack<QT == MOE_BF16>(v[j] * inv[j], v[2 + j] * inv[j]);
+          } else {
+            // rows gr and gr + 8: an even row's lane takes both rows of the first
+            // head, the odd one's both of the second
+            const int odd = gr & 1, d = dm * 16 + (gr & ~1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float x = v[2 * k] * inv[0], y = v[2 * k + 1] * inv[1];
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
+              if (h + odd < heads && d + 8 * k < D)
+                *reinterpret_cast<uint32_t*>(out + odd * a.out_head_stride + d + 8 * k) =
+                    odd ? pack<QT == MOE_BF16>(got, y) : pack<QT == MOE_BF16>(x, got);
+            }
+          }
         }
       }
+    }
+    }
+
+    // ------------------------------------------------ the four warps meet
+    if (!solo) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (gr == 0) {
+          s_m[warp][nt * 8 + 2 * tq + j] = m[nt][j];
+          s_l[warp][nt * 8 + 2 * tq + j] = l[nt][j];
+        }
     const bool split = ub > kVoid || ue < nb;
-    const float vscale = F8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.0f;
     constexpr int kQuads = DP / 4;
     const int part = cta - (split ? ln.owner(seg_start + kVoid) : cta);
     const int my_slot = cta * 2 + (part == 0 ? 1 : 0);
@@ -1034,6 +1094,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       }
     }
     if constexpr (!TEAM) __syncthreads();  // the merge buffer and the statistics are free again
+    }
 
     // ---------------------------------------------------- the next segment
     p += ue - ub;

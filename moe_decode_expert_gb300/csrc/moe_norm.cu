@@ -210,10 +210,8 @@ template <int DT, int OUT>
 moe_status_t dispatch(const moe_norm_t& n, bool wide, cudaStream_t st) {
   if (!wide) {
     if constexpr (OUT != kOutGroup) {
-      if (n.H <= 4 * 1024) {
-        const int thr = ((n.H + 3) / 4 + 31) / 32 * 32;
-        return launch<DT, 1, 4, OUT, false>(n, thr, st);
-      }
+      if (n.H <= 4 * 512) return launch<DT, 1, 4, OUT, false>(n, ((n.H + 3) / 4 + 31) / 32 * 32, st);
+      if (n.H <= 8 * 1024) return launch<DT, 1, 8, OUT, false>(n, ((n.H + 7) / 8 + 31) / 32 * 32, st);
       return launch<DT, 1, 32, OUT, false>(n, 1024, st);
     }
   }
