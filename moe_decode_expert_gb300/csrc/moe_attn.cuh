@@ -137,11 +137,12 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   }
 }
 
-// Two e4m3 values (low 16 bits) -> two fp16 values, exact.
-__device__ __forceinline__ uint32_t e4m3_half2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 values -> the low two and the high two as fp16 pairs, exact.
+__device__ __forceinline__ void e4m3_half4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 // What a combination of partial results keeps in shared memory (kThreads
@@ -602,6 +603,8 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       }
     }
     const float s2 = a.scale * kLog2e * (F8 && g.c.k_scale ? g.c.k_scale[kvh] : 1.0f);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) qscale[nt][0] *= s2, qscale[nt][1] *= s2;
 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -648,8 +651,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
             ldsm4(f, kslot + swz<S::kCpr>(mt * 16 + kr, ks + kc));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t a0 = e4m3_half2(f[2 * j]), a2 = e4m3_half2(f[2 * j] >> 16);
-              const uint32_t a1 = e4m3_half2(f[2 * j + 1]), a3 = e4m3_half2(f[2 * j + 1] >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3_half4(f[2 * j], a0, a2);
+              e4m3_half4(f[2 * j + 1], a1, a3);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma<false>(s[mt][nt], a0, a1, a2, a3, qf[nt][ks + j][0], qf[nt][ks + j][1]);
@@ -679,8 +683,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
         for (int mt = 0; mt < S::kMt; ++mt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float v = s[mt][nt][j] * s2;
-            if constexpr (F8 && QT == MOE_BF16) v *= qscale[nt][j & 1];
+            float v = s[mt][nt][j] * (F8 && QT == MOE_BF16 ? qscale[nt][j & 1] : s2);
             if (!whole && !((vm >> (mt * 16 + gr + 8 * (j >> 1))) & 1)) v = -INFINITY;
             s[mt][nt][j] = v;
             mx[j & 1] = fmaxf(mx[j & 1], v);
@@ -756,9 +759,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
             for (int j = 0; j < 2; ++j) {
               // 16-bit transposition leaves (token, token + 1) x (d, d + 1)
               // bytes in a register: pair the tokens of one d
-              const uint32_t x = __byte_perm(f[2 * j], 0, 0x3120), y = __byte_perm(f[2 * j + 1], 0, 0x3120);
-              const uint32_t a0 = e4m3_half2(x), a1 = e4m3_half2(x >> 16);
-              const uint32_t a2 = e4m3_half2(y), a3 = e4m3_half2(y >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3_half4(__byte_perm(f[2 * j], 0, 0x3120), a0, a1);
+              e4m3_half4(__byte_perm(f[2 * j + 1], 0, 0x3120), a2, a3);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma<false>(o[nt][dm + j], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
