@@ -925,9 +925,10 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       const int cols = max(e_hi - e_lo, 1);
       const int ng = max(1, min(kThreads / cols, count));  // threads per column quad
       const int gi = ng > 1 ? tid / cols : 0, e0 = ng > 1 ? tid - gi * cols : tid;
-      // kQ quads by kK parts in flight per thread, as registers allow
+      // kQ quads by kK parts in flight per thread, as registers allow (32 loads
+      // in flight spilled and cost 1 to 4 % over all)
       constexpr int kFew = S::kHeads * kQuads / (TEAM ? S::kTeam : 1) / kThreads;
-      constexpr int kFit = S::kCtas > 2 ? 8 : 32;
+      constexpr int kFit = S::kCtas > 2 ? 8 : 16;
       constexpr int kQ = kFew < 1 ? 1 : kFew > 4 ? 4 : kFew, kK = kFit / kQ < 16 ? kFit / kQ : 16;
       for (int eb = e_lo + e0; eb < e_hi; eb += kQ * kThreads) {
         float4 v[kQ];
