@@ -352,6 +352,8 @@ MOE_API moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_rope
  * moe_query_status).  Several new tokens of one sequence are several rows whose
  * table rows repeat and whose lengths count up.
  * One launch; results do not depend on timing (parts join in a fixed order).
+ * Limits: B * n_kv_heads * (max_pages * page_size / 16 + 6) below 2^31, n_q_heads
+ * <= 65536.
  * ws: moe_attention_workspace_bytes(), zero-filled once; not shared by calls
  * that can run at the same time. */
 typedef struct moe_attention {

@@ -12,17 +12,31 @@
 // in the same columns, so the running maximum and sum of a head live in the
 // lanes that hold its column.  movmatrix turns S^T fragments into P^T ones.
 //
-// Work is split evenly over the CTAs whatever the lengths: the (sequence,
-// kv head, unit of U tokens) triples form one line, with kVoid empty places
-// before each (sequence, kv head) for its fixed cost, and CTA c of n takes the
-// c-th n-th of it (every CTA finds its place from seq_lens itself).  A (sequence,
-// kv head) that ends up in several CTAs is joined by the last of them to arrive,
-// in groups of kJoin parts and then over the groups, always in the same order:
-// one launch, results independent of timing.
+// Weights go into the second product as bf16 in two terms (2^-17) or as fp16 in
+// one, 2^14 above their true value (2^-11, and normal down to 2^-28 of the
+// largest); scores, references, sums and outputs are fp32 throughout.
+//
+// Work is split evenly over workers whatever the lengths: the (sequence, kv
+// head, unit of U tokens) triples form one line, with kVoid empty places before
+// each segment, that is each (sequence, kv head), for its fixed cost; worker c of
+// n takes the c-th n-th of it and finds its place from seq_lens itself.  A
+// segment that ends up with several workers is joined by the last of them to
+// arrive, in groups of kJoin parts and then over the groups, always in the same
+// order: one launch, results independent of timing.
+//
+// A worker is a CTA, or, where segments are few, a team: a cluster of 8 CTAs whose
+// warps share each segment and sum their outputs through distributed shared
+// memory, which spares a short sequence the join through global memory (1531
+// tokens of 2 kv heads: 8.3 us against 13.7 with CTAs).
 //
 // A warp owns whole units: K and V of a unit are two slots of its own ring in
-// shared memory, filled by cp.async two slots ahead; only a part's end meets
-// at a CTA barrier.
+// shared memory, filled by cp.async two slots ahead, across segment ends; only the
+// end of a long segment's part meets at a CTA barrier.
+//
+// Measured (fraction of the 6787 GB/s copy): 64 sequences of up to 32k tokens,
+// 16 over 2 heads of 256, bf16: 320 us (100 %); 285k tokens of 8 e4m3 heads of
+// 128, groups of 5: 100 us (86 %); 250 windows of 512 over 12 fp16 heads of 64,
+// pages of 24: 69 us (77 %, bound by instructions: 8 columns for one head).
 
 #pragma once
 
@@ -42,10 +56,20 @@ constexpr int kMaxChunks = kMaxCtas * (1 + kSmallPer);  // partial slots in the 
 constexpr int kTeamCtas = 8;     // CTAs of a team (a cluster), and the most teams
 constexpr int kMaxTeams = 40;
 constexpr int kMaxParts = 64;    // partial results combined at a time
+// Places of the line that a team takes at least (one short sequence in one team:
+// 256 cost 16.3 us where 128 cost 9.4, the two heads then sharing a team).
 constexpr int kTeamMin = 128;
-constexpr int kSolo = 4;         // units up to which a segment is one warp's
-constexpr int kLong = 256;       // places per CTA from which a line keeps some back
-constexpr int kBack = 20;        // per cent of them
+// Units up to which a segment is one warp's alone (8 made 32 heads over 2 kv heads
+// of ragged 8k tokens 12 % slower; none made 20 short segments 1.7 times slower).
+constexpr int kSolo = 4;
+// A line of kLong places per CTA and more keeps kBack per cent of them back for the
+// CTAs that get done first: 327 to 320 us at 438 places per CTA; at 117 places the
+// extra joins cost more than the balance gains (98 to 103 us).
+constexpr int kLong = 256;
+constexpr int kBack = 20;
+// CTAs of an SM.  Rows of 64 elements leave registers for four, with units of half
+// the bytes (the window case: 75 us against 81 with three and 90 with two); wider
+// ones stay with two (three CTAs of half units at 128: within 2 % either way).
 constexpr int kCtas64 = 4;
 constexpr int kCtas128 = 2;
 constexpr int kCtas256 = 2;
@@ -160,9 +184,11 @@ struct Shape {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTeam = TEAM ? kTeamCtas : 1;  // CTAs of a worker
   static constexpr int kTw = kTeam * kWarps;          // its warps
-  // places before a segment's units: its fixed cost, in units
+  // places before a segment's units: its fixed cost, in units (2, 4, 6, 8 differ by
+  // 2 %; without any the window case took a third longer)
   static constexpr int kVoid = TEAM ? 0 : 4;
-  // places of the line a worker takes at least
+  // places of the line a worker takes at least (CTAs: 4 and 6 cost short batches 2
+  // us in joins, 16 and 20 2 us in streaming)
   static constexpr int kMinUnits = TEAM ? kTeamMin : 12;
   static constexpr int kBytes = F8 ? 1 : 2;
   static constexpr int kFill = (TEAM || DP > 64 ? 8192 : 4096) / (DP * kBytes);

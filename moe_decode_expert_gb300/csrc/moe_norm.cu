@@ -9,6 +9,9 @@
 // sum of squares and the row's largest magnitude come out of one reduction.
 // Magnitudes are reduced as unsigned bit patterns: their order is that of the
 // floats, with NaN above infinity, so a NaN reaches the row's scale.
+//
+// HBM bounds it: 16384 rows of 4096 with residual to e4m3 groups of 128 take 76 us,
+// 91 % of the 6787 GB/s copy; 16384 x 2048 in bf16 39.5 us (100 %).
 
 #include <cuda_fp8.h>
 
@@ -50,6 +53,8 @@ __device__ __forceinline__ float reciprocal(float s) {
 
 // Threads of a block at most: rows of one or two vectors per thread take
 // kThreads, of four or eight 512, scalar ones 1024 (512 with 16 elements each).
+// 256 threads leave an SM more rows in flight than 512 (16384 x 4096 e4m3: 76 us
+// against 89); a warp per row needs no barrier (16384 x 512: 11.4 us against 16.9).
 constexpr int kThreads = 256;
 constexpr int kWarpVecs = 128;  // rows of up to this many vectors: a warp each
 template <int VEC, int NV>

@@ -274,3 +274,56 @@ def test_offsets_past_32_bits(m):
     m.moe_paged_attention(cache, new[:1], table, lens, out, ws)
     assert torch.equal(out[0].float(), new[1].float().to(torch.float8_e4m3fn).float())
     m.moe_query_status(ws)
+
+
+@pytest.mark.parametrize("D,lens", [(256, [30000, 1, 2, 3, 4, 5]), (64, [3, 70000, 1, 1, 1])])
+def test_two_levels_of_joins(m, D, lens):
+    """More parts of one sequence than one CTA joins at a time."""
+    c = Case(m, lens, 4, 1, D, 16)
+    first, _ = c.check()
+    again, _ = c.run(ws=c.ws)
+    assert torch.equal(first, again)
+
+
+def test_a_line_long_enough_to_keep_some_back(m):
+    """Over 256 units per CTA: the last ones are taken by whoever gets done first;
+    results stay the same from run to run.  The reference is formed on the GPU."""
+    lens = [62500, 70000, 55001, 61000, 65537]
+    page, hkv, hq, D = 16, 4, 8, 256
+    need = [-(-n // page) for n in lens]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    k, v = (torch.randn(sum(need), page, hkv, D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    order = torch.randperm(sum(need), generator=g, device=DEV).to(torch.int32)
+    table = torch.full((5, max(need)), -1, dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    q = (torch.randn(5, hq, D, generator=g, device=DEV) * 1.5).to(torch.bfloat16)
+    cache = m.MoeKvCache(k, v)
+    ws = m.alloc_attention_workspace(cache, hq)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    outs = []
+    for _ in range(3):
+        out, lse = torch.empty_like(q), torch.empty(5, hq, device=DEV)
+        m.moe_paged_attention(cache, q, table, n, out, ws, lse=lse)
+        outs.append((out, lse))
+    m.moe_query_status(ws)
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+    for b, length in enumerate(lens):
+        pos = torch.arange(length, device=DEV)
+        pages, off = table[b].long()[pos // page], pos % page
+        for h in range(hkv):
+            kh, vh = k[pages, off, h].double(), v[pages, off, h].double()
+            qh = q[b, 2 * h:2 * h + 2].double()
+            s = qh @ kh.T * D ** -0.5
+            total = torch.logsumexp(s, 1)
+            p = torch.exp(s - total[:, None])
+            ref = p @ vh
+            ds = 2.0 ** -17 * D ** -0.5 * (qh.abs() @ kh.abs().T).amax(1, keepdim=True) + 2.0 ** -20
+            err = (2 * ds + 2.0 ** -17 + (length / 16 + 16) * 2.0 ** -22) * (p @ vh.abs())
+            d = (outs[0][0][b, 2 * h:2 * h + 2].double() - ref).abs()
+            assert (d <= rounded(ref, torch.bfloat16, 0.0, err)).all()
+            tol = ds[:, 0] + length * 2.0 ** -24 + 2.0 ** -22 * total.abs() + 2.0 ** -20
+            assert ((outs[0][1][b, 2 * h:2 * h + 2].double() - total).abs() <= tol).all()
