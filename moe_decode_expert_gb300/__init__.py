@@ -140,7 +140,24 @@ def _load():
         f.argtypes = args
         f.restype = res
     _lib = lib
+    _bind_fast_call(lib)
     return lib
+
+
+# The compiled form of the layer operators' checks (csrc/fast_call.cpp): returns
+# the entry's status, or -1 for arguments that the Python form is to explain.
+_fast = None
+
+
+def _bind_fast_call(lib):
+    global _fast
+    try:
+        from . import _fast_call
+    except ImportError:  # not built here: the Python form does the same
+        return
+    _fast_call.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (lib.moe_add_rmsnorm, lib.moe_rope_append, lib.moe_paged_attention)))
+    _fast = _fast_call
 
 
 def library():
@@ -321,8 +338,8 @@ _ATTN_T = struct.Struct("@5P5q5if0q")
 
 
 # A decode step makes these calls dozens of times per token and their kernels
-# take a few microseconds, so their checks are single comparisons and the
-# current stream is asked for as a number.
+# take a few microseconds, so their checks are made in compiled code where that
+# is built, and here in single comparisons, with the stream asked for as a number.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _FLOATS = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
@@ -372,6 +389,12 @@ def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=Non
     x's dtype, or float8_e4m3fn with ``scales`` [T, 1] (one per row) or
     [T, ceil(H / group)].  ``residual_out`` receives the rounded sum (may be
     ``residual`` itself).  Rows may be strided; see include/moe.h."""
+    if _fast is not None:
+        rc = _fast.norm(x, weight, out, residual, residual_out, scales, group, eps, stream)
+        if rc == 0:
+            return
+        if rc > 0:
+            _check(rc)
     shape, dt, dev = x.shape, x.dtype, x.get_device()
     if len(shape) != 2:
         raise ValueError(f"x: shape {tuple(shape)}, expected [T, H]")
@@ -461,6 +484,13 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
     RMS norm when ``q_norm_w`` and ``k_norm_w`` [D] are given, and stores k and v
     in the cache's ``slots`` [T] int64 (page * page_size + place; negative:
     not stored)."""
+    if _fast is not None:
+        rc = _fast.rope(cache._c, cache._dev, q, k, v, positions, slots, inv_freq, q_out, ws, q_norm_w, k_norm_w, eps,
+                        interleaved, stream)
+        if rc == 0:
+            return
+        if rc > 0:
+            _check(rc)
     shape, dt, dev = q.shape, q.dtype, q.get_device()
     code = _FLOATS.get(dt)
     if code is None:
@@ -500,6 +530,12 @@ def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, sc
     ``seq_lens`` [B] int32 cached tokens that ``block_table`` [B, max_pages]
     int32 places, into ``out`` [B, Hq, D] (and ``lse`` [B, Hq] fp32).  ``scale``
     defaults to D ** -0.5; ``window`` > 0 keeps the last ``window`` tokens."""
+    if _fast is not None:
+        rc = _fast.attention(cache._c, cache._dev, q, block_table, seq_lens, out, ws, scale, window, lse, stream)
+        if rc == 0:
+            return
+        if rc > 0:
+            _check(rc)
     shape, dt, dev = q.shape, q.dtype, q.get_device()
     code = _FLOATS.get(dt)
     if code is None:

@@ -11,6 +11,8 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +24,8 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 # see trace_phases.py); never loaded by the package unless asked for.
 TRACE_BUILD = os.path.join(ROOT, "_build", "moe_trace")
 TRACE_LIB = os.path.join(PKG, "libmoe_gb300_trace.so")
+# Argument checks of the layer operators in compiled code (see fast_call.cpp).
+FAST_CALL = os.path.join(PKG, "_fast_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -56,6 +60,34 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     return obj
 
 
+def build_fast_call() -> str | None:
+    """Compile ``csrc/fast_call.cpp`` (host code over PyTorch's headers) into the
+    extension module ``_fast_call``.  Without it (no headers, another compiler)
+    the binding checks and packs in Python: slower calls, the same kernels; so a
+    failure is reported and not raised."""
+    src = os.path.join(CSRC, "fast_call.cpp")
+    if os.path.exists(FAST_CALL) and os.path.getmtime(FAST_CALL) >= max(os.path.getmtime(src), _newest_dep()):
+        return FAST_CALL
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(_cuda_lib_dir()), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for d in inc:
+        cmd += ["-isystem", d]
+    tmp = FAST_CALL + f".tmp{os.getpid()}"
+    lib = os.path.join(root, "lib")
+    cmd += [src, "-o", tmp, "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"fast_call.cpp was not built (calls are checked in Python instead):\n{r.stderr[-2000:]}", file=sys.stderr)
+        return None
+    os.replace(tmp, FAST_CALL)
+    return FAST_CALL
+
+
 def build(verbose: bool = False, extra: list[str] | None = None, trace: bool = False) -> str:
     """Compile every CUDA source and link the shared library; returns its path.
     ``trace=True`` builds the phase-trace variant (``-DMOE_PHASE_TRACE``) into
@@ -64,8 +96,11 @@ def build(verbose: bool = False, extra: list[str] | None = None, trace: bool = F
     os.makedirs(build_dir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = list(extra or []) + (["-DMOE_PHASE_TRACE"] if trace else [])
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        fast = None if trace else ex.submit(build_fast_call)
         objs = list(ex.map(lambda s: _compile(s, extra, build_dir), srcs))
+        if fast is not None:
+            fast.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(lib) or os.path.getmtime(lib) < newest:
         tmp = lib + f".tmp{os.getpid()}"
