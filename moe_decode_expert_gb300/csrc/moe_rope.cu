@@ -9,7 +9,7 @@
 // stays in registers from head to head, and the norm weights go into the
 // rotation's factors: with all of it formed per head the kernel was bound by
 // instructions (284 per head and warp).  8192 tokens of 20 heads of 256, a quarter
-// rotated, per-head norms: 33 us, 75 % of the 6787 GB/s copy (57 us before), of
+// rotated, per-head norms: 31.3 us, 79 % of the 6787 GB/s copy (57 us before), of
 // which the instructions are still about 20.
 //
 // Angles.  a = pos * f.  f / 2pi is formed as a 64-bit binary fraction of a
@@ -91,9 +91,10 @@ inline int64_t r_blocks(const RopeArgs& a, int groups, int share) {
   return (static_cast<int64_t>(a.r.T) + tokens - 1) / tokens;
 }
 
-// LPH lanes per group.
+// LPH lanes per group.  Blocks per SM: seven, 72 registers (8192 tokens: 31.3 us,
+// 35.4 with six); the e4m3 form needs more (777 tokens: 6.3 us with six, 7.4).
 template <int DT, int LPH, bool F8, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, F8 ? 6 : 7) rope_append_kernel(RopeArgs a) {
   __shared__ float2 table[kTableMax];  // [token of the block][frequency]
   const moe_rope_t& r = a.r;
   const int tid = threadIdx.x, lane = tid & 31, c = tid % LPH;
@@ -107,31 +108,60 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
   pdl_launch_dependents();
   pdl_wait();
 
-  // the token's place in the cache
-  int64_t page = -1, off = 0;
-  if (live) {
-    const int64_t s = r.slots[t];
-    if (s >= a.slots) {
-      if (c == 0 && sub == 0 && blockIdx.y == 0) report_error(a.ctrl, kDevBadSlot, static_cast<uint32_t>(t));
-    } else if (s >= 0) {
-      page = a.slots <= 0x7fffffffll ? a.by_page(static_cast<int>(s)) : s / a.c.page_size;
-      off = s - page * a.c.page_size;
-    }
-  }
-  const int ntab = min(tokens, r.T - t0) * half;
-  for (int i = tid; i < ntab; i += kThreads) table[i] = rotation(r.positions[t0 + i / half], r.inv_freq[i % half]);
-  __syncthreads();
-
   // Which of this lane's elements turn, and with which lane's elements (halves).
   const int hc = half >> 3;  // chunks of a half
   const bool turns = PAIRS ? c * 4 < half : c < 2 * hc;
   const int partner = (lane & ~(LPH - 1)) + (PAIRS || !turns ? c : c < hc ? c + hc : c - hc);
   const int pc = partner & (LPH - 1);  // that lane's chunk
+
+  // The next heads, and their kind's norm weights (this chunk's and the
+  // partner's), are loaded while the ones before are worked on; the first ones
+  // before anything else is waited for.  Kinds: 0 queries, 1 keys, 2 values.
+  uint4 next[kAhead], wnext[2];
+  const uint16_t* src = nullptr;
+  auto begin = [&](int kind) {
+    const int r0 = kind == 0 ? 0 : kind == 1 ? hq : hq + hkv, r1 = kind == 0 ? hq : kind == 1 ? hq + hkv : a.heads;
+    const int lo = max(r0, h_lo), hi = min(r1, h_hi);
+    if (lo >= hi) return;
+    const void* in = kind == 0 ? r.q : kind == 1 ? r.k : r.v;
+    const int64_t ts = kind == 0 ? r.q_token_stride : kind == 1 ? r.k_token_stride : r.v_token_stride;
+    const int64_t hs = kind == 0 ? r.q_head_stride : kind == 1 ? r.k_head_stride : r.v_head_stride;
+    const int first = h_lo + (lo - h_lo) / a.share * a.share + sub;
+    src = static_cast<const uint16_t*>(in) + t * ts + (first - r0) * hs + c * 8;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = first + i * a.share;
+      next[i] = make_uint4(0, 0, 0, 0);
+      if (col_in && h >= lo && h < hi) next[i] = ld_ordered16(src);
+      src += a.share * hs;
+    }
+    const uint16_t* w = static_cast<const uint16_t*>(kind == 0 ? r.q_norm_w : r.k_norm_w);
+    if (kind < 2 && w && c * 8 < D) {
+      wnext[0] = ld_ordered16(w + c * 8);
+      wnext[1] = ld_ordered16(w + pc * 8);
+    }
+  };
+  begin(h_lo < hq ? 0 : h_lo < hq + hkv ? 1 : 2);
+  int64_t slot = -1;
+  if (live) asm volatile("ld.global.s64 %0, [%1];" : "=l"(slot) : "l"(r.slots + t) : "memory");
+
+  const int ntab = min(tokens, r.T - t0) * half;
+  for (int i = tid; i < ntab; i += kThreads) table[i] = rotation(r.positions[t0 + i / half], r.inv_freq[i % half]);
+  __syncthreads();
+
+  // the token's place in the cache
+  int64_t page = -1, off = 0;
+  if (slot >= a.slots) {
+    if (c == 0 && sub == 0 && blockIdx.y == 0) report_error(a.ctrl, kDevBadSlot, static_cast<uint32_t>(t));
+  } else if (slot >= 0) {
+    page = a.slots <= 0x7fffffffll ? a.by_page(static_cast<int>(slot)) : slot / a.c.page_size;
+    off = slot - page * a.c.page_size;
+  }
   const float inv_d = __frcp_rn(static_cast<float>(D));
 
-  // Heads r0 .. r1 - 1 of the token's row of heads, of one kind: 0 queries, 1
-  // keys, 2 values.  All groups of a warp make the same number of rounds.
-  auto walk = [&](auto kind, int r0, int r1, const void* in, int64_t in_ts, int64_t in_hs, void* outp, int64_t at,
+  // Heads r0 .. r1 - 1 of the token's row of heads, of one kind.  All groups of a
+  // warp make the same number of rounds.
+  auto walk = [&](auto kind, int r0, int r1, int64_t in_hs, void* outp, int64_t at,
                   int64_t out_hs, bool store, const void* norm_w, const float* scales) {
     constexpr int kKind = decltype(kind)::value;
     constexpr bool kToF8 = F8 && kKind != 0;
@@ -139,7 +169,6 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
     if (lo >= hi) return;
     const int first = h_lo + (lo - h_lo) / a.share * a.share;
     const int64_t step = a.share * in_hs, out_step = a.share * out_hs;
-    const uint16_t* src = static_cast<const uint16_t*>(in) + t * in_ts + (first + sub - r0) * in_hs + c * 8;
     int64_t to = at + (first + sub - r0) * out_hs + c * 8;
     // A turned element is (its own value times ca + its partner's times cb) *
     // 1/rms: the norm weights and the angle's sign go into the factors.
@@ -150,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) ca[j] = wp[j] = 1.0f;
       if (norm_w && in_d) {
-        unpack8<DT>(ld_ordered16(static_cast<const uint16_t*>(norm_w) + c * 8), ca);
-        unpack8<DT>(ld_ordered16(static_cast<const uint16_t*>(norm_w) + pc * 8), wp);
+        unpack8<DT>(wnext[0], ca);
+        unpack8<DT>(wnext[1], wp);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -165,22 +194,21 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
         }
       }
     }
-    // kAhead heads in hand, the next kAhead on their way
-    uint4 raw[kAhead], next[kAhead];
-    auto fetch = [&](int hb) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int h = hb + i * a.share + sub;
-        next[i] = make_uint4(0, 0, 0, 0);
-        if (col_in && h >= lo && h < hi) next[i] = ld_ordered16(src);
-        src += step;
-      }
-    };
-    fetch(first);
+    uint4 raw[kAhead];
     for (int hb = first; hb < hi; hb += kAhead * a.share) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
-      fetch(hb + kAhead * a.share);
+      if (hb + kAhead * a.share < hi) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int h = hb + (kAhead + i) * a.share + sub;
+          next[i] = make_uint4(0, 0, 0, 0);
+          if (col_in && h < hi) next[i] = ld_ordered16(src);
+          src += step;
+        }
+      } else if (kKind < 2) {
+        begin(kKind + 1);
+      }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i, to += out_step) {
         if (hb + i * a.share >= hi) break;  // the same for the whole warp
@@ -238,11 +266,11 @@ __global__ void __launch_bounds__(kThreads, 7) rope_append_kernel(RopeArgs a) {
       }
     }
   };
-  walk(std::integral_constant<int, 0>(), 0, hq, r.q, r.q_token_stride, r.q_head_stride, r.q_out,
+  walk(std::integral_constant<int, 0>(), 0, hq, r.q_head_stride, r.q_out,
        t * r.out_token_stride, r.out_head_stride, true, r.q_norm_w, nullptr);
-  walk(std::integral_constant<int, 1>(), hq, hq + hkv, r.k, r.k_token_stride, r.k_head_stride, a.c.k,
+  walk(std::integral_constant<int, 1>(), hq, hq + hkv, r.k_head_stride, a.c.k,
        page * a.c.k_page_stride + off * a.c.k_token_stride, a.c.k_head_stride, page >= 0, r.k_norm_w, a.c.k_scale);
-  walk(std::integral_constant<int, 2>(), hq + hkv, a.heads, r.v, r.v_token_stride, r.v_head_stride, a.c.v,
+  walk(std::integral_constant<int, 2>(), hq + hkv, a.heads, r.v_head_stride, a.c.v,
        page * a.c.v_page_stride + off * a.c.v_token_stride, a.c.v_head_stride, page >= 0, nullptr, a.c.v_scale);
 }
 
