@@ -134,3 +134,37 @@ def test_no_rows_other_stream_and_graph(m):
     xd.copy_(x2)
     graph.replay()
     _check16(out, norm_ref(x2, wt, None, EPS), torch.bfloat16)
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 7, 9, 15, 17, 31, 33, 255, 257, 263, 1021, 2049, 4099, 9001])
+def test_every_alignment_and_nothing_beside_the_rows(m, H):
+    """Rows that start at each place of an 8-byte word, in tensors whose other
+    elements must not change."""
+    T = 5
+    for off in range(4):
+        for stride in (H + 4 + off, H + 5 + off):
+            x, r, w = _inputs(T, H, torch.bfloat16, H + off)
+            xd = torch.full((T, stride), 9.0, dtype=torch.bfloat16, device=DEV)
+            rd, od, sd = xd.clone(), xd.clone(), xd.clone()
+            wd = torch.zeros(H + off, dtype=torch.bfloat16, device=DEV)
+            xd[:, off:off + H], rd[:, 3 - off:3 - off + H], wd[off:] = x.to(DEV), r.to(DEV), w.to(DEV)
+            out, ro = od[:, 1:1 + H], sd[:, (off + 2) % 4:(off + 2) % 4 + H]
+            m.moe_add_rmsnorm(xd[:, off:off + H], wd[off:], out, residual=rd[:, 3 - off:3 - off + H], residual_out=ro,
+                              eps=EPS)
+            y = norm_ref(x, w, r, EPS)
+            _check16(out, y, torch.bfloat16)
+            assert torch.equal(ro.cpu(), (x.float() + r.float()).to(torch.bfloat16))
+            rest = torch.ones(T, stride, dtype=torch.bool, device=DEV)
+            rest[:, 1:1 + H] = False
+            assert (od[rest] == 9).all()
+            rest[:] = True
+            rest[:, (off + 2) % 4:(off + 2) % 4 + H] = False
+            assert (sd[rest] == 9).all()
+            for b in (off, off + 4):
+                q = torch.full((T, stride + 8), 2.0, device=DEV).to(torch.float8_e4m3fn)
+                s = torch.empty(T, 1, device=DEV)
+                m.moe_add_rmsnorm(xd[:, off:off + H], wd[off:], q[:, b:b + H], residual=rd[:, 3 - off:3 - off + H],
+                                  scales=s, eps=EPS)
+                _check8(q[:, b:b + H].float(), s, y, 0)
+                qf = q.float()
+                assert (qf[:, :b] == 2).all() and (qf[:, b + H:] == 2).all()
