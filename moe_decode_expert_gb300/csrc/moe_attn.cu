@@ -15,6 +15,11 @@ int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Segments up to which teams are the workers: 8 segments of 4k tokens took 16.9 us
 // with teams against 15.4 with CTAs, 2 of 8k tokens 13.3 against 16.9.
 constexpr int kTeamSegments = 4;
+// Up to this many segments have a team each, if the table (or the window) keeps
+// them short enough: 32 of 128 units 12.9 us against 16.8 with CTAs, 16 of 64 units
+// 8.8 against 15.0; 8 of 256 units 15.7 against 15.0.
+constexpr int kTeamsEach = 32;
+constexpr int kTeamsEachUnits = 160;
 
 }  // namespace
 }  // namespace moe
@@ -79,6 +84,11 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.blocks = cache->page_size % 16 == 0;
   g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a->B * static_cast<int64_t>(g.c.n_kv_heads) * g.chunks <= kTeamSegments ? launch_attention_teams(g, nt, st)
-                                                                                 : launch_attention_ctas(g, nt, st);
+  const int64_t segments = static_cast<int64_t>(a->B) * g.c.n_kv_heads * g.chunks;
+  const int fill = 8192 / (padded_dim(cache->head_dim) * static_cast<int>(size));
+  const int unit = fill < 16 ? 16 : fill < 64 ? fill : 64;  // tokens of a team's unit
+  const int most = a->window > 0 && a->window < g.max_len ? a->window : g.max_len;  // tokens of a sequence
+  const bool teams =
+      segments <= kTeamSegments || (segments <= kTeamsEach && most / unit + 2 <= kTeamsEachUnits);
+  return teams ? launch_attention_teams(g, nt, st) : launch_attention_ctas(g, nt, st);
 }

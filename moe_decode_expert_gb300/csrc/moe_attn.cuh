@@ -22,7 +22,8 @@
 // n takes the c-th n-th of it and finds its place from seq_lens itself.  A
 // segment that ends up with several workers is joined by the last of them to
 // arrive, in groups of kJoin parts and then over the groups, always in the same
-// order: one launch, results independent of timing.
+// order: one launch, results independent of timing.  Where every segment is short
+// and has a worker of its own, the line is not cut inside segments.
 //
 // A worker is a CTA, or, where segments are few, a team: a cluster of 8 CTAs whose
 // warps share each segment and sum their outputs through distributed shared
@@ -59,6 +60,11 @@ constexpr int kMaxParts = 64;    // partial results combined at a time
 // Places of the line that a team takes at least (one short sequence in one team:
 // 256 cost 16.3 us where 128 cost 9.4, the two heads then sharing a team).
 constexpr int kTeamMin = 128;
+// Units up to which a segment is left whole where every one has a worker of its own:
+// what a join costs goes into 32 units of a CTA (16 or 48 the same; 64 segments of
+// up to 5 units 9.7 us against 13.8) and 256 of a team.
+constexpr int kWholeCta = 32;
+constexpr int kWholeTeam = 256;
 // Units up to which a segment is one warp's alone (8 made 32 heads over 2 kv heads
 // of ragged 8k tokens 12 % slower; none made 20 short segments 1.7 times slower).
 constexpr int kSolo = 4;
@@ -190,6 +196,8 @@ struct Shape {
   // places of the line a worker takes at least (CTAs: 4 and 6 cost short batches 2
   // us in joins, 16 and 20 2 us in streaming)
   static constexpr int kMinUnits = TEAM ? kTeamMin : 12;
+  // units up to which a segment is left whole where every one has a worker
+  static constexpr int kWhole = TEAM ? kWholeTeam : kWholeCta;
   static constexpr int kBytes = F8 ? 1 : 2;
   static constexpr int kFill = (TEAM || DP > 64 ? 8192 : 4096) / (DP * kBytes);
   static constexpr int kU = kFill < 16 ? 16 : kFill < 64 ? kFill : 64;  // tokens of a unit
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kVoid = S::kVoid, kMinUnits = S::kMinUnits;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
-  __shared__ int s_scan[kWarps], s_b, s_prefix, s_flag;
+  __shared__ int s_scan[kWarps], s_most[kWarps], s_b, s_prefix, s_flag;
 
   const moe_attention_t& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   const int rank = TEAM ? static_cast<int>(cluster_rank()) : 0;
   const int tw = rank * kWarps + warp;
   int my_len = 0, my_u = 0, my_inc = 0;  // a lane's sequence: length, places, places up to its end
-  int sum = 0;
+  int sum = 0, most = 0;  // places of all sequences (before * segs), and of the longest
   if (a.B <= 32) {
     if (lane < a.B) {
       my_len = clamp_len(a.seq_lens[lane]);
@@ -320,28 +328,44 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
       if (lane >= o) my_inc += v;
     }
     sum = __shfl_sync(0xffffffffu, my_inc, 31);
+    most = __reduce_max_sync(0xffffffffu, my_u);
   } else {
-    for (int i = tid; i < a.B; i += kThreads) sum += places(i);
+    for (int i = tid; i < a.B; i += kThreads) {
+      const int u = places(i);
+      sum += u;
+      most = max(most, u);
+    }
     sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) s_scan[warp] = sum;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      s_scan[warp] = sum;
+      s_most[warp] = most;
+    }
     __syncthreads();
     sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += s_scan[w];
+    for (int w = 0; w < kWarps; ++w) {
+      sum += s_scan[w];
+      most = max(most, s_most[w]);
+    }
   }
   Line ln;
   ln.total = sum * segs;
   ln.n = (ln.total + kMinUnits - 1) / kMinUnits;
   // a worker per segment, as long as there are workers: a segment of one unit
   // costs several units' time
-  ln.n = min(max(ln.n, a.B * segs), static_cast<int>(gridDim.x) / S::kTeam);
+  const int fit = static_cast<int>(gridDim.x) / S::kTeam;
+  ln.n = min(max(ln.n, a.B * segs), fit);
+  // Few and short segments: one worker each, with nothing to join.
+  const bool whole_segs = a.B * segs <= fit && most <= kVoid + S::kWhole;
+  if (whole_segs) ln.n = a.B * segs;
   if (worker >= ln.n) return;
   ln.each = static_cast<int>(static_cast<unsigned>(ln.total) / static_cast<unsigned>(ln.n));
   ln.more = ln.total - ln.each * ln.n;
   ln.wide = ln.total;
   ln.small = 1;
   ln.chunks = ln.n;
-  if (!TEAM && ln.each >= kLong) {
+  if (!TEAM && !whole_segs && ln.each >= kLong) {
     ln.each -= static_cast<int>(static_cast<unsigned>(ln.each) * kBack / 100u);
     ln.more = 0;
     ln.wide = ln.each * ln.n;
@@ -511,7 +535,11 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   p = ln.start(cta);
   p_end = ln.start(cta + 1);
   // The sequence that holds p: the one whose places, before * segs, reach it.
-  if (a.B <= 32) {
+  if (whole_segs) {
+    b = cta / segs;
+    prefix = 0;  // places count from the sequence's first
+    len = a.B <= 32 ? __shfl_sync(0xffffffffu, my_len, b) : clamp_len(a.seq_lens[b]);
+  } else if (a.B <= 32) {
     b = 31 - __clz(__ballot_sync(0xffffffffu, my_u > 0 && (my_inc - my_u) * segs <= p));
     prefix = __shfl_sync(0xffffffffu, my_inc - my_u, b);
     len = __shfl_sync(0xffffffffu, my_len, b);
@@ -549,6 +577,10 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   }
   lo = low(len);
   nb = places_of(lo, len);
+  if (whole_segs) {
+    p = (cta - b * segs) * nb;
+    p_end = p + nb;
+  }
   if constexpr (!TEAM) {
     keys = true;
     slot = 0;
