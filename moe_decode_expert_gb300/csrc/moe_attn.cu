@@ -88,7 +88,8 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   const int fill = 8192 / (padded_dim(cache->head_dim) * static_cast<int>(size));
   const int unit = fill < 16 ? 16 : fill < 64 ? fill : 64;  // tokens of a team's unit
   const int most = a->window > 0 && a->window < g.max_len ? a->window : g.max_len;  // tokens of a sequence
-  const bool teams =
-      segments <= kTeamSegments || (segments <= kTeamsEach && most / unit + 2 <= kTeamsEachUnits);
+  // (two tiles of heads at 256 leave room for one CTA per SM and 15 teams)
+  const int64_t each = nt == 2 && cache->head_dim > 128 ? 12 : kTeamsEach;
+  const bool teams = segments <= kTeamSegments || (segments <= each && most / unit + 2 <= kTeamsEachUnits);
   return teams ? launch_attention_teams(g, nt, st) : launch_attention_ctas(g, nt, st);
 }
