@@ -215,9 +215,12 @@ template <int DT, int OUT>
 moe_status_t dispatch(const moe_norm_t& n, bool wide, cudaStream_t st) {
   if (!wide) {
     if constexpr (OUT != kOutGroup) {
-      // A warp per narrow row (11874 x 115: 12.8 us with a CTA each).
+      // A warp per narrow row (11874 x 115: 3.5 us, 12.4 with a CTA each), up to 256
+      // elements where rows are many (11874 x 203: 5.3 us against 12.4, but 300 x 203:
+      // 2.6 against 2.2); at 333 a warp is no faster.
       if (n.H <= 4 * 32) return launch<DT, 1, 4, OUT, true>(n, 128, st);
-      if (n.H <= 16 * 32) return launch<DT, 1, 16, OUT, true>(n, 128, st);
+      if (n.H <= 8 * 32 && n.T >= 4 * sm_count())
+        return launch<DT, 1, 8, OUT, true>(n, 128, st);
       // Rows of single elements: few per thread while rows are few (65 x 6221: 3.9
       // us with 8, 5.3 with 16), more once rows fill the SMs, whose registers
       // then hold more rows at a time (9537 x 6221: 137 us with 16, 202 with 8).

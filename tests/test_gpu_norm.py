@@ -168,3 +168,18 @@ def test_every_alignment_and_nothing_beside_the_rows(m, H):
                 _check8(q[:, b:b + H].float(), s, y, 0)
                 qf = q.float()
                 assert (qf[:, :b] == 2).all() and (qf[:, b + H:] == 2).all()
+
+
+@pytest.mark.parametrize("H", [3, 127, 129, 203, 255, 257])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_narrow_rows(m, H, e4m3):
+    T = 5003  # more rows than the SMs hold warps' rows at a time, and no multiple of a CTA's
+    x, r, w = _inputs(T, H, torch.float16, H)
+    y = norm_ref(x, w, r, EPS)
+    out = torch.empty(T, H, dtype=torch.float8_e4m3fn if e4m3 else torch.float16, device=DEV)
+    s = torch.empty(T, 1, device=DEV) if e4m3 else None
+    m.moe_add_rmsnorm(x.to(DEV), w.to(DEV), out, residual=r.to(DEV), scales=s, eps=EPS)
+    if e4m3:
+        _check8(out.float(), s, y, 0)
+    else:
+        _check16(out, y, torch.float16)
