@@ -20,6 +20,12 @@ constexpr int kTeamSegments = 4;
 // 8.8 against 15.0; 8 of 256 units 15.7 against 15.0.
 constexpr int kTeamsEach = 32;
 constexpr int kTeamsEachUnits = 160;
+// Groups of more than 8 heads whose segments are few and short are split into one
+// tile of heads each, up to this many segments: 7 windows of 76 over 64 heads of 256
+// 7.6 us against 12.9, 70 sequences of 100 over 32 e4m3 heads of 128 6.9 against
+// 8.8; 300 of 60 stay (7.4 us, 11.7 as 600).
+constexpr int kSplit = 304;
+constexpr int kSplitUnits = 32;
 
 }  // namespace
 }  // namespace moe
@@ -65,7 +71,7 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.a = *a;
   g.ws = static_cast<uint8_t*>(ws);
   g.group = a->n_q_heads / cache->n_kv_heads;
-  const int nt = n_tiles(g.group);
+  int nt = n_tiles(g.group);
   g.chunks = (g.group + 8 * nt - 1) / (8 * nt);
   g.hpc = (g.group + g.chunks - 1) / g.chunks;
   // Tokens are 32-bit numbers; units round a length up by less than 64.
@@ -84,12 +90,24 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.blocks = cache->page_size % 16 == 0;
   g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t segments = static_cast<int64_t>(a->B) * g.c.n_kv_heads * g.chunks;
+  int64_t segments = static_cast<int64_t>(a->B) * g.c.n_kv_heads * g.chunks;
   const int fill = 8192 / (padded_dim(cache->head_dim) * static_cast<int>(size));
   const int unit = fill < 16 ? 16 : fill < 64 ? fill : 64;  // tokens of a team's unit
+  // the same of a CTA's unit
+  const int cta_fill = padded_dim(cache->head_dim) <= 64 ? fill / 2 : fill;
+  const int cta_unit = cta_fill < 16 ? 16 : cta_fill < 64 ? cta_fill : 64;
   const int most = a->window > 0 && a->window < g.max_len ? a->window : g.max_len;  // tokens of a sequence
   // (two tiles of heads at 256 leave room for one CTA per SM and 15 teams)
-  const int64_t each = nt == 2 && cache->head_dim > 128 ? 12 : kTeamsEach;
+  int64_t each = nt == 2 && cache->head_dim > 128 ? 12 : kTeamsEach;
+  // (not where that takes segments their teams: 18 of 300 tokens 7.0 us, 36 8.1 with CTAs)
+  if (nt == 2 && 2 * segments <= kSplit && most / cta_unit + 2 <= kSplitUnits &&
+      (segments > each || 2 * segments <= kTeamsEach)) {
+    nt = 1;
+    g.chunks = (g.group + 7) / 8;
+    g.hpc = (g.group + g.chunks - 1) / g.chunks;
+    each = kTeamsEach;
+    segments = static_cast<int64_t>(a->B) * g.c.n_kv_heads * g.chunks;
+  }
   const bool teams = segments <= kTeamSegments || (segments <= each && most / unit + 2 <= kTeamsEachUnits);
   return teams ? launch_attention_teams(g, nt, st) : launch_attention_ctas(g, nt, st);
 }

@@ -68,6 +68,8 @@ constexpr int kWholeTeam = 256;
 // Units up to which a segment is one warp's alone (8 made 32 heads over 2 kv heads
 // of ragged 8k tokens 12 % slower; none made 20 short segments 1.7 times slower).
 constexpr int kSolo = 4;
+// ... and where each has a CTA anyway (35 of up to 7 units 5.5 us, 6.6 with 2 and 8.6 with 4).
+constexpr int kSoloWhole = 1;
 // A line of kLong places per CTA and more keeps kBack per cent of them back for the
 // CTAs that get done first: 327 to 320 us at 438 places per CTA; at 117 places the
 // extra joins cost more than the balance gains (98 to 103 us).
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   auto mine = [&](int sidx, int places_of_seg, int ub, int ue, int& u, int& end, int& step) {
     const int u0 = max(ub - kVoid, 0);
     end = ue - kVoid;
-    if (!TEAM && places_of_seg <= kVoid + kSolo && u0 == 0 && ue == places_of_seg) {
+    if (!TEAM && places_of_seg <= kVoid + (whole_segs ? kSoloWhole : kSolo) && u0 == 0 && ue == places_of_seg) {
       u = 0;
       step = 1;
       if ((sidx & (kWarps - 1)) != warp) end = 0;
