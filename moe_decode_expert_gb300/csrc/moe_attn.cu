@@ -9,9 +9,14 @@ moe_status_t launch_attention_ctas(const AttnArgs& g, int nt, cudaStream_t st) {
 
 namespace {
 
-// n tiles of 8 heads of a segment: two when a group has more than 8 heads.
-int n_tiles(int group) { return group > 8 ? 2 : 1; }
 int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// n tiles of 8 heads of a segment: two when a group has more than 8 heads, but one
+// for rows of more than 128 elements, where two leave no room for a second CTA on
+// an SM; there the tiles' lines lie side by side and read the rows at about the
+// same time, the later ones from L2 (32 heads over 2 of 256: 4 sequences of up to
+// 8k tokens 25 us against 48, 64 of them 143 against 142; rows of 96, 53 sequences
+// of 16k: 154 against 126).
+int n_tiles(int group, int dp) { return group > 8 && dp <= 128 ? 2 : 1; }
 // Segments up to which teams are the workers: 8 segments of 4k tokens took 16.9 us
 // with teams against 15.4 with CTAs, 2 of 8k tokens 13.3 against 16.9.
 constexpr int kTeamSegments = 4;
@@ -36,8 +41,7 @@ extern "C" size_t moe_attention_workspace_bytes(const moe_kv_cache_t* cache, int
   if (!cache || cache->n_kv_heads < 1 || cache->head_dim < 1 || cache->head_dim > 256 || n_q_heads < 1 ||
       n_q_heads % cache->n_kv_heads)
     return 0;
-  const int nt = n_tiles(n_q_heads / cache->n_kv_heads);
-  const int dp = padded_dim(cache->head_dim);
+  const int dp = padded_dim(cache->head_dim), nt = n_tiles(n_q_heads / cache->n_kv_heads, dp);
   // up to four CTAs per SM at head_dim <= 64, else two
   const size_t chunks = dp > 64 ? kMaxChunks / 2 : kMaxChunks;
   return kPartsAt + chunks * 2 * 8 * nt * dp * sizeof(float);
@@ -71,13 +75,11 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.a = *a;
   g.ws = static_cast<uint8_t*>(ws);
   g.group = a->n_q_heads / cache->n_kv_heads;
-  int nt = n_tiles(g.group);
-  g.chunks = (g.group + 8 * nt - 1) / (8 * nt);
-  g.hpc = (g.group + g.chunks - 1) / g.chunks;
+  const int tiles = (g.group + 7) / 8, dp = padded_dim(cache->head_dim);
   // Tokens are 32-bit numbers; units round a length up by less than 64.
   const int64_t cap = static_cast<int64_t>(a->max_pages) * cache->page_size;
   // The line of units is counted in 32 bits.
-  if (cap / 16 + 2 + 4 > 0x7fffffffll / g.chunks / cache->n_kv_heads / a->B)
+  if (cap / 16 + 2 + 4 > 0x7fffffffll / tiles / cache->n_kv_heads / a->B)
     return set_error(MOE_ERR_UNSUPPORTED, "batch * kv heads * table tokens too large");
   g.by_page = FastDiv(cache->page_size);
   const int64_t size = cache->dtype == MOE_E4M3 ? 1 : 2;
@@ -90,24 +92,24 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.blocks = cache->page_size % 16 == 0;
   g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int64_t segments = static_cast<int64_t>(a->B) * g.c.n_kv_heads * g.chunks;
-  const int fill = 8192 / (padded_dim(cache->head_dim) * static_cast<int>(size));
+  const int fill = 8192 / (dp * static_cast<int>(size));
   const int unit = fill < 16 ? 16 : fill < 64 ? fill : 64;  // tokens of a team's unit
   // the same of a CTA's unit
-  const int cta_fill = padded_dim(cache->head_dim) <= 64 ? fill / 2 : fill;
+  const int cta_fill = dp <= 64 ? fill / 2 : fill;
   const int cta_unit = cta_fill < 16 ? 16 : cta_fill < 64 ? cta_fill : 64;
   const int most = a->window > 0 && a->window < g.max_len ? a->window : g.max_len;  // tokens of a sequence
-  // (two tiles of heads at 256 leave room for one CTA per SM and 15 teams)
-  int64_t each = nt == 2 && cache->head_dim > 128 ? 12 : kTeamsEach;
+  int nt = n_tiles(g.group, dp), chunks = (tiles + nt - 1) / nt;
+  const int64_t kv = static_cast<int64_t>(a->B) * g.c.n_kv_heads;
   // (not where that takes segments their teams: 18 of 300 tokens 7.0 us, 36 8.1 with CTAs)
-  if (nt == 2 && 2 * segments <= kSplit && most / cta_unit + 2 <= kSplitUnits &&
-      (segments > each || 2 * segments <= kTeamsEach)) {
+  if (nt == 2 && kv * tiles <= kSplit && most / cta_unit + 2 <= kSplitUnits &&
+      (kv * chunks > kTeamsEach || kv * tiles <= kTeamsEach)) {
     nt = 1;
-    g.chunks = (g.group + 7) / 8;
-    g.hpc = (g.group + g.chunks - 1) / g.chunks;
-    each = kTeamsEach;
-    segments = static_cast<int64_t>(a->B) * g.c.n_kv_heads * g.chunks;
+    chunks = tiles;
   }
-  const bool teams = segments <= kTeamSegments || (segments <= each && most / unit + 2 <= kTeamsEachUnits);
+  g.hpc = (g.group + chunks - 1) / chunks;
+  const int64_t segments = kv * chunks;
+  const bool teams = segments <= kTeamSegments || (segments <= kTeamsEach && most / unit + 2 <= kTeamsEachUnits);
+  g.sides = !teams && nt == 1 && chunks <= kMaxSides ? chunks : 1;
+  g.chunks = chunks / g.sides;
   return teams ? launch_attention_teams(g, nt, st) : launch_attention_ctas(g, nt, st);
 }

@@ -25,6 +25,10 @@
 // order: one launch, results independent of timing.  Where every segment is short
 // and has a worker of its own, the line is not cut inside segments.
 //
+// Head chunks of a kv head beyond the first are further segments, or, up to
+// kMaxSides of them, lines of their own side by side (blockIdx.y), on which as many
+// workers read the same rows at about the same time.
+//
 // A worker is a CTA, or, where segments are few, a team: a cluster of 8 CTAs whose
 // warps share each segment and sum their outputs through distributed shared
 // memory, which spares a short sequence the join through global memory (1531
@@ -56,6 +60,7 @@ constexpr int kSmallPer = 2;     // small chunks per CTA of a long line
 constexpr int kMaxChunks = kMaxCtas * (1 + kSmallPer);  // partial slots in the workspace: two per chunk
 constexpr int kTeamCtas = 8;     // CTAs of a team (a cluster), and the most teams
 constexpr int kMaxTeams = 40;
+constexpr int kMaxSides = 8;     // lines side by side
 constexpr int kMaxParts = 64;    // partial results combined at a time
 // Places of the line that a team takes at least (one short sequence in one team:
 // 256 cost 16.3 us where 128 cost 9.4, the two heads then sharing a team).
@@ -99,7 +104,8 @@ struct AttnArgs {
   moe_kv_cache_t c;
   moe_attention_t a;
   uint8_t* ws;
-  int32_t chunks;  // head chunks of a kv head
+  int32_t chunks;  // head chunks of a kv head on a line
+  int32_t sides;   // lines side by side, one per further head chunk
   int32_t hpc;     // query heads of a chunk (<= 8 * NT)
   int32_t group;   // query heads of a kv head
   int32_t max_len; // max_pages * page_size, saturated
@@ -354,6 +360,8 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   Line ln;
   ln.total = sum * segs;
   ln.n = (ln.total + kMinUnits - 1) / kMinUnits;
+  // This line's slots and counters.
+  const int at0 = static_cast<int>(blockIdx.y * gridDim.x) * (1 + kSmallPer);
   // a worker per segment, as long as there are workers: a segment of one unit
   // costs several units' time
   const int fit = static_cast<int>(gridDim.x) / S::kTeam;
@@ -599,8 +607,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     const int seg_start = p - ub;
     if (ue <= kVoid) break;  // the share ends before the segment's first unit: it is the next CTA's
     const int kvh = g.chunks == 1 ? seg : seg / g.chunks, chunk = seg - kvh * g.chunks;
-    const int heads = min(g.hpc, g.group - chunk * g.hpc);  // query heads of this segment
-    const int h0 = kvh * g.group + chunk * g.hpc;
+    const int h_in = (chunk * g.sides + static_cast<int>(blockIdx.y)) * g.hpc;
+    const int heads = min(g.hpc, g.group - h_in);  // query heads of this segment
+    const int h0 = kvh * g.group + h_in;
     if constexpr (TEAM) {
       keys = true;
       slot = 0;
@@ -897,7 +906,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     const bool split = ub > kVoid || ue < nb;
     constexpr int kQuads = DP / 4;
     const int part = cta - (split ? ln.owner(seg_start + kVoid) : cta);
-    const int my_slot = cta * 2 + (part == 0 ? 1 : 0);
+    const int my_slot = (at0 + cta) * 2 + (part == 0 ? 1 : 0);
     // this CTA's share of the segment's column quads, and the heads it touches
     const int all = heads * kQuads, per = TEAM ? (all + S::kTeam - 1) / S::kTeam : all;
     const int e_lo = min(rank * per, all), e_hi = min(e_lo + per, all);
@@ -1122,8 +1131,8 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
 
     // --------------------------------------- parts of other workers join
     if (split) {
-      const int first = cta - part;  // the segment's first worker
-      const int n_parts = ln.owner(seg_start + nb - 1) - first + 1;
+      const int first = at0 + cta - part;  // the segment's first worker's slots
+      const int n_parts = ln.owner(seg_start + nb - 1) + at0 - first + 1;
       // Arrive at a counter; true for the whole CTA if it is the last of n.
       // (release and acquire by one thread; the barriers extend them to the CTA)
       auto arrive = [&](uint32_t* counter, int n) {
@@ -1174,11 +1183,11 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
   if (TEAM || ln.chunks == ln.n) break;
   // the next small chunk, if any is left; the last CTA to find none clears the count
   __syncthreads();
-  if (tid == 0) s_flag = ln.n + static_cast<int>(atomicAdd(counters + kMaxChunks * 4, 1u));
+  if (tid == 0) s_flag = ln.n + static_cast<int>(atomicAdd(counters + kMaxChunks * 4 + blockIdx.y, 1u));
   __syncthreads();
   cta = s_flag;
   if (cta >= ln.chunks) {
-    if (tid == 0 && cta == ln.chunks + ln.n - 1) counters[kMaxChunks * 4] = 0u;
+    if (tid == 0 && cta == ln.chunks + ln.n - 1) counters[kMaxChunks * 4 + blockIdx.y] = 0u;
     break;
   }
   }
@@ -1221,7 +1230,7 @@ moe_status_t launch(const AttnArgs& g, cudaStream_t st) {
     }
     grid_of[dev].store(grid, std::memory_order_release);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid / g.sides), static_cast<unsigned>(g.sides));
   cfg.numAttrs = TEAM ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, g) != cudaSuccess) return check_launch("paged_attention_kernel");
   stat_kernels(1);
@@ -1236,9 +1245,7 @@ moe_status_t pick(const AttnArgs& g, int nt, cudaStream_t st) {
     if (D <= 128) return launch<QT, F8, 128, 1, TEAM>(g, st);
     return launch<QT, F8, 256, 1, TEAM>(g, st);
   }
-  if (D <= 64) return launch<QT, F8, 64, 2, TEAM>(g, st);
-  if (D <= 128) return launch<QT, F8, 128, 2, TEAM>(g, st);
-  return launch<QT, F8, 256, 2, TEAM>(g, st);
+  return D <= 64 ? launch<QT, F8, 64, 2, TEAM>(g, st) : launch<QT, F8, 128, 2, TEAM>(g, st);
 }
 
 template <bool TEAM>

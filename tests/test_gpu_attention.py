@@ -327,3 +327,66 @@ def test_a_line_long_enough_to_keep_some_back(m):
             assert (d <= rounded(ref, torch.bfloat16, 0.0, err)).all()
             tol = ds[:, 0] + length * 2.0 ** -24 + 2.0 ** -22 * total.abs() + 2.0 ** -20
             assert ((outs[0][1][b, 2 * h:2 * h + 2].double() - total).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(9, 1), (16, 1), (17, 1), (33, 1), (64, 1), (72, 1), (40, 2)])
+def test_wide_rows_with_their_heads_on_several_lines(m, hq, hkv, e4m3):
+    """Groups of more than 8 heads of 256, up to 8 lines and past them."""
+    c = Case(m, [2700, 31, 0, 517], hq, hkv, 256, 16, torch.float16, e4m3)
+    first, _ = c.check()
+    again, _ = c.run(ws=c.ws)
+    assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D,hq,hkv", [(64, 24, 2), (128, 40, 4), (256, 12, 1), (256, 64, 4), (96, 8, 8)])
+def test_short_segments_with_a_cta_each(m, D, hq, hkv, e4m3):
+    lens = [76, 0, 1, 16, 17, 33, 64, 65, 100, 76, 5, 48, 49, 31, 32, 128, 90, 3]
+    c = Case(m, lens, hq, hkv, D, 16, e4m3=e4m3)
+    c.check()
+    c.check(window=20)
+
+
+def test_long_lines_side_by_side(m):
+    """Over 256 units per CTA on each of two lines."""
+    lens = [110000, 108001, 105003]
+    page, hkv, G, D = 16, 2, 12, 256
+    need = [-(-n // page) for n in lens]
+    g = torch.Generator(device=DEV).manual_seed(6)
+    k, v = (torch.randn(sum(need), page, hkv, D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    order = torch.randperm(sum(need), generator=g, device=DEV).to(torch.int32)
+    table = torch.full((3, max(need)), -1, dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    q = (torch.randn(3, G * hkv, D, generator=g, device=DEV) * 1.5).to(torch.bfloat16)
+    cache = m.MoeKvCache(k, v)
+    ws = m.alloc_attention_workspace(cache, G * hkv)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    outs = []
+    for _ in range(3):
+        out, lse = torch.empty_like(q), torch.empty(3, G * hkv, device=DEV)
+        m.moe_paged_attention(cache, q, table, n, out, ws, lse=lse)
+        outs.append((out, lse))
+    m.moe_query_status(ws)
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+    for b, length in enumerate(lens):
+        pos = torch.arange(length, device=DEV)
+        pages, off = table[b].long()[pos // page], pos % page
+        for h in range(hkv):
+            kh, vh = k[pages, off, h].double(), v[pages, off, h].double()
+            mine = slice(G * h, G * h + G)
+            qh = q[b, mine].double()
+            s = qh @ kh.T * D ** -0.5
+            total = torch.logsumexp(s, 1)
+            p = torch.exp(s - total[:, None])
+            ref = p @ vh
+            ds = 2.0 ** -17 * D ** -0.5 * (qh.abs() @ kh.abs().T).amax(1, keepdim=True) + 2.0 ** -20
+            err = (2 * ds + 2.0 ** -17 + (length / 16 + 16) * 2.0 ** -22) * (p @ vh.abs())
+            d = (outs[0][0][b, mine].double() - ref).abs()
+            assert (d <= rounded(ref, torch.bfloat16, 0.0, err)).all()
+            tol = ds[:, 0] + length * 2.0 ** -24 + 2.0 ** -22 * total.abs() + 2.0 ** -20
+            assert ((outs[0][1][b, mine].double() - total).abs() <= tol).all()
