@@ -42,9 +42,7 @@ extern "C" size_t moe_attention_workspace_bytes(const moe_kv_cache_t* cache, int
       n_q_heads % cache->n_kv_heads)
     return 0;
   const int dp = padded_dim(cache->head_dim), nt = n_tiles(n_q_heads / cache->n_kv_heads, dp);
-  // up to four CTAs per SM at head_dim <= 64, else two
-  const size_t chunks = dp > 64 ? kMaxChunks / 2 : kMaxChunks;
-  return kPartsAt + chunks * 2 * 8 * nt * dp * sizeof(float);
+  return kPartsAt + static_cast<size_t>(max_chunks(dp)) * 2 * 8 * nt * dp * sizeof(float);
 }
 
 extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws,
@@ -109,7 +107,9 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.hpc = (g.group + chunks - 1) / chunks;
   const int64_t segments = kv * chunks;
   const bool teams = segments <= kTeamSegments || (segments <= kTeamsEach && most / unit + 2 <= kTeamsEachUnits);
-  g.sides = !teams && nt == 1 && chunks <= kMaxSides ? chunks : 1;
+  // (48 heads over 1 of 128, 64 sequences of up to 32k tokens: 243 us, 292 with the
+  // chunks' segments one after the other on one line)
+  g.sides = !teams && chunks <= kMaxSides ? chunks : 1;
   g.chunks = chunks / g.sides;
   return teams ? launch_attention_teams(g, nt, st) : launch_attention_ctas(g, nt, st);
 }

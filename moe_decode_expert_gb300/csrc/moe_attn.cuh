@@ -58,6 +58,8 @@ constexpr int kMaxSms = 160;     // SMs that a launch fills
 constexpr int kMaxCtas = 4 * kMaxSms;
 constexpr int kSmallPer = 2;     // small chunks per CTA of a long line
 constexpr int kMaxChunks = kMaxCtas * (1 + kSmallPer);  // partial slots in the workspace: two per chunk
+// Chunks of all lines of a launch: four CTAs an SM at head_dim <= 64, else two.
+constexpr int max_chunks(int dp) { return dp > 64 ? kMaxChunks / 2 : kMaxChunks; }
 constexpr int kTeamCtas = 8;     // CTAs of a team (a cluster), and the most teams
 constexpr int kMaxTeams = 40;
 constexpr int kMaxSides = 8;     // lines side by side
@@ -213,6 +215,7 @@ struct Shape {
   static constexpr int kHeads = 8 * NT;
   // parts joined at a time: kMaxParts groups hold every chunk of a launch
   static constexpr int kJoin = DP > 64 ? 32 : 64;
+  static_assert(kCtas * kMaxSms * (1 + kSmallPer) <= max_chunks(DP), "every chunk has its slots in the workspace");
   static_assert(kJoin <= kMaxParts && kCtas * kMaxSms * (1 + kSmallPer) <= kJoin * kMaxParts, "two levels of joins do");
   static constexpr int kRow = DP * kBytes;                                            // bytes of a row
   static constexpr int kSlot = kU * kRow;

@@ -390,3 +390,15 @@ def test_long_lines_side_by_side(m):
             assert (d <= rounded(ref, torch.bfloat16, 0.0, err)).all()
             tol = ds[:, 0] + length * 2.0 ** -24 + 2.0 ** -22 * total.abs() + 2.0 ** -20
             assert ((outs[0][1][b, mine].double() - total).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(20, 1), (64, 1), (34, 2), (144, 1)])
+def test_groups_of_several_chunks_in_a_wide_table(m, D, hq, hkv, e4m3):
+    """Chunks of 16 heads on lines side by side; a table wide enough that the
+    sequences are not known to be short."""
+    c = Case(m, [1200, 31, 0, 517, 64, 3], hq, hkv, D, 64, torch.float16, e4m3, max_pages=400)
+    first, _ = c.check()
+    again, _ = c.run(ws=c.ws)
+    assert torch.equal(first, again)
