@@ -11,7 +11,7 @@
 // floats, with NaN above infinity, so a NaN reaches the row's scale.
 //
 // HBM bounds it: 16384 rows of 4096 with residual to e4m3 groups of 128 take 76 us,
-// 91 % of the 6787 GB/s copy; 16384 x 2048 in bf16 39.5 us (100 %).
+// 91 % of the 6787 GB/s copy; 16384 x 2048 in bf16 39.5 us (100 %), 2047 43 (91 %).
 
 #include <cuda_fp8.h>
 
@@ -52,15 +52,47 @@ __device__ __forceinline__ float reciprocal(float s) {
 }
 
 // Threads of a block at most: rows of one or two vectors per thread take
-// kThreads, of four or eight 512, scalar ones 1024 (512 with 16 elements each).
+// kThreads, of four or eight 512, pairs and scalar ones 1024 (eight pairs 512).
 // 256 threads leave an SM more rows in flight than 512 (16384 x 4096 e4m3: 76 us
 // against 89); a warp per row needs no barrier (16384 x 512: 11.4 us against 16.9).
 constexpr int kThreads = 256;
 constexpr int kWarpVecs = 128;  // rows of up to this many vectors: a warp each
 template <int VEC, int NV>
-constexpr int kMaxThreads = VEC == 1 ? (NV == 16 ? 512 : 1024) : NV < 4 ? kThreads : 512;
+constexpr int kMaxThreads = VEC == 1 ? 1024 : VEC == 2 ? (NV == 8 ? 512 : 1024) : NV < 4 ? kThreads : 512;
 
-// VEC elements (8: one 16-byte load, 1: any alignment) NV times per thread.
+// A row's pairs of one tensor: as 4-byte words where `like` (they lie on word
+// boundaries), else as two elements each.  Branches are uniform and hold nothing
+// that waits for a load: with a choice per pair, converted there, 9537 rows of 6221
+// took 229 us, with single elements 136, so 103.
+template <int NV>
+struct Pairs {
+  uint32_t lo[NV], hi[NV];
+  __device__ __forceinline__ void load(const uint16_t* p, bool like, int c, int step, int H) {
+    if (like) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        lo[v] = hi[v] = 0u;
+        if (c + v * step + 1 < H) lo[v] = *reinterpret_cast<const uint32_t*>(p + c + v * step);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        lo[v] = hi[v] = 0u;
+        if (c + v * step + 1 < H) {
+          lo[v] = p[c + v * step];
+          hi[v] = p[c + v * step + 1];
+        }
+      }
+    }
+  }
+  template <int DT>
+  __device__ __forceinline__ float2 get(int v) const {
+    return unpack2<DT>(lo[v] | (hi[v] << 16));
+  }
+};
+
+// VEC elements (8: one 16-byte load; 2: a pair, at any alignment; 1: any
+// alignment) NV times per thread.
 // WARP: a warp per row; else a CTA per row.
 template <int DT, int VEC, int NV, int OUT, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel(moe_norm_t a) {
@@ -78,6 +110,15 @@ __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel
   const uint16_t* w = static_cast<const uint16_t*>(a.weight);
   uint16_t* ro = static_cast<uint16_t*>(a.residual_out) + row * a.residual_out_stride;
   const bool res = a.residual != nullptr, res_out = a.residual_out != nullptr;
+
+  // Pairs begin where x has a word boundary: at column `early`.  What they leave,
+  // column 0 or the last one, is one thread's extra element.
+  const auto at = [](const void* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)); };
+  const auto like_x = [&](const void* p) { return ((at(x) ^ at(p)) & 2u) == 0; };
+  const int early = VEC == 2 ? (at(x) >> 1) & 1 : 0;
+  [[maybe_unused]] const int c0 = early + 2 * tid, step = 2 * nthr;
+  [[maybe_unused]] const int extra = tid == 0 && early ? 0 : tid == nthr - 1 && ((a.H - early) & 1) ? a.H - 1 : -1;
+  [[maybe_unused]] float hx = 0.0f;
 
   float h[NV * VEC];
   [[maybe_unused]] uint4 wv[VEC == 8 ? NV : 1];  // weights stay packed
@@ -101,6 +142,23 @@ __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[v * 8 + j] = res ? xf[j] + rf[j] : xf[j];
     }
+  } else if constexpr (VEC == 2) {
+    Pairs<NV> xp, rp;
+    xp.load(x, true, c0, step, a.H);
+    if (res) rp.load(r, like_x(r), c0, step, a.H);
+    if (extra >= 0) {
+      hx = load_scalar<DT>(x, extra);
+      if (res) hx += load_scalar<DT>(r, extra);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float2 p = xp.template get<DT>(v);
+      if (res) {
+        const float2 q = rp.template get<DT>(v);
+        p.x += q.x, p.y += q.y;
+      }
+      h[2 * v] = p.x, h[2 * v + 1] = p.y;
+    }
   } else {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -117,7 +175,17 @@ __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel
   uint32_t mx = 0u;
 #pragma unroll
   for (int i = 0; i < NV * VEC; ++i) sum = fmaf(h[i], h[i], sum);
-  if (OUT == kOutRow) {
+  if constexpr (VEC == 2) sum = fmaf(hx, hx, sum);
+  [[maybe_unused]] Pairs<VEC == 2 ? NV : 1> wp;
+  if constexpr (VEC == 2 && OUT == kOutRow) {
+    wp.load(w, like_x(w), c0, step, a.H);
+    if (extra >= 0) mx = __float_as_uint(hx * load_scalar<DT>(w, extra)) & 0x7fffffffu;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const float2 p = wp.template get<DT>(v);
+      mx = max(mx, max(__float_as_uint(h[2 * v] * p.x) & 0x7fffffffu, __float_as_uint(h[2 * v + 1] * p.y) & 0x7fffffffu));
+    }
+  } else if (OUT == kOutRow) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float w8[VEC];
@@ -150,6 +218,60 @@ __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel
 
   uint8_t* o8 = static_cast<uint8_t*>(a.out) + row * a.out_stride;
   uint16_t* o16 = static_cast<uint16_t*>(a.out) + row * a.out_stride;
+  if constexpr (VEC == 2) {
+    // A row's pairs out again, u(v) of pair v.
+    const auto store = [&](uint16_t* p, auto u) {
+      if (like_x(p)) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const float2 q = u(v);
+          if (c0 + v * step + 1 < a.H) *reinterpret_cast<uint32_t*>(p + c0 + v * step) = pack2(DT, q.x, q.y);
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const float2 q = u(v);
+          if (c0 + v * step + 1 < a.H) {
+            store_out(p, c0 + v * step, q.x, DT);
+            store_out(p, c0 + v * step + 1, q.y, DT);
+          }
+        }
+      }
+    };
+    // (for 16-bit outputs the weights are loaded only now, from L1: beside x and r their
+    // loads delayed those, 16384 x 2047 in single elements 133 us against 73)
+    if constexpr (OUT == kOutSame) wp.load(w, like_x(w), c0, step, a.H);
+    if (res_out) store(ro, [&](int v) { return make_float2(h[2 * v], h[2 * v + 1]); });
+    const auto y = [&](int v) {
+      const float2 p = wp.template get<DT>(v);
+      return make_float2(h[2 * v] * rstd * p.x, h[2 * v + 1] * rstd * p.y);
+    };
+    if (extra >= 0) {
+      const float ye = hx * rstd * load_scalar<DT>(w, extra);
+      if (res_out) store_out(ro, extra, hx, DT);
+      if (OUT == kOutSame) store_out(o16, extra, ye, DT);
+      else o8[extra] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(ye * inv, __NV_SATFINITE, __NV_E4M3));
+    }
+    if constexpr (OUT == kOutSame) {
+      store(o16, y);
+    } else {
+      const bool even = ((at(o8) + early) & 1u) == 0;  // pairs of bytes on 2-byte boundaries
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const float2 q = y(v);
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q.x * inv, q.y * inv), __NV_SATFINITE, __NV_E4M3);
+        uint8_t* o = o8 + c0 + v * step;
+        if (c0 + v * step + 1 < a.H) {
+          if (even) {
+            *reinterpret_cast<uint16_t*>(o) = static_cast<uint16_t>(two);
+          } else {
+            o[0] = static_cast<uint8_t>(two);
+            o[1] = static_cast<uint8_t>(two >> 8);
+          }
+        }
+      }
+    }
+  } else {
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     if constexpr (VEC == 8) {
@@ -188,8 +310,7 @@ __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel
     } else {
       const int c = v * nthr + tid;
       if (c < a.H) {
-        // The weight comes from L1 again: held in registers beside x and r, its
-        // loads delayed theirs (16384 x 2047: 133 us against 73).
+        // the weight comes from L1 again, as above
         const float y = h[v] * rstd * load_scalar<DT>(w, c);
         if (res_out) store_out(ro, c, h[v], DT);
         if (OUT == kOutSame)
@@ -198,6 +319,7 @@ __global__ void __launch_bounds__(WARP ? 128 : kMaxThreads<VEC, NV>) norm_kernel
           o8[c] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3));
       }
     }
+  }
   }
 }
 
@@ -215,19 +337,20 @@ template <int DT, int OUT>
 moe_status_t dispatch(const moe_norm_t& n, bool wide, cudaStream_t st) {
   if (!wide) {
     if constexpr (OUT != kOutGroup) {
-      // A warp per narrow row (11874 x 115: 3.5 us, 12.4 with a CTA each), up to 256
-      // elements where rows are many (11874 x 203: 5.3 us against 12.4, but 300 x 203:
-      // 2.6 against 2.2); at 333 a warp is no faster.
+      // Many rows: as many elements per thread as registers allow, so that an SM holds
+      // more rows at a time (16384 x 2047 with residual: 43 us with 16, 45 with 8, 68
+      // with 4; 9537 x 6221: 103 with 16, 112 with 32).  Up to 512 elements a warp per
+      // row (11874 x 203: 4.5 us against 12.4, 5000 x 333 3.4 against 5.4), up to 128
+      // in single ones (11874 x 115: 3.5 against 4.2 in pairs).
+      const bool many = n.T >= 4 * sm_count();
       if (n.H <= 4 * 32) return launch<DT, 1, 4, OUT, true>(n, 128, st);
-      if (n.H <= 8 * 32 && n.T >= 4 * sm_count())
-        return launch<DT, 1, 8, OUT, true>(n, 128, st);
-      // Rows of single elements: few per thread while rows are few (65 x 6221: 3.9
-      // us with 8, 5.3 with 16), more once rows fill the SMs, whose registers
-      // then hold more rows at a time (9537 x 6221: 137 us with 16, 202 with 8).
-      if (n.H <= 4 * 512) return launch<DT, 1, 4, OUT, false>(n, ((n.H + 3) / 4 + 31) / 32 * 32, st);
-      if (n.H <= 16 * 512 && n.T >= 4 * sm_count())
-        return launch<DT, 1, 16, OUT, false>(n, ((n.H + 15) / 16 + 31) / 32 * 32, st);
-      if (n.H <= 8 * 1024) return launch<DT, 1, 8, OUT, false>(n, ((n.H + 7) / 8 + 31) / 32 * 32, st);
+      if (many && n.H <= 8 * 32) return launch<DT, 2, 4, OUT, true>(n, 128, st);
+      if (many && n.H <= 16 * 32) return launch<DT, 2, 8, OUT, true>(n, 128, st);
+      if (many && n.H <= 16 * 512)
+        return launch<DT, 2, 8, OUT, false>(n, ((n.H + 15) / 16 + 31) / 32 * 32, st);
+      // Few rows: few elements per thread (300 x 203: 1.9 us, 2.6 with a warp each).
+      if (n.H <= 4 * 512) return launch<DT, 2, 2, OUT, false>(n, ((n.H + 3) / 4 + 31) / 32 * 32, st);
+      if (n.H <= 8 * 1024) return launch<DT, 2, 4, OUT, false>(n, ((n.H + 7) / 8 + 31) / 32 * 32, st);
       return launch<DT, 1, 32, OUT, false>(n, 1024, st);
     }
   }

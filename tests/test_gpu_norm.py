@@ -183,3 +183,26 @@ def test_many_narrow_rows(m, H, e4m3):
         _check8(out.float(), s, y, 0)
     else:
         _check16(out, y, torch.float16)
+
+
+@pytest.mark.parametrize("H", [333, 511, 512, 513, 1023, 2047, 6221, 8191])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_odd_rows(m, H, e4m3):
+    """More rows than four per SM, alike and unlike in where they begin."""
+    T = 701
+    x, r, w = _inputs(T, H, torch.bfloat16, H)
+    y = norm_ref(x, w, r, EPS)
+    for pad in (0, 1):
+        xd = torch.zeros(T, H + pad + 1, dtype=torch.bfloat16, device=DEV)[:, pad:pad + H]
+        xd.copy_(x)
+        rd = torch.zeros(T, H + pad, dtype=torch.bfloat16, device=DEV)[:, pad:]
+        rd.copy_(r)
+        out = torch.empty(T, H, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16, device=DEV)
+        ro = torch.empty(T, H, dtype=torch.bfloat16, device=DEV)
+        s = torch.empty(T, 1, device=DEV) if e4m3 else None
+        m.moe_add_rmsnorm(xd, w.to(DEV), out, residual=rd, residual_out=ro, scales=s, eps=EPS)
+        if e4m3:
+            _check8(out.float(), s, y, 0)
+        else:
+            _check16(out, y, torch.bfloat16)
+        assert torch.equal(ro.cpu(), (x.float() + r.float()).to(torch.bfloat16))
