@@ -27,7 +27,8 @@
 //
 // Head chunks of a kv head beyond the first are further segments, or, up to
 // kMaxSides of them, lines of their own side by side (blockIdx.y), on which as many
-// workers read the same rows at about the same time.
+// workers read the same rows at about the same time.  Neighbouring kv heads, whose rows
+// of a token are neighbours in memory, get lines side by side too (kv_sides).
 //
 // A worker is a CTA, or, where segments are few, a team: a cluster of 8 CTAs whose
 // warps share each segment and sum their outputs through distributed shared
@@ -107,7 +108,8 @@ struct AttnArgs {
   moe_attention_t a;
   uint8_t* ws;
   int32_t chunks;  // head chunks of a kv head on a line
-  int32_t sides;   // lines side by side, one per further head chunk
+  int32_t sides;   // lines side by side, one per further head chunk ...
+  int32_t kv_sides;  // ... times those over neighbouring kv heads (a divisor of n_kv_heads)
   int32_t hpc;     // query heads of a chunk (<= 8 * NT)
   int32_t group;   // query heads of a kv head
   int32_t max_len; // max_pages * page_size, saturated
@@ -320,7 +322,8 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
 
   // The line's length and shape.  Up to 32 sequences: every warp by itself, a
   // sequence per lane.
-  const int segs = g.c.n_kv_heads * g.chunks;  // segments of a sequence
+  const int segs = g.c.n_kv_heads / g.kv_sides * g.chunks;  // segments of a sequence on this line
+  const int side = static_cast<int>(blockIdx.y) / g.kv_sides, kv_side = static_cast<int>(blockIdx.y) - side * g.kv_sides;
   // the worker, and this CTA's and warp's number in it
   const int worker = static_cast<int>(blockIdx.x) / S::kTeam;
   const int rank = TEAM ? static_cast<int>(cluster_rank()) : 0;
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
 #pragma unroll
     for (int r = 0; r < kRr; ++r) npage[r] = -1, noff[r] = 0, nvalid[r] = false;
     if (!nhave) return;
-    nkvh = g.chunks == 1 ? cseg : cseg / g.chunks;
+    nkvh = (g.chunks == 1 ? cseg : cseg / g.chunks) * g.kv_sides + kv_side;
     const int32_t* table = a.block_table + cb * a.table_stride;
 #pragma unroll
     for (int r = 0; r < kRr; ++r) {
@@ -609,8 +612,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
     const int ue = min(nb, ub + p_end - p);
     const int seg_start = p - ub;
     if (ue <= kVoid) break;  // the share ends before the segment's first unit: it is the next CTA's
-    const int kvh = g.chunks == 1 ? seg : seg / g.chunks, chunk = seg - kvh * g.chunks;
-    const int h_in = (chunk * g.sides + static_cast<int>(blockIdx.y)) * g.hpc;
+    const int kv = g.chunks == 1 ? seg : seg / g.chunks, chunk = seg - kv * g.chunks;
+    const int kvh = kv * g.kv_sides + kv_side;
+    const int h_in = (chunk * g.sides + side) * g.hpc;
     const int heads = min(g.hpc, g.group - h_in);  // query heads of this segment
     const int h0 = kvh * g.group + h_in;
     if constexpr (TEAM) {
@@ -1233,7 +1237,7 @@ moe_status_t launch(const AttnArgs& g, cudaStream_t st) {
     }
     grid_of[dev].store(grid, std::memory_order_release);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(grid / g.sides), static_cast<unsigned>(g.sides));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid / (g.sides * g.kv_sides)), static_cast<unsigned>(g.sides * g.kv_sides));
   cfg.numAttrs = TEAM ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, g) != cudaSuccess) return check_launch("paged_attention_kernel");
   stat_kernels(1);

@@ -402,3 +402,13 @@ def test_groups_of_several_chunks_in_a_wide_table(m, D, hq, hkv, e4m3):
     first, _ = c.check()
     again, _ = c.run(ws=c.ws)
     assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("head_major", [False, True])
+@pytest.mark.parametrize("D,hq,hkv", [(64, 12, 12), (96, 14, 7), (128, 40, 8), (128, 60, 6), (128, 120, 4), (256, 36, 3)])
+def test_kv_heads_on_lines_side_by_side(m, D, hq, hkv, head_major):
+    c = Case(m, [900, 31, 0, 517, 64, 3, 1, 200, 16, 77, 130], hq, hkv, D, 32, torch.float16, True,
+             head_major=head_major, max_pages=500)
+    first, _ = c.check()
+    again, _ = c.run(ws=c.ws)
+    assert torch.equal(first, again)
