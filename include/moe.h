@@ -351,6 +351,9 @@ MOE_API moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_rope
  * or past the table is clamped; both are recorded in ws (MOE_ERR_DEVICE from
  * moe_query_status).  Several new tokens of one sequence are several rows whose
  * table rows repeat and whose lengths count up.
+ * Infinite values make their columns infinite, and both signs together NaN.  (Over an
+ * fp16 cache a weight below 2^-39 of the head's largest is zero, and zero times an
+ * infinite value is NaN; over a bf16 one that begins at 2^-126, as in fp32.)
  * One launch; results do not depend on timing (parts join in a fixed order).
  * Limits: B * n_kv_heads * (max_pages * page_size / 16 + 6) below 2^31, n_q_heads
  * <= 65536.
