@@ -61,11 +61,27 @@ def random_layer(cfg: LayerCfg, device, generator=None) -> dict:
     return w
 
 
+def places(positions, block_table, page_size):
+    """Cache slots (int64) and lengths (int32) of the tokens at ``positions``.  Positions
+    are device values that a captured step counts up, so what they are is found out on
+    the device: one outside the table gets slot -1 (nothing is stored) and a length
+    that the attention clamps and records, and ``Decoder.check`` raises."""
+    last = block_table.shape[1] * page_size
+    inside = (positions >= 0) & (positions < last)
+    at = positions.clamp(0, last - 1)
+    page = block_table.gather(1, (at // page_size)[:, None])[:, 0].to(torch.int64)
+    slots = torch.where(inside, page * page_size + at % page_size, -1)
+    return slots, (positions.clamp(-2, last) + 1).to(torch.int32)
+
+
 class Decoder:
     """Layers, their paged caches and everything a step needs, for ``batch``
-    sequences of up to ``max_len`` tokens."""
+    sequences of up to ``max_len`` tokens (rounded up to whole pages).  A sequence
+    stepped past them loses its further tokens and is reported by ``check``."""
 
     def __init__(self, cfg: LayerCfg, layers: list[dict], batch: int, max_len: int, device):
+        if not layers or batch < 1 or max_len < 1:
+            raise ValueError("a decoder needs layers, and batch and max_len of at least 1")
         self.cfg, self.layers, self.B = cfg, layers, batch
         m, dt = cfg.moe, cfg.moe.torch_dtype
         H, D, hq, hkv, P = m.hidden, cfg.head_dim, cfg.n_q_heads, cfg.n_kv_heads, cfg.page_size
@@ -109,10 +125,8 @@ class Decoder:
     def step(self, h):
         """One token per sequence: ``h`` [B, hidden] its embeddings; returns the
         last layer's block output and the residual it is still to be added to."""
-        c, P = self.cfg, self.cfg.page_size
-        page = self.block_table.gather(1, (self.positions // P)[:, None])[:, 0].to(torch.int64)
-        slots = page * P + self.positions % P
-        lens = (self.positions + 1).to(torch.int32)
+        c = self.cfg
+        slots, lens = places(self.positions, self.block_table, c.page_size)
         x = h
         for i, (w, cache) in enumerate(zip(self.layers, self.caches)):
             if i == 0:
