@@ -269,8 +269,11 @@ MOE_API moe_status_t moe_sum_partials(const float* partials, int32_t n_parts, in
  * 1 <= H <= 32768 and any row strides >= H; rows whose pointers and strides
  * are multiples of 16 bytes with H % 8 == 0 take the wide loads.  group is 0
  * or a power of two from 16 to 256, and then needs those wide rows (H need
- * not be a multiple of it).  residual_out may be residual or x, and out may
- * be x, with the same strides (in place); no other overlap. */
+ * not be a multiple of it).  Outputs may lie on x or residual (in place) as
+ * long as no row of theirs shares a byte with another row's input: the rows
+ * are then at the same distance in bytes, which for an e4m3 out is twice x's
+ * stride in elements.  Other overlaps of x, residual, out and residual_out are
+ * refused (MOE_ERR_INVALID_ARG); weight and scales lie apart from all. */
 typedef struct moe_norm {
   const void* x;         /* [T, H] dtype                                     */
   const void* residual;  /* [T, H] dtype, or NULL                            */

@@ -369,6 +369,30 @@ moe_status_t dispatch(const moe_norm_t& n, bool wide, cudaStream_t st) {
   return launch<DT, 8, 8, OUT, false>(n, thr, st);
 }
 
+// A tensor's rows by their bytes.
+struct Rows {
+  const void* at;
+  int64_t step;   // from row to row
+  int64_t bytes;  // of a row, at most step
+};
+
+// Whether a row of `a` shares a byte with a row of `b` other than (same_row: or the same as)
+// its own number's.  A row is read whole before any of it is written, so in place is fine
+// row by row; other rows are other CTAs'.  At different distances any overlap counts.
+bool overlap(const Rows& a, const Rows& b, int32_t T, bool same_row) {
+  const int64_t p = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.at));
+  const int64_t q = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at));
+  const int64_t last = T - 1;
+  if (p + last * a.step + a.bytes <= q || q + last * b.step + b.bytes <= p) return false;
+  if (last == 0) return same_row;
+  if (a.step != b.step) return true;
+  // row i + k of b begins d + k * step bytes behind row i of a
+  const int64_t d = q - p, s = a.step, near = -d / s;
+  for (int64_t k = near - 1; k <= near + 1; ++k)
+    if ((k != 0 || same_row) && k >= -last && k <= last && d + k * s < a.bytes && d + k * s + b.bytes > 0) return true;
+  return false;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -404,6 +428,13 @@ extern "C" moe_status_t moe_add_rmsnorm(const moe_norm_t* n, void* stream) {
                     (strides & 7) == 0;
   if (n->group && !wide)
     return set_error(MOE_ERR_UNSUPPORTED, "group scales need H %% 8 == 0 and 16-byte aligned rows");
+  const int64_t width = 2ll * n->H;
+  const Rows x{n->x, 2 * n->x_stride, width}, r{n->residual, 2 * n->residual_stride, width};
+  const Rows o{n->out, (e4m3 ? 1 : 2) * n->out_stride, e4m3 ? n->H : width};
+  const Rows ro{n->residual_out, 2 * n->residual_out_stride, width};
+  if (overlap(x, o, n->T, false) || (n->residual && overlap(r, o, n->T, false)) ||
+      (n->residual_out && (overlap(x, ro, n->T, false) || overlap(r, ro, n->T, false) || overlap(o, ro, n->T, true))))
+    return set_error(MOE_ERR_INVALID_ARG, "rows of out or residual_out overlap other rows that are read or written");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int out = !e4m3 ? kOutSame : n->group ? kOutGroup : kOutRow;
   if (n->dtype == MOE_BF16)
