@@ -384,6 +384,16 @@ def _flat(t, name, shape, dtype, index):
     return t.data_ptr()
 
 
+def _workspace(ws, cache, q):
+    """Address and bytes of a workspace on the cache's and the queries' device, whose
+    elements lie one after the other (an expanded tensor counts more than it has)."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor")
+    if cache._dev != q.get_device() or ws.get_device() != cache._dev:
+        raise ValueError(f"cache on {cache.device} and ws on {ws.device}, expected both on {q.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=None, group=0, eps=1e-6, stream=None):
     """RMS norm of ``x (+ residual)`` [T, H] times ``weight`` [H] into ``out``:
     x's dtype, or float8_e4m3fn with ``scales`` [T, 1] (one per row) or
@@ -508,8 +518,7 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
     slot = _flat(slots, "slots", (T,), torch.int64, dev)
     n_freq = inv_freq.numel()
     freq = _flat(inv_freq, "inv_freq", (n_freq,), torch.float32, dev)
-    if cache._dev != dev or ws.get_device() != dev:
-        raise ValueError(f"cache on {cache.device} and ws on {ws.device}, expected both on {q.device}")
+    ws_p, ws_bytes = _workspace(ws, cache, q)
     qn = kn = 0
     if q_norm_w is not None or k_norm_w is not None:
         if q_norm_w is None or k_norm_w is None:
@@ -519,7 +528,7 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
     args = _ROPE_T.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), pos, slot, freq, qn, kn,
                         qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], T, hq, 2 * n_freq, code,
                         1 if interleaved else 0, eps)
-    rc = (_lib or _load()).moe_rope_append(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
+    rc = (_lib or _load()).moe_rope_append(cache._c, args, ws_p, ws_bytes, _launch_stream(dev, stream))
     if rc:
         _check(rc)
 
@@ -550,11 +559,10 @@ def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, sc
     bs = _rows(block_table, "block_table", (B, pages), torch.int32, dev)
     lens = _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
     lse_p = 0 if lse is None else _flat(lse, "lse", (B, hq), torch.float32, dev)
-    if cache._dev != dev or ws.get_device() != dev:
-        raise ValueError(f"cache on {cache.device} and ws on {ws.device}, expected both on {q.device}")
+    ws_p, ws_bytes = _workspace(ws, cache, q)
     args = _ATTN_T.pack(q.data_ptr(), out.data_ptr(), lse_p, block_table.data_ptr(), lens, qs[0], qs[1], os_[0], os_[1],
                         bs[0], B, hq, pages, window, code, D ** -0.5 if scale is None else scale)
-    rc = (_lib or _load()).moe_paged_attention(cache._c, args, ws.data_ptr(), ws.numel(), _launch_stream(dev, stream))
+    rc = (_lib or _load()).moe_paged_attention(cache._c, args, ws_p, ws_bytes, _launch_stream(dev, stream))
     if rc:
         _check(rc)
 

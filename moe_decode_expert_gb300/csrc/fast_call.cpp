@@ -47,6 +47,11 @@ bool flat(const at::Tensor* t, std::initializer_list<int64_t> sizes, at::ScalarT
   return rows(t, sizes, dtype, dev) && t->is_contiguous();
 }
 
+// A workspace: elements one after the other (an expanded tensor counts more than it has).
+bool workspace(const at::Tensor& t, int dev) {
+  return t.is_cuda() && t.get_device() == dev && t.layout() == at::kStrided && t.is_contiguous();
+}
+
 int float_code(at::ScalarType t) {
   return t == at::kHalf ? MOE_F16 : t == at::kBFloat16 ? MOE_BF16 : 0;
 }
@@ -131,7 +136,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = q.size(0), hq = q.size(1), D = c->head_dim, hkv = c->n_kv_heads, nf = t[5]->numel();
   const at::ScalarType dt = q.scalar_type();
   const int code = float_code(dt);
-  if (!code || cache_dev != dev || !ws.is_cuda() || ws.get_device() != dev || T > kIntMax || hq > kIntMax ||
+  if (!code || cache_dev != dev || !workspace(ws, dev) || T > kIntMax || hq > kIntMax ||
       nf > kIntMax / 2 || !rows(&q, {T, hq, D}, dt, dev) || !rows(t[1], {T, hkv, D}, dt, dev) ||
       !rows(t[2], {T, hkv, D}, dt, dev) || !flat(t[3], {T}, at::kLong, dev) || !flat(t[4], {T}, at::kLong, dev) ||
       !flat(t[5], {nf}, at::kFloat, dev) || !rows(t[6], {T, hq, D}, dt, dev))
@@ -164,7 +169,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   m.eps = static_cast<float>(eps);
   void* st;
   if (!stream_of(a[14], dev, &st)) return leave_it();
-  return PyLong_FromLong(rope_entry(c, &m, ws.data_ptr(), static_cast<size_t>(ws.numel()), st));
+  return PyLong_FromLong(rope_entry(c, &m, ws.data_ptr(), ws.nbytes(), st));
 }
 
 // attention(cache, cache device, q, block_table, seq_lens, out, ws, scale, window, lse, stream)
@@ -180,7 +185,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t B = q->size(0), hq = q->size(1), D = c->head_dim, pages = table->size(1);
   const at::ScalarType dt = q->scalar_type();
   const int code = float_code(dt);
-  if (PyErr_Occurred() || !code || cache_dev != dev || !ws->is_cuda() || ws->get_device() != dev || B > kIntMax ||
+  if (PyErr_Occurred() || !code || cache_dev != dev || !workspace(*ws, dev) || B > kIntMax ||
       hq > kIntMax || pages > kIntMax || window < 0 || window > kIntMax || !rows(q, {B, hq, D}, dt, dev) ||
       !rows(out, {B, hq, D}, dt, dev) || !rows(table, {B, pages}, at::kInt, dev) || !flat(lens, {B}, at::kInt, dev))
     return leave_it();
@@ -205,7 +210,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return leave_it();
   void* st;
   if (!stream_of(a[10], dev, &st)) return leave_it();
-  return PyLong_FromLong(attn_entry(c, &m, ws->data_ptr(), static_cast<size_t>(ws->numel()), st));
+  return PyLong_FromLong(attn_entry(c, &m, ws->data_ptr(), ws->nbytes(), st));
 }
 
 // bind(moe_add_rmsnorm, moe_rope_append, moe_paged_attention): the loaded library's entries

@@ -1,0 +1,45 @@
+"""Workspaces as the compiled and the Python form of the layer operators take them."""
+import pytest
+import torch
+
+from tests.test_gpu_fast_call import DEV, m  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_workspaces(m, monkeypatch, fast):  # noqa: F811
+    monkeypatch.setattr(m, "_fast", m._fast if fast else None)
+    kv = torch.zeros(4, 16, 2, 64, dtype=BF, device=DEV)
+    cache = m.MoeKvCache(kv, kv.clone())
+    ws = m.alloc_attention_workspace(cache, 4)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q, k = (torch.randn(2, h, 64, generator=g, device=DEV).to(BF) for h in (4, 2))
+    pos, f = torch.arange(2, device=DEV), torch.rand(32, device=DEV)
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([1, 1], dtype=torch.int32, device=DEV)
+
+    def both(ws):
+        qo, out = torch.zeros_like(q), torch.zeros_like(q)
+        m.moe_rope_append(cache, q, k, k, pos, pos * 16, f, qo, ws)
+        m.moe_paged_attention(cache, qo, table, lens, out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    want = both(ws)
+    assert torch.equal(want, k.repeat_interleave(2, 1))  # one token: its value
+    # the bytes count, whatever the elements are
+    wide = torch.zeros(ws.numel() // 4 + 64, dtype=torch.float32, device=DEV)
+    wide = wide[(-wide.data_ptr()) % 256 // 4:][:ws.numel() // 4]
+    assert torch.equal(both(wide), want)
+    m.moe_query_status(wide)
+    for bad in (torch.zeros(1, dtype=torch.uint8, device=DEV).expand(ws.numel()),
+                torch.zeros(2 * ws.numel(), dtype=torch.uint8, device=DEV)[::2]):
+        for call in (lambda: m.moe_rope_append(cache, q, k, k, pos, pos, f, q.clone(), bad),
+                     lambda: m.moe_paged_attention(cache, q, table, lens, q.clone(), bad)):
+            with pytest.raises(ValueError, match="ws"):
+                call()
+    for short in (wide[:32], ws[:128]):
+        with pytest.raises(m.MoeError):
+            m.moe_rope_append(cache, q, k, k, pos, pos, f, q.clone(), short)
