@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -155,8 +156,13 @@ def _bind_fast_call(lib):
         from . import _fast_call
     except ImportError:  # not built here: the Python form does the same
         return
-    _fast_call.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (lib.moe_add_rmsnorm, lib.moe_rope_append, lib.moe_paged_attention)))
+    entries = (lib.moe_add_rmsnorm, lib.moe_rope_append, lib.moe_paged_attention)
+    structs = (_NORM_T, _CACHE_T, _ROPE_T, _ATTN_T)
+    if getattr(_fast_call, "built_for", None) != torch.__version__ or not _fast_call.bind(
+            *(ctypes.cast(f, ctypes.c_void_p).value for f in entries), *(t.size for t in structs)):
+        warnings.warn("the compiled argument checks were built for another PyTorch or header and are not used: "
+                      "build them with __graft_entry__.build()")
+        return
     _fast = _fast_call
 
 

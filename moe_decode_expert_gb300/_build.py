@@ -24,8 +24,10 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 # see trace_phases.py); never loaded by the package unless asked for.
 TRACE_BUILD = os.path.join(ROOT, "_build", "moe_trace")
 TRACE_LIB = os.path.join(PKG, "libmoe_gb300_trace.so")
-# Argument checks of the layer operators in compiled code (see fast_call.cpp).
-FAST_CALL = os.path.join(PKG, "_fast_call.so")
+# Argument checks of the layer operators in compiled code (see fast_call.cpp); the name
+# tells the interpreter, the key what it was compiled for.
+FAST_CALL = os.path.join(PKG, "_fast_call" + sysconfig.get_config_var("EXT_SUFFIX"))
+FAST_CALL_KEY = os.path.join(ROOT, "_build", "fast_call.key")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -62,29 +64,46 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
 
 def build_fast_call() -> str | None:
     """Compile ``csrc/fast_call.cpp`` (host code over PyTorch's headers) into the
-    extension module ``_fast_call``.  Without it (no headers, another compiler)
-    the binding checks and packs in Python: slower calls, the same kernels; so a
-    failure is reported and not raised."""
+    extension module ``_fast_call``, anew where it was compiled for another PyTorch
+    or in another way.  Without it (no headers, another compiler, none) the binding
+    checks and packs in Python: slower calls, the same kernels; so a failure is
+    reported and not raised, and leaves no older module behind."""
     src = os.path.join(CSRC, "fast_call.cpp")
-    if os.path.exists(FAST_CALL) and os.path.getmtime(FAST_CALL) >= max(os.path.getmtime(src), _newest_dep()):
-        return FAST_CALL
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(_cuda_lib_dir()), "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMOE_TORCH_VERSION="{torch.__version__}"', "-I", INCLUDE]
     for d in inc:
         cmd += ["-isystem", d]
-    tmp = FAST_CALL + f".tmp{os.getpid()}"
     lib = os.path.join(root, "lib")
-    cmd += [src, "-o", tmp, "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-            "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        print(f"fast_call.cpp was not built (calls are checked in Python instead):\n{r.stderr[-2000:]}", file=sys.stderr)
+    cmd += [src, "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    key = "\n".join([sys.version, *cmd])
+    if os.path.exists(FAST_CALL) and os.path.getmtime(FAST_CALL) >= max(os.path.getmtime(src), _newest_dep()):
+        try:
+            with open(FAST_CALL_KEY) as f:
+                if f.read() == key:
+                    return FAST_CALL
+        except OSError:
+            pass
+    for old in (FAST_CALL, os.path.join(os.path.dirname(FAST_CALL), "_fast_call.so")):  # (the name without a tag: once)
+        if os.path.exists(old):
+            os.remove(old)
+    tmp = FAST_CALL + f".tmp{os.getpid()}"
+    try:
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        failed = r.stderr[-2000:] if r.returncode != 0 else None
+    except OSError as e:  # no compiler
+        failed = str(e)
+    if failed is not None:
+        print(f"fast_call.cpp was not built (calls are checked in Python instead):\n{failed}", file=sys.stderr)
         return None
     os.replace(tmp, FAST_CALL)
+    os.makedirs(os.path.dirname(FAST_CALL_KEY), exist_ok=True)
+    with open(FAST_CALL_KEY, "w") as f:
+        f.write(key)
     return FAST_CALL
 
 

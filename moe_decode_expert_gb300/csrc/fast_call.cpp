@@ -213,17 +213,25 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(attn_entry(c, &m, ws->data_ptr(), ws->nbytes(), st));
 }
 
-// bind(moe_add_rmsnorm, moe_rope_append, moe_paged_attention): the loaded library's entries
+// bind(moe_add_rmsnorm, moe_rope_append, moe_paged_attention: the loaded library's entries,
+// sizes of moe_norm_t, moe_kv_cache_t, moe_rope_t, moe_attention_t): False, and nothing
+// bound, where the structs compiled here are others.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 3) {
-    PyErr_SetString(PyExc_TypeError, "three addresses expected");
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "three addresses and four sizes expected");
     return nullptr;
   }
-  norm_entry = reinterpret_cast<NormFn>(PyLong_AsVoidPtr(a[0]));
-  rope_entry = reinterpret_cast<RopeFn>(PyLong_AsVoidPtr(a[1]));
-  attn_entry = reinterpret_cast<AttnFn>(PyLong_AsVoidPtr(a[2]));
+  void* entries[3];
+  for (int i = 0; i < 3; ++i) entries[i] = PyLong_AsVoidPtr(a[i]);
+  const size_t sizes[4] = {sizeof(moe_norm_t), sizeof(moe_kv_cache_t), sizeof(moe_rope_t), sizeof(moe_attention_t)};
+  bool same = true;
+  for (int i = 0; i < 4; ++i) same &= PyLong_AsSize_t(a[3 + i]) == sizes[i];
   if (PyErr_Occurred()) return nullptr;
-  Py_RETURN_NONE;
+  if (!same) Py_RETURN_FALSE;
+  norm_entry = reinterpret_cast<NormFn>(entries[0]);
+  rope_entry = reinterpret_cast<RopeFn>(entries[1]);
+  attn_entry = reinterpret_cast<AttnFn>(entries[2]);
+  Py_RETURN_TRUE;
 }
 
 // C++ exceptions (of torch's accessors) end here.
@@ -247,4 +255,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast_call", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast_call() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__fast_call() {
+  PyObject* mod = PyModule_Create(&module);
+  // The tensor class is compiled in: the binding uses this module with that PyTorch only.
+  if (mod && PyModule_AddStringConstant(mod, "built_for", MOE_TORCH_VERSION) < 0) Py_CLEAR(mod);
+  return mod;
+}
