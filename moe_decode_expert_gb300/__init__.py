@@ -346,8 +346,6 @@ _ATTN_T = struct.Struct("@5P5q5if0q")
 # A decode step makes these calls dozens of times per token and their kernels
 # take a few microseconds, so their checks are made in compiled code where that
 # is built, and here in single comparisons, with the stream asked for as a number.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
 _FLOATS = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
 
 
@@ -355,10 +353,12 @@ def _launch_stream(index, stream):
     """The raw stream a call on tensors of CUDA device `index` goes to."""
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if index != _current_device():
-        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
+    # (private, so asked for here: a PyTorch without CUDA has neither and still imports this)
+    current = torch._C._cuda_getDevice()
+    if index != current:
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{current}")
     if stream is None:
-        return _raw_stream(index)
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
