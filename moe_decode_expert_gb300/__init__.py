@@ -13,6 +13,8 @@ Functions carry the C names (``moe_router_topk``, ``moe_decode_forward``,
 from __future__ import annotations
 
 import ctypes
+import math
+import operator
 import os
 import struct
 import warnings
@@ -362,10 +364,33 @@ def _launch_stream(index, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is required, got {type(t).__name__}")
+    return t
+
+
+def _int32(v, name):
+    try:
+        v = operator.index(v)
+    except TypeError:
+        raise ValueError(f"{name}: an integer is required, got {type(v).__name__}") from None
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name}: {v} does not fit 32 bits")
+    return v
+
+
+def _fp32(v, name):
+    if not hasattr(v, "__float__"):
+        raise ValueError(f"{name}: a number is required, got {type(v).__name__}")
+    v = float(v)
+    if 3.4028235e38 < abs(v) < math.inf:
+        raise ValueError(f"{name}: {v} does not fit fp32")
+    return v
+
+
 def _explain(t, name, shape, dtype, index):
     """Raises for the first thing wrong with an argument (contiguous rows asked for)."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} is required")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
@@ -377,7 +402,7 @@ def _explain(t, name, shape, dtype, index):
 
 def _rows(t, name, shape, dtype, index):
     """Strides of a tensor of this shape, type and device with contiguous rows."""
-    st = t.stride()
+    st = _tensor(t, name).stride()
     if t.shape != shape or t.dtype is not dtype or t.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
         _explain(t, name, shape, dtype, index)
     return st
@@ -385,7 +410,7 @@ def _rows(t, name, shape, dtype, index):
 
 def _flat(t, name, shape, dtype, index):
     """Address of a contiguous tensor of this shape, type and device."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+    if _tensor(t, name).shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         _explain(t, name, shape, dtype, index)
     return t.data_ptr()
 
@@ -393,7 +418,7 @@ def _flat(t, name, shape, dtype, index):
 def _workspace(ws, cache, q):
     """Address and bytes of a workspace on the cache's and the queries' device, whose
     elements lie one after the other (an expanded tensor counts more than it has)."""
-    if not isinstance(ws, torch.Tensor) or not ws.is_contiguous():
+    if not _tensor(ws, "ws").is_contiguous():
         raise ValueError("ws must be a contiguous tensor")
     if cache._dev != q.get_device() or ws.get_device() != cache._dev:
         raise ValueError(f"cache on {cache.device} and ws on {ws.device}, expected both on {q.device}")
@@ -411,14 +436,15 @@ def moe_add_rmsnorm(x, weight, out, residual=None, residual_out=None, scales=Non
             return
         if rc > 0:
             _check(rc)
-    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    shape, dt, dev = _tensor(x, "x").shape, x.dtype, x.get_device()
     if len(shape) != 2:
         raise ValueError(f"x: shape {tuple(shape)}, expected [T, H]")
     T, H = shape
     code = _FLOATS.get(dt)
     if code is None:
         raise ValueError(f"x: dtype {dt}, expected float16 or bfloat16")
-    e4m3 = out.dtype is torch.float8_e4m3fn
+    e4m3 = _tensor(out, "out").dtype is torch.float8_e4m3fn
+    group, eps = _int32(group, "group"), _fp32(eps, "eps")
     xs = _rows(x, "x", shape, dt, dev)[0]
     os_ = _rows(out, "out", shape, out.dtype if e4m3 else dt, dev)[0]
     _rows(weight, "weight", (H,), dt, dev)
@@ -454,7 +480,7 @@ class MoeKvCache:
     are fine) with contiguous rows.  Holds the tensors; checked once here."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        if k.dim() != 4:
+        if _tensor(k, "k").dim() != 4:
             raise ValueError(f"k: shape {tuple(k.shape)}, expected [pages, page, kv heads, head_dim]")
         if k.dtype not in (torch.float16, torch.bfloat16, torch.float8_e4m3fn):
             raise ValueError(f"k: dtype {k.dtype}, expected float16, bfloat16 or float8_e4m3fn")
@@ -500,14 +526,16 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
     RMS norm when ``q_norm_w`` and ``k_norm_w`` [D] are given, and stores k and v
     in the cache's ``slots`` [T] int64 (page * page_size + place; negative:
     not stored)."""
-    if _fast is not None:
+    if _fast is not None and isinstance(cache, MoeKvCache):
         rc = _fast.rope(cache._c, cache._dev, q, k, v, positions, slots, inv_freq, q_out, ws, q_norm_w, k_norm_w, eps,
                         interleaved, stream)
         if rc == 0:
             return
         if rc > 0:
             _check(rc)
-    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    if not isinstance(cache, MoeKvCache):
+        raise ValueError("cache: a MoeKvCache is required")
+    shape, dt, dev = _tensor(q, "q").shape, q.dtype, q.get_device()
     code = _FLOATS.get(dt)
     if code is None:
         raise ValueError(f"q: dtype {dt}, expected float16 or bfloat16")
@@ -522,7 +550,7 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
     os_ = _rows(q_out, "q_out", shape, dt, dev)
     pos = _flat(positions, "positions", (T,), torch.int64, dev)
     slot = _flat(slots, "slots", (T,), torch.int64, dev)
-    n_freq = inv_freq.numel()
+    n_freq = _tensor(inv_freq, "inv_freq").numel()
     freq = _flat(inv_freq, "inv_freq", (n_freq,), torch.float32, dev)
     ws_p, ws_bytes = _workspace(ws, cache, q)
     qn = kn = 0
@@ -533,7 +561,7 @@ def moe_rope_append(cache: MoeKvCache, q, k, v, positions, slots, inv_freq, q_ou
         kn = _flat(k_norm_w, "k_norm_w", (D,), dt, dev)
     args = _ROPE_T.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), pos, slot, freq, qn, kn,
                         qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], T, hq, 2 * n_freq, code,
-                        1 if interleaved else 0, eps)
+                        1 if interleaved else 0, _fp32(eps, "eps"))
     rc = (_lib or _load()).moe_rope_append(cache._c, args, ws_p, ws_bytes, _launch_stream(dev, stream))
     if rc:
         _check(rc)
@@ -545,13 +573,15 @@ def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, sc
     ``seq_lens`` [B] int32 cached tokens that ``block_table`` [B, max_pages]
     int32 places, into ``out`` [B, Hq, D] (and ``lse`` [B, Hq] fp32).  ``scale``
     defaults to D ** -0.5; ``window`` > 0 keeps the last ``window`` tokens."""
-    if _fast is not None:
+    if _fast is not None and isinstance(cache, MoeKvCache):
         rc = _fast.attention(cache._c, cache._dev, q, block_table, seq_lens, out, ws, scale, window, lse, stream)
         if rc == 0:
             return
         if rc > 0:
             _check(rc)
-    shape, dt, dev = q.shape, q.dtype, q.get_device()
+    if not isinstance(cache, MoeKvCache):
+        raise ValueError("cache: a MoeKvCache is required")
+    shape, dt, dev = _tensor(q, "q").shape, q.dtype, q.get_device()
     code = _FLOATS.get(dt)
     if code is None:
         raise ValueError(f"q: dtype {dt}, expected float16 or bfloat16")
@@ -561,13 +591,14 @@ def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, sc
     B, hq, _ = shape
     qs = _rows(q, "q", shape, dt, dev)
     os_ = _rows(out, "out", shape, dt, dev)
-    pages = block_table.shape[-1] if block_table.dim() else 0
+    pages = block_table.shape[-1] if _tensor(block_table, "block_table").dim() else 0
     bs = _rows(block_table, "block_table", (B, pages), torch.int32, dev)
     lens = _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
     lse_p = 0 if lse is None else _flat(lse, "lse", (B, hq), torch.float32, dev)
     ws_p, ws_bytes = _workspace(ws, cache, q)
     args = _ATTN_T.pack(q.data_ptr(), out.data_ptr(), lse_p, block_table.data_ptr(), lens, qs[0], qs[1], os_[0], os_[1],
-                        bs[0], B, hq, pages, window, code, D ** -0.5 if scale is None else scale)
+                        bs[0], B, hq, pages, _int32(window, "window"), code,
+                        D ** -0.5 if scale is None else _fp32(scale, "scale"))
     rc = (_lib or _load()).moe_paged_attention(cache._c, args, ws_p, ws_bytes, _launch_stream(dev, stream))
     if rc:
         _check(rc)

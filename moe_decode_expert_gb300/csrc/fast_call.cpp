@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -78,13 +79,16 @@ const moe_kv_cache_t* cache_of(PyObject* o) {
 
 constexpr int64_t kIntMax = 0x7fffffff;
 
+// Whether a number is one in fp32 too.
+bool fits(double v) { return !std::isfinite(v) || std::fabs(v) <= FLT_MAX; }
+
 // norm(x, weight, out, residual, residual_out, scales, group, eps, stream)
 PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor *x, *w, *out, *r = nullptr, *ro = nullptr, *sc = nullptr;
   if (n != 9 || !norm_entry || !(x = tensor(a[0])) || !(w = tensor(a[1])) || !(out = tensor(a[2]))) return leave_it();
   const long group = PyLong_AsLong(a[6]);
   const double eps = PyFloat_AsDouble(a[7]);
-  if (PyErr_Occurred() || !x->is_cuda() || x->dim() != 2 || group < 0 || group > 65536) return leave_it();
+  if (PyErr_Occurred() || !fits(eps) || !x->is_cuda() || x->dim() != 2 || group < 0 || group > 65536) return leave_it();
   const int dev = x->get_device();
   const int64_t T = x->size(0), H = x->size(1);
   const at::ScalarType dt = x->scalar_type();
@@ -131,7 +135,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const long cache_dev = PyLong_AsLong(a[1]);
   const double eps = PyFloat_AsDouble(a[12]);
   const int inter = PyObject_IsTrue(a[13]);
-  if (PyErr_Occurred() || !c || !q.is_cuda() || q.dim() != 3) return leave_it();
+  if (PyErr_Occurred() || !fits(eps) || !c || !q.is_cuda() || q.dim() != 3) return leave_it();
   const int dev = q.get_device();
   const int64_t T = q.size(0), hq = q.size(1), D = c->head_dim, hkv = c->n_kv_heads, nf = t[5]->numel();
   const at::ScalarType dt = q.scalar_type();
@@ -206,8 +210,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   m.max_pages = static_cast<int32_t>(pages);
   m.window = static_cast<int32_t>(window);
   m.dtype = code;
-  m.scale = static_cast<float>(a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : PyFloat_AsDouble(a[7]));
-  if (PyErr_Occurred()) return leave_it();
+  const double scale = a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : PyFloat_AsDouble(a[7]);
+  if (PyErr_Occurred() || !fits(scale)) return leave_it();
+  m.scale = static_cast<float>(scale);
   void* st;
   if (!stream_of(a[10], dev, &st)) return leave_it();
   return PyLong_FromLong(attn_entry(c, &m, ws->data_ptr(), ws->nbytes(), st));

@@ -26,3 +26,50 @@ def test_a_workspace_of_other_memory_than_it_counts_is_refused(m, ws):  # noqa: 
     for call, args in ((m.moe_rope_append, rope), (m.moe_paged_attention, attn)):
         with pytest.raises(ValueError, match="ws"):
             call(*args)
+
+
+def test_what_is_no_tensor_is_named(m):  # noqa: F811
+    x, w = torch.zeros(2, 64, dtype=BF), torch.zeros(64, dtype=BF)
+    for args, kw, name in (((None, w, x), {}, "x"), ((x, None, x), {}, "weight"), ((x, w, None), {}, "out"),
+                           ((x, w, x), dict(residual=1.0), "residual"), ((x, w, x), dict(residual=x, residual_out=[]), "residual_out"),
+                           ((x, w, x.to(torch.float8_e4m3fn)), dict(scales=3), "scales")):
+        with pytest.raises(ValueError, match=rf"^{name}\b"):
+            m.moe_add_rmsnorm(*args, **kw)
+    rope, attn = _args(m)
+    for call, args, names in ((m.moe_rope_append, rope, "cache q k v positions slots inv_freq q_out ws".split()),
+                              (m.moe_paged_attention, attn, "cache q block_table seq_lens out ws".split())):
+        for i, name in enumerate(names):
+            with pytest.raises(ValueError, match=rf"^{name}\b"):
+                call(*args[:i], None, *args[i + 1:])
+    with pytest.raises(ValueError, match="^k_norm_w"):
+        m.moe_rope_append(*rope, q_norm_w=torch.zeros(64, dtype=BF), k_norm_w=2)
+    with pytest.raises(ValueError, match="^lse"):
+        m.moe_paged_attention(*attn, lse=0)
+    kv = torch.zeros(4, 16, 2, 64, dtype=BF)
+    for k, v, s, name in ((None, kv, None, "k"), (kv, None, None, "v"), (kv.to(torch.float8_e4m3fn), kv, None, "v"),
+                          (kv.to(torch.float8_e4m3fn), kv.to(torch.float8_e4m3fn), 1.0, "k_scale")):
+        with pytest.raises(ValueError, match=rf"^{name}\b"):
+            m.MoeKvCache(k, v, s, s)
+
+
+def test_numbers_that_no_argument_holds_are_refused(m):  # noqa: F811
+    x, w = torch.zeros(2, 64, dtype=BF), torch.zeros(64, dtype=BF)
+    e4, s = x.to(torch.float8_e4m3fn), torch.zeros(2, 1)
+    _, attn = _args(m)
+    for call in (lambda: m.moe_add_rmsnorm(x, w, e4, scales=s, group=2 ** 40),
+                 lambda: m.moe_add_rmsnorm(x, w, x, eps="small"),
+                 lambda: m.moe_paged_attention(*attn, window=2 ** 31),
+                 lambda: m.moe_paged_attention(*attn, window=None),
+                 lambda: m.moe_paged_attention(*attn, window=1.5),
+                 lambda: m.moe_paged_attention(*attn, scale="1")):
+        with pytest.raises(ValueError, match="group|eps|window|scale"):
+            call()
+
+
+def test_numbers_past_fp32_are_refused(m):  # noqa: F811
+    x, w = torch.zeros(2, 64, dtype=BF), torch.zeros(64, dtype=BF)
+    rope, attn = _args(m)
+    for call in (lambda: m.moe_add_rmsnorm(x, w, x, eps=1e39), lambda: m.moe_rope_append(*rope, eps=1e300),
+                 lambda: m.moe_paged_attention(*attn, scale=-1e39)):
+        with pytest.raises(ValueError, match="fp32"):
+            call()
