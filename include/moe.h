@@ -358,8 +358,8 @@ MOE_API moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_rope
  * fp16 cache a weight below 2^-39 of the head's largest is zero, and zero times an
  * infinite value is NaN; over a bf16 one that begins at 2^-126, as in fp32.)
  * One launch; results do not depend on timing (parts join in a fixed order).
- * Limits: B * n_kv_heads * (max_pages * page_size / 16 + 6) below 2^31, n_q_heads
- * <= 65536.
+ * Limits: B * n_kv_heads * ceil(n_q_heads / n_kv_heads / 8) * (max_pages * page_size / 16 + 6)
+ * below 2^31, n_q_heads <= 65536.
  * ws: moe_attention_workspace_bytes(), zero-filled once; not shared by calls
  * that can run at the same time. */
 typedef struct moe_attention {
