@@ -374,6 +374,11 @@ typedef struct moe_attention {
 } moe_attention_t;
 
 MOE_API size_t moe_attention_workspace_bytes(const moe_kv_cache_t* cache, int32_t n_q_heads);
+/* Which kernels serve a batch of these sizes: 1 single CTAs, 2 teams of CTAs that share
+ * a sequence, 0 for sizes that are refused.  Both compute the same; for tests and
+ * measurements. */
+MOE_API int32_t moe_attention_form(const moe_kv_cache_t* cache, int32_t B, int32_t n_q_heads, int32_t max_pages,
+                                   int32_t window);
 MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws,
                                          size_t ws_bytes, void* stream);
 

@@ -37,7 +37,7 @@ EXPORTS = ("moe_abi_version", "moe_workspace_bytes", "moe_workspace_init", "moe_
            "moe_decode_forward", "moe_grouped_forward", "moe_query_status", "moe_last_error",
            "moe_get_stats", "moe_reset_stats", "moe_set_wait_timeout_ns", "moe_test_wait_timeout",
            "moe_decode_forward_noalloc", "moe_sum_partials", "moe_add_rmsnorm", "moe_rope_append",
-           "moe_attention_workspace_bytes", "moe_paged_attention")
+           "moe_attention_workspace_bytes", "moe_attention_form", "moe_paged_attention")
 
 
 class MoeError(RuntimeError):
@@ -136,6 +136,7 @@ def _load():
         "moe_add_rmsnorm": ([ctypes.c_char_p, vp], ctypes.c_int),
         "moe_rope_append": ([ctypes.c_char_p, ctypes.c_char_p, vp, sz, vp], ctypes.c_int),
         "moe_attention_workspace_bytes": ([ctypes.c_char_p, i32], sz),
+        "moe_attention_form": ([ctypes.c_char_p, i32, i32, i32, i32], i32),
         "moe_paged_attention": ([ctypes.c_char_p, ctypes.c_char_p, vp, sz, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
@@ -506,6 +507,11 @@ class MoeKvCache:
 
 def moe_attention_workspace_bytes(cache: MoeKvCache, n_q_heads: int) -> int:
     return int(_load().moe_attention_workspace_bytes(cache._c, int(n_q_heads)))
+
+
+def moe_attention_form(cache: MoeKvCache, B: int, n_q_heads: int, max_pages: int, window: int = 0) -> str | None:
+    """Which kernels serve a batch of these sizes: "ctas" or "teams" (None: refused)."""
+    return (None, "ctas", "teams")[_load().moe_attention_form(cache._c, B, n_q_heads, max_pages, window)]
 
 
 def alloc_attention_workspace(cache: MoeKvCache, n_q_heads: int) -> torch.Tensor:

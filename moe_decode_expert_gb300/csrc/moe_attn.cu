@@ -37,6 +37,52 @@ constexpr int kSplitUnits = 32;
 // such lines gain no more and cost short batches 2 %.
 constexpr int kKvSides = 4;
 
+// Tokens that a table of this many pages holds, as the kernel counts them.
+int32_t longest(const moe_kv_cache_t* c, int32_t max_pages) {
+  const int64_t cap = static_cast<int64_t>(max_pages) * c->page_size;
+  return static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
+}
+
+// How a batch is launched: from its sizes alone, as the lengths are the device's.
+struct Plan {
+  int nt;      // tiles of 8 heads of a segment
+  int hpc, chunks, sides, kv_sides;  // as in AttnArgs
+  bool teams;  // workers are teams of CTAs
+};
+
+Plan plan_of(const moe_kv_cache_t* c, int32_t B, int32_t n_q_heads, int32_t max_len, int32_t window) {
+  Plan p;
+  const int group = n_q_heads / c->n_kv_heads, tiles = (group + 7) / 8, dp = padded_dim(c->head_dim);
+  const int fill = 8192 / (dp * (c->dtype == MOE_E4M3 ? 1 : 2));
+  const int unit = fill < 16 ? 16 : fill < 64 ? fill : 64;  // tokens of a team's unit
+  // the same of a CTA's unit
+  const int cta_fill = dp <= 64 ? fill / 2 : fill;
+  const int cta_unit = cta_fill < 16 ? 16 : cta_fill < 64 ? cta_fill : 64;
+  const int most = window > 0 && window < max_len ? window : max_len;  // tokens of a sequence
+  p.nt = n_tiles(group, dp);
+  p.chunks = (tiles + p.nt - 1) / p.nt;
+  const int64_t kv = static_cast<int64_t>(B) * c->n_kv_heads;
+  // (not where that takes segments their teams: 18 of 300 tokens 7.0 us, 36 8.1 with CTAs)
+  if (p.nt == 2 && kv * tiles <= kSplit && most / cta_unit + 2 <= kSplitUnits &&
+      (kv * p.chunks > kTeamsEach || kv * tiles <= kTeamsEach)) {
+    p.nt = 1;
+    p.chunks = tiles;
+  }
+  p.hpc = (group + p.chunks - 1) / p.chunks;
+  const int64_t segments = kv * p.chunks;
+  p.teams = segments <= kTeamSegments || (segments <= kTeamsEach && most / unit + 2 <= kTeamsEachUnits);
+  // (48 heads over 1 of 128, 64 sequences of up to 32k tokens: 243 us, 292 with the
+  // chunks' segments one after the other on one line)
+  p.sides = !p.teams && p.chunks <= kMaxSides ? p.chunks : 1;
+  p.chunks /= p.sides;
+  // neighbouring kv heads side by side, where their rows are neighbours in memory
+  p.kv_sides = 1;
+  if (!p.teams && c->k_head_stride < c->k_token_stride)
+    for (int n = kKvSides / p.sides; n > 1 && p.kv_sides == 1; --n)
+      if (c->n_kv_heads % n == 0) p.kv_sides = n;
+  return p;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -78,7 +124,7 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.a = *a;
   g.ws = static_cast<uint8_t*>(ws);
   g.group = a->n_q_heads / cache->n_kv_heads;
-  const int tiles = (g.group + 7) / 8, dp = padded_dim(cache->head_dim);
+  const int tiles = (g.group + 7) / 8;
   // Tokens are 32-bit numbers; units round a length up by less than 64.
   const int64_t cap = static_cast<int64_t>(a->max_pages) * cache->page_size;
   // The line of units is counted in 32 bits.
@@ -93,33 +139,20 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   g.v_token = static_cast<uint32_t>(cache->v_token_stride * size);
   g.v_head = static_cast<uint32_t>(cache->v_head_stride * size);
   g.blocks = cache->page_size % 16 == 0;
-  g.max_len = static_cast<int32_t>(cap < 0x7fffff00 ? cap : 0x7fffff00);
+  g.max_len = longest(cache, a->max_pages);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int fill = 8192 / (dp * static_cast<int>(size));
-  const int unit = fill < 16 ? 16 : fill < 64 ? fill : 64;  // tokens of a team's unit
-  // the same of a CTA's unit
-  const int cta_fill = dp <= 64 ? fill / 2 : fill;
-  const int cta_unit = cta_fill < 16 ? 16 : cta_fill < 64 ? cta_fill : 64;
-  const int most = a->window > 0 && a->window < g.max_len ? a->window : g.max_len;  // tokens of a sequence
-  int nt = n_tiles(g.group, dp), chunks = (tiles + nt - 1) / nt;
-  const int64_t kv = static_cast<int64_t>(a->B) * g.c.n_kv_heads;
-  // (not where that takes segments their teams: 18 of 300 tokens 7.0 us, 36 8.1 with CTAs)
-  if (nt == 2 && kv * tiles <= kSplit && most / cta_unit + 2 <= kSplitUnits &&
-      (kv * chunks > kTeamsEach || kv * tiles <= kTeamsEach)) {
-    nt = 1;
-    chunks = tiles;
-  }
-  g.hpc = (g.group + chunks - 1) / chunks;
-  const int64_t segments = kv * chunks;
-  const bool teams = segments <= kTeamSegments || (segments <= kTeamsEach && most / unit + 2 <= kTeamsEachUnits);
-  // (48 heads over 1 of 128, 64 sequences of up to 32k tokens: 243 us, 292 with the
-  // chunks' segments one after the other on one line)
-  g.sides = !teams && chunks <= kMaxSides ? chunks : 1;
-  g.chunks = chunks / g.sides;
-  // neighbouring kv heads side by side, where their rows are neighbours in memory
-  g.kv_sides = 1;
-  if (!teams && cache->k_head_stride < cache->k_token_stride)
-    for (int n = kKvSides / g.sides; n > 1 && g.kv_sides == 1; --n)
-      if (cache->n_kv_heads % n == 0) g.kv_sides = n;
-  return teams ? launch_attention_teams(g, nt, st) : launch_attention_ctas(g, nt, st);
+  const Plan plan = plan_of(cache, a->B, a->n_q_heads, g.max_len, a->window);
+  g.hpc = plan.hpc;
+  g.chunks = plan.chunks;
+  g.sides = plan.sides;
+  g.kv_sides = plan.kv_sides;
+  return plan.teams ? launch_attention_teams(g, plan.nt, st) : launch_attention_ctas(g, plan.nt, st);
+}
+
+extern "C" int32_t moe_attention_form(const moe_kv_cache_t* cache, int32_t B, int32_t n_q_heads, int32_t max_pages,
+                                      int32_t window) {
+  if (!cache || cache->n_kv_heads < 1 || cache->page_size < 1 || cache->head_dim < 1 || cache->head_dim > 256 ||
+      B < 1 || n_q_heads < 1 || n_q_heads % cache->n_kv_heads || max_pages < 0 || window < 0)
+    return 0;
+  return plan_of(cache, B, n_q_heads, longest(cache, max_pages), window).teams ? 2 : 1;
 }
