@@ -66,12 +66,15 @@ def places(positions, block_table, page_size):
     are device values that a captured step counts up, so what they are is found out on
     the device: one outside the table gets slot -1 (nothing is stored) and a length
     that the attention clamps and records, and ``Decoder.check`` raises."""
-    last = block_table.shape[1] * page_size
-    inside = (positions >= 0) & (positions < last)
-    at = positions.clamp(0, last - 1)
-    page = block_table.gather(1, (at // page_size)[:, None])[:, 0].to(torch.int64)
-    slots = torch.where(inside, page * page_size + at % page_size, -1)
-    return slots, (positions.clamp(-2, last) + 1).to(torch.int32)
+    # (each operation is a launch of its own in a step, so there are as few as there can be)
+    pages = block_table.shape[1]
+    column = positions // page_size
+    inside = column.clamp(0, pages - 1)
+    slots = torch.add(positions % page_size, block_table.gather(1, inside[:, None])[:, 0], alpha=page_size)
+    slots.masked_fill_(column != inside, -1)
+    lens = torch.empty_like(block_table[:, 0], memory_format=torch.contiguous_format)
+    torch.add(positions.clamp(-2, pages * page_size), 1, out=lens)
+    return slots, lens
 
 
 class Decoder:
