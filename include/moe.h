@@ -348,7 +348,9 @@ MOE_API moe_status_t moe_rope_append(const moe_kv_cache_t* cache, const moe_rope
  *   s_j = scale * q . k_j ;  p = softmax(s) ;  out = sum_j p_j v_j ;
  *   lse = ln sum_j exp(s_j)                         (optional, fp32)
  * for query head h over key/value head h / (n_q_heads / n_kv_heads).  A
- * sequence of length 0 gives zeros and lse = -infinity.  Only tokens inside the
+ * sequence of length 0 gives zeros and lse = -infinity.  Weights enter the second
+ * product to 2^-17 (bf16 cache), or to 2^-11 and 2^-39 of the head's largest (fp16
+ * and e4m3 caches).  Only tokens inside the
  * range are read, so unused table entries and unwritten slots may hold
  * anything.  A page id outside the cache drops its tokens, and a length below 0
  * or past the table is clamped; both are recorded in ws (MOE_ERR_DEVICE from

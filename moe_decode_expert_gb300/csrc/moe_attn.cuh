@@ -14,7 +14,10 @@
 //
 // Weights go into the second product as bf16 in two terms (2^-17) or as fp16 in
 // one, 2^14 above their true value (2^-11, and normal down to 2^-28 of the
-// largest); scores, references, sums and outputs are fp32 throughout.
+// largest; below that 2^-39 of it, absolute).  One fp16 term is no coarser than the
+// half step of an fp16 output, an eighth of a bf16 one's; a second term would
+// be a second product for every value.  Scores, references, sums and outputs are fp32
+// throughout.
 //
 // Work is split evenly over workers whatever the lengths: the (sequence, kv
 // head, unit of U tokens) triples form one line, with kVoid empty places before
@@ -33,14 +36,14 @@
 // A worker is a CTA, or, where segments are few, a team: a cluster of 8 CTAs whose
 // warps share each segment and sum their outputs through distributed shared
 // memory, which spares a short sequence the join through global memory (1531
-// tokens of 2 kv heads: 8.3 us against 13.7 with CTAs).
+// tokens of 2 kv heads: 8.4 to 8.7 us against 13.7 with CTAs).
 //
 // A warp owns whole units: K and V of a unit are two slots of its own ring in
 // shared memory, filled by cp.async two slots ahead, across segment ends; only the
 // end of a long segment's part meets at a CTA barrier.
 //
 // Measured (fraction of the 6787 GB/s copy): 64 sequences of up to 32k tokens,
-// 16 over 2 heads of 256, bf16: 320 us (100 %); 285k tokens of 8 e4m3 heads of
+// 16 over 2 heads of 256, bf16: 320 to 331 us by GPU (100 to 97 %); 285k tokens of 8 e4m3 heads of
 // 128, groups of 5: 100 us (86 %); 250 windows of 512 over 12 fp16 heads of 64,
 // pages of 24: 69 us (77 %, bound by instructions: 8 columns for one head).
 
