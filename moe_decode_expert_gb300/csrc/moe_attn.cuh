@@ -835,8 +835,9 @@ __global__ void __launch_bounds__(Shape<QT, F8, DP, NT, TEAM>::kThreads, (Shape<
               mma<S::kBf16>(o[nt][dm], f[0], f[1], f[2], f[3], pf[mt][nt][0], pf[mt][nt][1]);
             if constexpr (S::kBf16) {
               // A weight's low term is zero or of either sign: an infinite value times it
-              // would turn the high term's infinity into NaN.  (0 to 2 % of a call's time;
-              // a high term rounded down, with a positive rest, costs none but a bit of it.)
+              // would turn the high term's infinity into NaN.  (0 to 2 % of a call's time:
+              // 64 sequences up to 32k 328.5 us with and without, 100 of up to 700 over groups
+              // of 20 heads of 64 15.25 against 14.97.)
 #pragma unroll
               for (int i = 0; i < 4; ++i) f[i] = finite2(f[i]);
 #pragma unroll
