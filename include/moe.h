@@ -384,6 +384,94 @@ MOE_API int32_t moe_attention_form(const moe_kv_cache_t* cache, int32_t B, int32
 MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* a, void* ws,
                                          size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit projections and the end of a decode step: rows and weights quantised
+ * to e4m3 with fp32 scales of 128 columns (moe_add_rmsnorm with group 128
+ * writes the same form), the product of two such matrices, and the drawing of
+ * a token from each row of logits.  Conventions as above; the extents in bytes
+ * of an output, from its first to its last element, overlap no other tensor's.
+ * ------------------------------------------------------------------------ */
+
+/* Quantisation: x [T, H] in blocks of `rows` (1 or 128) rows by 128 columns,
+ *   s = max(max |x|, 2^-96) / 448 over the block;  out = e4m3(x / s)
+ * (the last block of a row or column may be smaller).  rows = 1 is the form of
+ * activations, rows = 128 that of weights.  A NaN makes its block's scale and
+ * values NaN; an infinity its scale infinite, itself NaN and the others zero.
+ * Any T >= 0, H >= 1 and row strides >= H; rows whose pointers and strides are
+ * multiples of 16 bytes (8 for out) with H % 8 == 0 take the wide loads.
+ * Limit: ceil(T / rows) * ceil(H / 128) below 2^31. */
+typedef struct moe_quant {
+  const void* x; /* [T, H] dtype                                             */
+  void* out;     /* [T, H] MOE_E4M3                                          */
+  float* scales; /* [ceil(T / rows), ceil(H / 128)]                          */
+  int64_t x_stride, out_stride; /* between rows                              */
+  int32_t T, H;
+  int32_t rows;  /* 1 or 128                                                 */
+  int32_t dtype; /* MOE_F16 or MOE_BF16                                      */
+} moe_quant_t;
+
+MOE_API moe_status_t moe_quantize_e4m3(const moe_quant_t* q, void* stream);
+
+/* Product of quantised rows with a quantised weight:
+ *   out[t][n] = sum_b xs[t][b] ws[n / 128][b] sum_{k in block b} x[t][k] w[n][k]
+ * over the blocks b of 128 columns (the last may be smaller), each block's sum
+ * in fp32 on the tensor cores, the sum over blocks in fp32 in the order of k
+ * (in up to 8 parts of it when rows are few, added in order), rounded once to
+ * out_dtype.  Results do not depend on timing.
+ * Any M, N >= 0, K >= 1; x and w begin on 16 bytes and their row strides are
+ * multiples of 16 elements; what lies between the rows is not
+ * read.  out has any strides >= N between rows.  Scales are any floats: a NaN
+ * or infinity in a row, a weight row or a scale reaches only what it is a
+ * factor of.  Limit: ceil(M / 16) * ceil(N / 128) below 2^28.
+ * ws: any workspace of this library (only its status word is used: a wait that
+ * ran out is recorded there, MOE_ERR_TIMEOUT from moe_query_status). */
+typedef struct moe_linear {
+  const void* x;         /* [M, K] MOE_E4M3                                  */
+  const float* x_scales; /* [M, ceil(K / 128)]                               */
+  const void* w;         /* [N, K] MOE_E4M3                                  */
+  const float* w_scales; /* [ceil(N / 128), ceil(K / 128)]                   */
+  void* out;             /* [M, N] out_dtype                                 */
+  int64_t x_stride, w_stride, out_stride; /* between rows                    */
+  int32_t M, N, K;
+  int32_t out_dtype; /* MOE_F16, MOE_BF16 or MOE_F32                         */
+} moe_linear_t;
+
+MOE_API moe_status_t moe_linear_e4m3(const moe_linear_t* l, void* ws, size_t ws_bytes, void* stream);
+
+/* One token from each row of logits l [V], by its own parameters and one given
+ * random number u in [0, 1):
+ *   w_i = exp((l_i - max l) / temperature)          ranked by (l desc, i asc)
+ *   top_k: the first top_k ranks stay;
+ *   top_p: of those the rank r stays while the sum of w over the ranks before
+ *          it is below top_p times the sum over all of them;
+ *   min_p: and while w_i >= min_p;
+ *   token = the first i, in the order of i, at which the sum of the staying w
+ *   exceeds u times their whole sum;  logprob = ln(w_token / whole sum).
+ * Rank 0 always stays.  temperature <= 0 takes rank 0 (logprob 0); top_k <= 0
+ * or >= V, top_p >= 1 and min_p <= 0 ask for nothing; u is clamped to [0, 1);
+ * a NaN parameter asks for nothing (a NaN temperature is 1, a NaN u is 0).
+ * Logits of -infinity and NaN are never drawn; +infinite ones share the row.
+ * A row without any other gives token -1 and logprob -infinity.
+ * Weights are fixed-point numbers, accurate to 2^-28 relative and to 2^-44 of the
+ * row's largest (smaller ones are never drawn), and their sums are exact: results
+ * depend neither on timing nor on the other rows.
+ * Any B >= 0, 1 <= V <= 393216 and any row stride >= V. */
+typedef struct moe_sampling {
+  const void* logits;       /* [B, V] dtype                                  */
+  const float* uniforms;    /* [B]                                           */
+  const float* temperature; /* [B], or NULL: 1                               */
+  const int32_t* top_k;     /* [B], or NULL                                  */
+  const float* top_p;       /* [B], or NULL                                  */
+  const float* min_p;       /* [B], or NULL                                  */
+  int64_t* tokens;          /* [B]                                           */
+  float* logprobs;          /* [B], or NULL                                  */
+  int64_t logits_stride;    /* between rows                                  */
+  int32_t B, V;
+  int32_t dtype; /* MOE_F16, MOE_BF16 or MOE_F32                             */
+} moe_sampling_t;
+
+MOE_API moe_status_t moe_sample(const moe_sampling_t* s, void* stream);
+
 /* Synchronise `stream`, then read and clear the device status word of `ws`
  * (ws == NULL: the word in the built-in array of moe_decode_forward_noalloc on
  * the current device).  Returns MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE (or

@@ -37,7 +37,8 @@ EXPORTS = ("moe_abi_version", "moe_workspace_bytes", "moe_workspace_init", "moe_
            "moe_decode_forward", "moe_grouped_forward", "moe_query_status", "moe_last_error",
            "moe_get_stats", "moe_reset_stats", "moe_set_wait_timeout_ns", "moe_test_wait_timeout",
            "moe_decode_forward_noalloc", "moe_sum_partials", "moe_add_rmsnorm", "moe_rope_append",
-           "moe_attention_workspace_bytes", "moe_attention_form", "moe_paged_attention")
+           "moe_attention_workspace_bytes", "moe_attention_form", "moe_paged_attention", "moe_quantize_e4m3",
+           "moe_linear_e4m3", "moe_sample")
 
 
 class MoeError(RuntimeError):
@@ -138,6 +139,9 @@ def _load():
         "moe_attention_workspace_bytes": ([ctypes.c_char_p, i32], sz),
         "moe_attention_form": ([ctypes.c_char_p, i32, i32, i32, i32], i32),
         "moe_paged_attention": ([ctypes.c_char_p, ctypes.c_char_p, vp, sz, vp], ctypes.c_int),
+        "moe_quantize_e4m3": ([ctypes.c_char_p, vp], ctypes.c_int),
+        "moe_linear_e4m3": ([ctypes.c_char_p, vp, sz, vp], ctypes.c_int),
+        "moe_sample": ([ctypes.c_char_p, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -344,6 +348,10 @@ _NORM_T = struct.Struct("@6P4q5if")
 _CACHE_T = struct.Struct("@4P6q5i0q")
 _ROPE_T = struct.Struct("@9P8q5if0q")
 _ATTN_T = struct.Struct("@5P5q5if0q")
+# and of moe_quant_t, moe_linear_t and moe_sampling_t.
+_QUANT_T = struct.Struct("@3P2q4i0q")
+_LINEAR_T = struct.Struct("@5P3q4i0q")
+_SAMPLING_T = struct.Struct("@8Pq3i0q")
 
 
 # A decode step makes these calls dozens of times per token and their kernels
@@ -606,6 +614,93 @@ def moe_paged_attention(cache: MoeKvCache, q, block_table, seq_lens, out, ws, sc
                         bs[0], B, hq, pages, _int32(window, "window"), code,
                         D ** -0.5 if scale is None else _fp32(scale, "scale"))
     rc = (_lib or _load()).moe_paged_attention(cache._c, args, ws_p, ws_bytes, _launch_stream(dev, stream))
+    if rc:
+        _check(rc)
+
+
+# ---------------------------- 8-bit projections and the end of a decode step
+def moe_quantize_e4m3(x, out, scales, rows=1, stream=None):
+    """``x`` [T, H] (float16 or bfloat16) to float8_e4m3fn ``out`` [T, H] with one
+    fp32 scale per block of ``rows`` (1: activations, 128: weights) by 128 elements
+    in ``scales`` [ceil(T / rows), ceil(H / 128)].  Rows may be strided."""
+    shape, dt, dev = _tensor(x, "x").shape, x.dtype, x.get_device()
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected [T, H]")
+    T, H = shape
+    code = _FLOATS.get(dt)
+    if code is None:
+        raise ValueError(f"x: dtype {dt}, expected float16 or bfloat16")
+    rows = _int32(rows, "rows")
+    if rows not in (1, 128):
+        raise ValueError("rows must be 1 or 128")
+    xs = _rows(x, "x", shape, dt, dev)[0]
+    os_ = _rows(out, "out", shape, torch.float8_e4m3fn, dev)[0]
+    s = _flat(scales, "scales", (-(-T // rows), -(-H // 128)), torch.float32, dev)
+    args = _QUANT_T.pack(x.data_ptr(), out.data_ptr(), s, xs, os_, _int32(T, "T"), _int32(H, "H"), rows, code)
+    rc = (_lib or _load()).moe_quantize_e4m3(args, _launch_stream(dev, stream))
+    if rc:
+        _check(rc)
+
+
+def alloc_status_workspace(device) -> torch.Tensor:
+    """The smallest workspace: the status word that moe_query_status reads, for
+    operators that need no other (moe_linear_e4m3, moe_rope_append)."""
+    ws = torch.zeros(512, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + 256]
+
+
+def moe_linear_e4m3(x, x_scales, w, w_scales, out, ws, stream=None):
+    """``out`` [M, N] (float16, bfloat16 or float32) = ``x`` [M, K] times ``w``
+    [N, K] transposed, both float8_e4m3fn: ``x`` with ``x_scales`` [M, ceil(K /
+    128)], ``w`` with ``w_scales`` [ceil(N / 128), ceil(K / 128)] fp32, as
+    moe_quantize_e4m3 (rows 1 and 128) and moe_add_rmsnorm (group 128) leave
+    them.  Row strides of x and w are multiples of 16; those of out are free."""
+    dev = _tensor(x, "x").get_device()
+    if x.dim() != 2 or _tensor(w, "w").dim() != 2:
+        raise ValueError(f"x and w: shapes {tuple(x.shape)} and {tuple(w.shape)}, expected [M, K] and [N, K]")
+    (M, K), N = x.shape, w.shape[0]
+    code = _DT_CODE.get(_tensor(out, "out").dtype)
+    if code is None:
+        raise ValueError(f"out: dtype {out.dtype}, expected float16, bfloat16 or float32")
+    kb = -(-K // 128)
+    xs = _rows(x, "x", (M, K), torch.float8_e4m3fn, dev)[0]
+    wst = _rows(w, "w", (N, K), torch.float8_e4m3fn, dev)[0]
+    os_ = _rows(out, "out", (M, N), out.dtype, dev)[0]
+    xsc = _flat(x_scales, "x_scales", (M, kb), torch.float32, dev)
+    wsc = _flat(w_scales, "w_scales", (-(-N // 128), kb), torch.float32, dev)
+    if _tensor(ws, "ws").get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on {x.device} is required")
+    args = _LINEAR_T.pack(x.data_ptr(), xsc, w.data_ptr(), wsc, out.data_ptr(), xs, wst, os_, _int32(M, "M"),
+                          _int32(N, "N"), _int32(K, "K"), code)
+    rc = (_lib or _load()).moe_linear_e4m3(args, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                           _launch_stream(dev, stream))
+    if rc:
+        _check(rc)
+
+
+def moe_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None,
+               stream=None):
+    """One token per row of ``logits`` [B, V] (float16, bfloat16 or float32) into
+    ``tokens`` [B] int64, drawn with the given ``uniforms`` [B] fp32 in [0, 1) from
+    what each row's ``temperature``, ``top_p``, ``min_p`` [B] fp32 and ``top_k`` [B]
+    int32 leave (None: temperature 1, no filter), and its log-probability there
+    into ``logprobs`` [B] fp32.  A row of -infinity gives token -1."""
+    shape, dev = _tensor(logits, "logits").shape, logits.get_device()
+    if len(shape) != 2 or not shape[1]:
+        raise ValueError(f"logits: shape {tuple(shape)}, expected [B, V]")
+    B, V = shape
+    code = _DT_CODE.get(logits.dtype)
+    if code is None:
+        raise ValueError(f"logits: dtype {logits.dtype}, expected float16, bfloat16 or float32")
+    ls = _rows(logits, "logits", shape, logits.dtype, dev)[0]
+    f32 = lambda t, name: 0 if t is None else _flat(t, name, (B,), torch.float32, dev)  # noqa: E731
+    args = _SAMPLING_T.pack(
+        logits.data_ptr(), _flat(uniforms, "uniforms", (B,), torch.float32, dev), f32(temperature, "temperature"),
+        0 if top_k is None else _flat(top_k, "top_k", (B,), torch.int32, dev), f32(top_p, "top_p"),
+        f32(min_p, "min_p"), _flat(tokens, "tokens", (B,), torch.int64, dev), f32(logprobs, "logprobs"), ls,
+        _int32(B, "B"), _int32(V, "V"), code)
+    rc = (_lib or _load()).moe_sample(args, _launch_stream(dev, stream))
     if rc:
         _check(rc)
 

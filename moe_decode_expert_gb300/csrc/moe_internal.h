@@ -151,6 +151,24 @@ moe_status_t launch_tc_router(const moe_cfg_t& c, const void* x, const void* rou
 moe_status_t launch_tc_passes(const moe_cfg_t& c, const BlockPtrs& p, uint8_t* ws, const WsLayout& L, int32_t T,
                               int fused_nsplit, cudaStream_t st);
 
+// Bytes [at, at + bytes) that a tensor's elements lie in, and whether two such ranges meet.
+struct Span {
+  uintptr_t at;
+  int64_t bytes;
+};
+inline bool meet(const Span& a, const Span& b) {
+  return a.at < b.at + static_cast<uintptr_t>(b.bytes) && b.at < a.at + static_cast<uintptr_t>(a.bytes);
+}
+// The range of `rows` rows of `width` elements of `size` bytes, `stride` elements apart; false
+// for rows further apart than any device memory (2^46 elements in all), whose addresses may
+// not fit 63 bits.
+inline bool row_span(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t size, Span& s) {
+  const int64_t most = int64_t(1) << 46;
+  if (rows > 1 && stride > most / (rows - 1)) return false;
+  s = Span{reinterpret_cast<uintptr_t>(p), ((rows - 1) * stride + width) * size};
+  return true;
+}
+
 // Serialises every read-then-raise of a kernel attribute (any host thread).
 std::mutex& attr_mutex();
 

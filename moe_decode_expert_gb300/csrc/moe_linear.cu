@@ -1,0 +1,707 @@
+// moe_linear.cu — product of e4m3 rows with an e4m3 weight, both with fp32 scales
+// of blocks of 128 (x: per row and 128 columns; w: per 128 x 128), on tcgen05.
+//
+//   out[t][n] = sum_b xs[t][b] ws[n / 128][b] P_b[t][n],
+//   P_b[t][n] = sum_{k in block b} x[t][k] w[n][k]
+//
+// A block's product P_b is four tensor-core steps of 32 into an fp32 accumulator in
+// tensor memory that starts at zero; an epilogue warp reads it and adds it, times
+// its two scales, to fp32 sums in registers while the next block's product is made
+// in another accumulator.  A block of K is 128 bytes, one row of the 128-byte
+// swizzle, so a stage of the ring is one block of both operands.
+
+#include <algorithm>
+
+#include "moe_common.cuh"
+#include "moe_internal.h"
+#include "moe_tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBlock = 128;               // columns (and weight rows) of a scale
+constexpr uint32_t kTile = 128 * kBlock;  // bytes of 128 rows of a block
+constexpr int kFewRows = 128;             // up to here the weight is the MMA's M
+
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A and B e4m3, both
+// K-major, M = 128, N.
+template <int N>
+constexpr uint32_t idesc_e4m3() {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Fetch a tile into L2 (may come before griddepcontrol.wait: L2 is where writes meet).
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
+  if (dt == MOE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Cluster-wide barrier in two halves; every thread of every CTA takes part in both.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The address in CTA `rank`'s shared memory that `addr` is in this one's.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Copy of this CTA's shared memory into another's, counted on a barrier there.
+__device__ __forceinline__ void bulk_to_peer(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Writes of this thread to shared memory, made visible to copies.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ============================================================ few rows
+// The weight's rows are the MMA's M (128 per tile) and NT tokens its N, so the
+// weight, the larger operand, is streamed once for them.  S CTAs of a cluster share
+// a tile's blocks of K; each then adds the S partial sums (in the order of K) of 1 / S
+// of the columns, which the others send it as one copy each.  (Plain stores to
+// another CTA's shared memory took 0.35 us per column.)
+template <int NT>
+struct Few {
+  static constexpr uint32_t kStage = kTile + NT * kBlock;
+  static constexpr int kMaxStages = NT == 128 ? 4 : 5;
+  static constexpr int kAcc = NT <= 32 ? 4 : 2;  // accumulators in tensor memory
+  static constexpr uint32_t kCols = NT * kAcc;
+  static constexpr int kChunk = 16;       // blocks whose scales are staged at a time
+  static constexpr int kPitch = NT + 4;   // floats per block of staged scales
+  static constexpr uint32_t kScales = kChunk * kPitch * 4;
+  // Of a CTA's shared memory: the ring, one or two chunks of scales, and the others' sums of
+  // its columns.  At least the share that its columns are of the SM's 512, so that no CTA
+  // waits for columns that another holds.
+  static size_t smem(int stages, int nkb, int S) {
+    const size_t n = stages * kStage + (nkb > kChunk ? 2 : 1) * kScales + (S > 1 ? (NT + S) * 512 : 0) + 1024;
+    const size_t least = static_cast<size_t>(kCols) * 227 * 1024 / 512;
+    return n < least ? least : n;
+  }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
+    linear_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
+                      moe_linear_t a, int KB, int S, int mtiles, int stages, Control* ctrl, uint64_t timeout) {
+  using F = Few<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* scales = reinterpret_cast<float*>(smem + stages * F::kStage);
+  __shared__ __align__(8) uint64_t full[F::kMaxStages], empty[F::kMaxStages], tfull[F::kAcc], tempty[F::kAcc], done, inbox;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile int s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x % S);
+  const int tile = static_cast<int>(blockIdx.x / S);
+  const int m0 = tile % mtiles * NT, nt = tile / mtiles, n0 = nt * 128;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / S);
+  const int nkb = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / S) - kb0;
+  float* parts = scales + ((KB + S - 1) / S > F::kChunk ? 2 : 1) * (F::kScales / 4);
+  const int width = (NT + S - 1) / S;  // columns whose sums this CTA adds
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < F::kAcc; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 4); }
+    mbar_init(&done, 1);
+    mbar_init(&inbox, 1);
+    mbar_fence_init();
+    s_abort = 0;
+    // (others' sums of this CTA's columns that there are tokens for)
+    if (S > 1)
+      mbar_arrive_expect_tx(&inbox, static_cast<uint32_t>(max(min(min(NT, a.M - m0) - rank * width, width), 0) * (S - 1)) * 512u);
+    tensormap_prefetch(&mapW);
+    tensormap_prefetch(&mapX);
+    for (int i = 0; i < min(nkb, stages); ++i) tma_prefetch_2d(&mapW, (kb0 + i) * kBlock, n0);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_s, F::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // (after the allocation: a CTA of the next kernel that got its columns first would wait for
+  // this one, and this one for those columns)
+  pdl_launch_dependents();
+  if (S > 1) cluster_arrive();
+  pdl_wait();
+  const uint32_t tbase = tmem_base_s;
+
+  if (warp == 0) {
+    if (lane == 0) {  // ---------------------------------------------- TMA producer
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+      for (int i = 0; i < nkb; ++i) {
+        if (!tc_wait_polled(&empty[stage], phase ^ 1u, timeout, &s_abort)) {
+          s_abort = 1;
+          report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+          break;
+        }
+        uint8_t* st = smem + stage * F::kStage;
+        mbar_arrive_expect_tx(&full[stage], F::kStage);
+        tma_load_2d(st, &mapW, &full[stage], (kb0 + i) * kBlock, n0);
+        tma_load_2d(st + kTile, &mapX, &full[stage], (kb0 + i) * kBlock, m0);
+        issued_mask |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
+      }
+      // let every copy this thread issued land before the CTA exits
+      for (int s = 0; s < stages; ++s)
+        if (issued_mask & (1u << s)) mbar_wait_until(&full[s], (issued_phase >> s) & 1u, global_ns() + timeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {  // ---------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = idesc_e4m3<NT>();
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < nkb; ++i) {
+        const int b = i % F::kAcc;
+        if (!tc_wait_polled(&tempty[b], ((i / F::kAcc) & 1) ^ 1u, timeout, &s_abort) ||
+            !tc_wait_polled(&full[stage], phase, timeout, &s_abort)) {
+          s_abort = 1;
+          report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sA = smem_u32(smem + stage * F::kStage), sB = sA + kTile;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_e4m3(tbase + static_cast<uint32_t>(b * NT), sw128_desc(sA + 32 * k), sw128_desc(sB + 32 * k), idesc, k != 0);
+        tc_commit(&empty[stage]);
+        tc_commit(&tfull[b]);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
+      }
+      tc_commit(&done);  // completes once every MMA issued above has completed
+      mbar_wait_until(&done, 0, global_ns() + timeout);
+    }
+    __syncwarp();
+  } else {  // ---------------------------------------------------- epilogue, 128 threads
+    const int q = warp & 3;
+    const int row = 32 * q + lane;      // weight row of the tile = TMEM lane
+    const int etid = threadIdx.x - 64;  // 0..127
+    constexpr int kPer = NT * F::kChunk / 128, kStep = NT == 32 || NT == 64 ? 32 : 16;
+    float acc[NT];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
+    float next[kPer];
+    // products of both scales for blocks [c * kChunk, ..), zero beyond M and the last block
+    const auto fetch = [&](int chunk) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int at = etid + 128 * u, t = at / F::kChunk, i = chunk * F::kChunk + at % F::kChunk;
+        next[u] = 0.0f;
+        if (i < nkb && m0 + t < a.M)
+          next[u] = a.x_scales[static_cast<int64_t>(m0 + t) * KB + kb0 + i] *
+                    a.w_scales[static_cast<int64_t>(nt) * KB + kb0 + i];
+      }
+    };
+    const auto stage_scales = [&](int buf) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int at = etid + 128 * u;
+        scales[(buf * F::kChunk + at % F::kChunk) * F::kPitch + at / F::kChunk] = next[u];
+      }
+    };
+    fetch(0);
+    bool ok = true;
+    for (int i = 0; i < nkb; ++i) {
+      const int chunk = i / F::kChunk, in = i % F::kChunk;
+      if (in == 0) {
+        stage_scales(chunk & 1);
+        named_bar_sync(1, 128);  // (also: every warp is past the chunk before the last, whose place this was)
+        if ((chunk + 1) * F::kChunk < nkb) fetch(chunk + 1);
+      }
+      const int b = i % F::kAcc;
+      // (a wait that ran out leaves the loop running without it, so that all warps meet at the barriers)
+      ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], (i / F::kAcc) & 1, timeout, &s_abort));
+      if (ok) {
+        tc_fence_after();
+        const float4* sc = reinterpret_cast<const float4*>(scales + ((chunk & 1) * F::kChunk + in) * F::kPitch);
+        const uint32_t ta = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * NT);
+#pragma unroll
+        for (int c0 = 0; c0 < NT; c0 += kStep) {
+          uint32_t v[kStep];
+          if constexpr (kStep == 32) tmem_ld32_issue(ta + c0, v);
+          else tmem_ld16_issue(ta + c0, v);
+          tmem_ld_wait();
+          tmem_ld_tie(v);
+          if (c0 + kStep == NT) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < kStep / 4; ++j) {
+            const float4 s = sc[c0 / 4 + j];
+            acc[c0 + 4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[c0 + 4 * j]);
+            acc[c0 + 4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[c0 + 4 * j + 1]);
+            acc[c0 + 4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[c0 + 4 * j + 2]);
+            acc[c0 + 4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[c0 + 4 * j + 3]);
+          }
+        }
+      } else {
+        s_abort = 1;
+      }
+    }
+    if (!ok && lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+    const int n = n0 + row;
+    if (S == 1) {
+      if (n < a.N) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if (m0 + c < a.M) store_out(a.out, static_cast<size_t>((m0 + c) * a.out_stride + n), acc[c], a.out_dtype);
+      }
+    } else {
+      // into the ring, which nothing fills or reads any more (every product was waited for)
+      float* own = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int c = 0; c < NT; ++c) own[c * 128 + row] = acc[c];
+      fence_async();
+      named_bar_sync(1, 128);
+      cluster_wait();  // every CTA of the cluster runs
+      const int cols = min(NT, a.M - m0);  // with tokens
+      if (etid < S && etid != rank && !s_abort) {
+        const int many = min(cols - etid * width, width);
+        if (many > 0)
+          bulk_to_peer(peer_addr(smem_u32(parts + rank * width * 128), etid), own + etid * width * 128, many * 512u,
+                       peer_addr(smem_u32(&inbox), etid));
+      }
+      const bool here = tc_wait_polled(&inbox, 0, timeout, &s_abort);
+      if (!here) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+      const int c0 = rank * width, many = here && n < a.N ? min(cols - c0, width) : 0;
+      for (int j0 = 0; j0 < many; j0 += 8) {  // 8 columns at a time: a load's latency per part, not per value
+        float sum[8] = {};
+        for (int r = 0; r < S; ++r) {
+          const float* from = (r == rank ? own + c0 * 128 : parts + r * width * 128) + j0 * 128 + row;
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = j0 + j < many ? from[j * 128] : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < many)
+            store_out(a.out, static_cast<size_t>((m0 + c0 + j0 + j) * a.out_stride + n), sum[j], a.out_dtype);
+      }
+    }
+  }
+  if (S > 1) {
+    if (warp < 2) cluster_wait();
+    cluster_arrive();  // this CTA's copies have arrived, and it is not left before those it sent have
+    cluster_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, F::kCols);
+  }
+}
+
+// =========================================================== many rows
+// Tiles of 256 tokens by 256 weight rows, each of a pair of CTAs: the tokens are the
+// MMA's M (128 per CTA), the weight rows its N, and each CTA stages half of both (32 KB
+// a block), so that a pair reads every byte once.  The sums of a token's 256 columns
+// are in 4 threads' registers, 64 each; 16 warps read a block's product from tensor
+// memory (two accumulators of 256 columns) while the next is made.
+struct Many {
+  static constexpr uint32_t kStage = 2 * kTile;
+  static constexpr int kStages = 5;
+  static constexpr int kWarps = 16;  // of the epilogue
+  static constexpr int kThreads = 128 + 32 * kWarps;
+  // registers per thread: 96 at launch (five warps on each of the SM's quarters); the first four
+  // warps give up what the others take, 128 * 56 + 512 * 104 <= 640 * 96
+  static constexpr int kChunk = 16;                        // blocks whose scales are staged at a time,
+  static constexpr int kScales = kChunk * (128 + 2);       // floats: the rows' and the two weight blocks'
+  static constexpr uint32_t kTurn = 32 * 64;               // bytes a warp turns its results in
+  static constexpr size_t kSmem = kStages * kStage + 2 * kScales * 4 + kWarps * kTurn + 1024;
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// (Released to the CTA only: what it orders, reads of tensor memory, the fence before it has
+// ordered; a release to the cluster waits for the thread's memory operations, 335 us against 212
+// for 8192 x 5120 x 4096.)
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A warp's 32 rows of 64 results to memory, 64 bytes of each row at a time: through shared
+// memory (16-byte pieces, their order turned by the row against bank conflicts), so that
+// neighbouring lanes write neighbouring bytes.  SIZE: bytes of an output.
+template <int SIZE>
+__device__ __forceinline__ void many_store(const moe_linear_t& a, const float (&acc)[64], uint8_t* turn, int m0, int n0,
+                                           int lane, int wide) {
+  constexpr int kCols = 64 / SIZE, kPiece = 16 / SIZE;  // of a pass, of a piece
+#pragma unroll
+  for (int c0 = 0; c0 < 64; c0 += kCols) {
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (SIZE == 4) w[j] = __float_as_uint(acc[c0 + 4 * p + j]);
+        else w[j] = pack2(a.out_dtype, acc[c0 + 8 * p + 2 * j], acc[c0 + 8 * p + 2 * j + 1]);
+      }
+      *reinterpret_cast<uint4*>(turn + lane * 64 + ((p ^ (lane >> 1)) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int n = n0 + c0;
+    if (wide && n + kCols <= a.N) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), p = lane & 3;
+        const uint4 v = *reinterpret_cast<const uint4*>(turn + r * 64 + ((p ^ (r >> 1)) & 3) * 16);
+        if (m0 + r < a.M)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + ((m0 + r) * a.out_stride + n + p * kPiece) * SIZE) = v;
+      }
+    } else {
+      for (int i = lane; i < 32 * kCols; i += 32) {
+        const int r = i / kCols, c = i % kCols;
+        const uint8_t* at = turn + r * 64 + ((c / kPiece ^ (r >> 1)) & 3) * 16 + c % kPiece * SIZE;
+        if (m0 + r < a.M && n + c < a.N) {
+          uint8_t* o = static_cast<uint8_t*>(a.out) + ((m0 + r) * a.out_stride + n + c) * SIZE;
+          if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(at);
+          else *reinterpret_cast<uint16_t*>(o) = *reinterpret_cast<const uint16_t*>(at);
+        }
+      }
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
+    linear_many_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
+                       moe_linear_t a, int KB, int mtiles, int tiles, int wide, Control* ctrl, uint64_t timeout) {
+  using G = Many;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], tfull[2], tempty[2], done;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ volatile int s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x & 1u);  // in the pair; 0 issues the MMAs
+  const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * G::kWarps); }
+    mbar_init(&done, 1);
+    mbar_fence_init();
+    s_abort = 0;
+    tensormap_prefetch(&mapX);
+    tensormap_prefetch(&mapW);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_s)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // both CTAs' barriers are set up before either signals the other's
+  cluster_wait();
+  tc_fence_after();
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint32_t tbase = tmem_base_s;
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == 0) {
+    if (lane == 0) {  // ---------------------------------------------- TMA producer
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+      for (int t = first; t < tiles && !s_abort; t += step) {
+        const int m0 = t % mtiles * 256 + rank * 128, n0 = t / mtiles * 256 + rank * 128;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!tc_wait_polled(&empty[stage], phase ^ 1u, timeout, &s_abort)) {
+            s_abort = 1;
+            report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+            break;
+          }
+          uint8_t* st = smem + stage * G::kStage;
+          const uint32_t bar = peer_addr(smem_u32(&full[stage]), 0);  // rank 0's, for both
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * G::kStage);
+          tma_load_2d_pair(st, &mapX, bar, kb * kBlock, m0);
+          tma_load_2d_pair(st + kTile, &mapW, bar, kb * kBlock, n0);
+          issued_mask |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // let every copy of the pair land before a CTA exits (rank 1 leaves after rank 0)
+      if (rank == 0)
+        for (int s = 0; s < G::kStages; ++s)
+          if (issued_mask & (1u << s)) mbar_wait_until(&full[s], (issued_phase >> s) & 1u, global_ns() + timeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {  // --------------------------------- MMA issuer
+      constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(256 >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
+      int stage = 0, b = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step)
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!tc_wait_polled(&tempty[b], bphase ^ 1u, timeout, &s_abort) ||
+              !tc_wait_polled(&full[stage], phase, timeout, &s_abort)) {
+            s_abort = 1;
+            report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sA = smem_u32(smem + stage * G::kStage), sB = sA + kTile;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3_pair(tbase + static_cast<uint32_t>(b * 256), sw128_desc(sA + 32 * k), sw128_desc(sB + 32 * k), idesc,
+                          k != 0);
+          tc_commit_pair(&empty[stage]);
+          tc_commit_pair(&tfull[b]);
+          if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+          b ^= 1;
+          bphase ^= b == 0;
+        }
+      // completes once every MMA issued above has completed
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done))
+                   : "memory");
+      mbar_wait_until(&done, 0, global_ns() + timeout);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {  // ------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int q = warp & 3, g = (warp - 4) >> 2;  // quarter of the TMEM lanes, quarter of the columns
+    const int etid = threadIdx.x - 128;
+    const uint32_t lane0 = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(64 * g);
+    const uint32_t free_bar = peer_addr(smem_u32(&tempty[0]), 0);
+    float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage);
+    uint8_t* turn = reinterpret_cast<uint8_t*>(scales + 2 * G::kScales) + (warp - 4) * G::kTurn;
+    // A chunk's scales go through registers one chunk ahead: 4 blocks of a row per thread, and
+    // one of a weight block in 32 of them.  (Loaded by each thread for its own row they missed
+    // L1, which 128 rows 4 KB / 32 apart overflow: 1.15 us per block.)
+    float next[4], next_w = 0.0f;
+    const auto fetch = [&](int t, int kb0) {
+      const int m = min(t % mtiles * 256 + rank * 128 + (etid >> 2), a.M - 1);
+      const int kb = kb0 + (etid & 3) * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) next[j] = kb + j < KB ? a.x_scales[static_cast<int64_t>(m) * KB + kb + j] : 0.0f;
+      if (etid < 2 * G::kChunk && kb0 + (etid >> 1) < KB)
+        next_w = a.w_scales[static_cast<int64_t>(min(t / mtiles * 256 + 128 * (etid & 1), a.N - 1) / 128) * KB + kb0 +
+                            (etid >> 1)];
+    };
+    int b = 0, buf = 0;
+    uint32_t bphase = 0;
+    bool ok = true;
+    if (first < tiles) fetch(first, 0);
+    for (int t = first; t < tiles; t += step) {
+      float acc[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) acc[c] = 0.0f;
+      for (int kb0 = 0; kb0 < KB; kb0 += G::kChunk) {
+        float* sc = scales + buf * G::kScales;
+        buf ^= 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[((etid & 3) * 4 + j) * 128 + (etid >> 2)] = next[j];
+        if (etid < 2 * G::kChunk) sc[G::kChunk * 128 + etid] = next_w;
+        named_bar_sync(1, 32 * G::kWarps);  // (also: every warp is past the chunk before the last, whose place this was)
+        if (kb0 + G::kChunk < KB) fetch(t, kb0 + G::kChunk);
+        else if (t + step < tiles) fetch(t + step, 0);
+        const int n = min(G::kChunk, KB - kb0);
+        for (int i = 0; i < n; ++i) {
+          // (a wait that ran out leaves the loops running without it, so that all warps meet at the barriers)
+          ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], bphase, timeout, &s_abort));
+          if (!ok) {
+            s_abort = 1;
+            continue;
+          }
+          tc_fence_after();
+          const float s = sc[i * 128 + 32 * q + lane] * sc[G::kChunk * 128 + 2 * i + (g >> 1)];
+          const uint32_t ta = lane0 + static_cast<uint32_t>(b * 256);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t v[16];
+            tmem_ld16_issue(ta + 16 * h, v);
+            tmem_ld_wait();
+            tmem_ld_tie(v);
+            if (h == 3) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[16 * h + j] = fmaf(__uint_as_float(v[j]), s, acc[16 * h + j]);
+          }
+          b ^= 1;
+          bphase ^= b == 0;
+        }
+      }
+      if (!ok) continue;
+      const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * 256 + 64 * g;
+      if (m0 >= a.M || n0 >= a.N) continue;
+      if (a.out_dtype == MOE_F32) many_store<4>(a, acc, turn, m0, n0, lane, wide);
+      else many_store<2>(a, acc, turn, m0, n0, lane, wide);
+    }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // neither CTA's memory goes while the other's MMAs or arrivals may touch it
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512u) : "memory");
+  }
+}
+
+// ================================================================ host
+// 2-D K-major map of bytes: `inner` per row, `outer` rows `stride` apart; box of
+// 128 x box_rows, 128-byte swizzle; zeros outside.
+bool byte_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_rows) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer}, strides[1] = {stride};
+  cuuint32_t box[2] = {kBlock, box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+moe_status_t launch_few(const moe_linear_t& l, int KB, Control* ctrl, cudaStream_t st) {
+  const int mtiles = (l.M - 1) / NT + 1;
+  const int64_t tiles = static_cast<int64_t>(mtiles) * ((l.N - 1) / 128 + 1);
+  const int S = static_cast<int>(tiles >= sm_count() ? 1 : std::min<int64_t>({4, (KB + 1) / 2, sm_count() / tiles}));
+  const int nkb = (KB + S - 1) / S, stages = std::min(Few<NT>::kMaxStages, std::max(nkb, 2));
+  CUtensorMap mw, mx;
+  if (!byte_map(&mw, l.w, l.K, l.N, l.w_stride, 128) || !byte_map(&mx, l.x, l.K, l.M, l.x_stride, NT))
+    return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
+  const size_t smem = Few<NT>::smem(stages, nkb, S);
+  if (raise_smem_limit(linear_few_kernel<NT>, smem) != cudaSuccess) return check_launch("linear_few_kernel (smem)");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(S), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, linear_few_kernel<NT>, mw, mx, l, KB, S, mtiles, stages, ctrl, wait_timeout_ns()) != cudaSuccess)
+    return check_launch("linear_few_kernel");
+  stat_kernels(1);
+  return MOE_OK;
+}
+
+moe_status_t launch_many(const moe_linear_t& l, int KB, Control* ctrl, cudaStream_t st) {
+  const int mtiles = (l.M - 1) / 256 + 1;
+  const int tiles = mtiles * ((l.N - 1) / 256 + 1);
+  CUtensorMap mx, mw;
+  if (!byte_map(&mx, l.x, l.K, l.M, l.x_stride, 128) || !byte_map(&mw, l.w, l.K, l.N, l.w_stride, 128))
+    return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
+  if (raise_smem_limit(linear_many_kernel, Many::kSmem) != cudaSuccess) return check_launch("linear_many_kernel (smem)");
+  const int per = l.out_dtype == MOE_F32 ? 4 : 8;
+  const int wide = (reinterpret_cast<uintptr_t>(l.out) & 15u) == 0 && l.out_stride % per == 0;
+  const int pairs = sm_count() / 2;
+  if (launch_pdl(linear_many_kernel, dim3(2 * (tiles < pairs ? tiles : pairs)), dim3(Many::kThreads), Many::kSmem, st, mx,
+                 mw, l, KB, mtiles, tiles, wide, ctrl, wait_timeout_ns()) != cudaSuccess)
+    return check_launch("linear_many_kernel");
+  stat_kernels(1);
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_linear_e4m3(const moe_linear_t* l, void* ws, size_t ws_bytes, void* stream) {
+  if (!l) return set_error(MOE_ERR_INVALID_ARG, "moe_linear_t is NULL");
+  if (l->M < 0 || l->N < 0 || l->K < 1) return set_error(MOE_ERR_INVALID_ARG, "M and N must be >= 0 and K >= 1");
+  if (l->out_dtype != MOE_F16 && l->out_dtype != MOE_BF16 && l->out_dtype != MOE_F32)
+    return set_error(MOE_ERR_UNSUPPORTED, "out_dtype must be MOE_F16, MOE_BF16 or MOE_F32");
+  if (l->M == 0 || l->N == 0) return MOE_OK;
+  if (!l->x || !l->x_scales || !l->w || !l->w_scales || !l->out)
+    return set_error(MOE_ERR_INVALID_ARG, "x / x_scales / w / w_scales / out is NULL");
+  if (!ws || ws_bytes < sizeof(Control) || reinterpret_cast<uintptr_t>(ws) % kWsAlign)
+    return set_error(MOE_ERR_WORKSPACE, "a 256-byte aligned workspace of this library is needed");
+  moe_linear_t a = *l;
+  // a single row's stride says nothing
+  if (a.M == 1) a.x_stride = (a.K + 15ll) & ~15ll, a.out_stride = a.N;
+  if (a.N == 1) a.w_stride = (a.K + 15ll) & ~15ll;
+  if (a.x_stride < a.K || a.w_stride < a.K || a.out_stride < a.N)
+    return set_error(MOE_ERR_INVALID_ARG, "row strides must be at least the rows' lengths");
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.x), w = reinterpret_cast<uintptr_t>(a.w),
+                  o = reinterpret_cast<uintptr_t>(a.out);
+  if ((x | w) & 15u) return set_error(MOE_ERR_UNSUPPORTED, "x and w must begin on 16 bytes");
+  if ((a.x_stride | a.w_stride) & 15)
+    return set_error(MOE_ERR_UNSUPPORTED, "the row strides of x and w must be multiples of 16");
+  const int size = a.out_dtype == MOE_F32 ? 4 : 2;
+  if ((o & (size - 1)) || ((reinterpret_cast<uintptr_t>(a.x_scales) | reinterpret_cast<uintptr_t>(a.w_scales)) & 3u))
+    return set_error(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+  const int KB = (a.K - 1) / kBlock + 1, nb = (a.N - 1) / 128 + 1;
+  if (((a.M - 1ll) / 16 + 1) * nb >= int64_t(1) << 28)
+    return set_error(MOE_ERR_UNSUPPORTED, "ceil(M / 16) * ceil(N / 128) must be below 2^28");
+  Span xs, wsp, os;
+  if (!row_span(a.x, a.M, a.x_stride, a.K, 1, xs) || !row_span(a.w, a.N, a.w_stride, a.K, 1, wsp) ||
+      !row_span(a.out, a.M, a.out_stride, a.N, size, os) || a.x_stride >= int64_t(1) << 40 ||
+      a.w_stride >= int64_t(1) << 40)
+    return set_error(MOE_ERR_INVALID_ARG, "row strides reach past any memory");
+  const Span ss{reinterpret_cast<uintptr_t>(a.x_scales), 4ll * a.M * KB};
+  const Span ts{reinterpret_cast<uintptr_t>(a.w_scales), 4ll * nb * KB};
+  if (meet(os, xs) || meet(os, wsp) || meet(os, ss) || meet(os, ts) ||
+      meet(os, Span{reinterpret_cast<uintptr_t>(ws), sizeof(Control)}))
+    return set_error(MOE_ERR_INVALID_ARG, "out must not overlap the other tensors");
+  Control* ctrl = static_cast<Control*>(ws);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.M <= 16) return launch_few<16>(a, KB, ctrl, st);
+  if (a.M <= 32) return launch_few<32>(a, KB, ctrl, st);
+  if (a.M <= 64) return launch_few<64>(a, KB, ctrl, st);
+  if (a.M <= kFewRows) return launch_few<128>(a, KB, ctrl, st);
+  return launch_many(a, KB, ctrl, st);
+}
