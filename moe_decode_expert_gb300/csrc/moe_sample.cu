@@ -1,20 +1,20 @@
 // moe_sample.cu — a token from each row of logits: temperature, top-k, top-p,
 // min-p and one given random number per row.
 //
-// A cluster of CTAs holds a row in shared memory (read from HBM once).  Weights
-// exp((l - max) / T) are fixed-point numbers of 45 bits at most, so that every sum
-// of them is exact and does not depend on the order of its terms; whichever threads
-// hold a row, the same token comes out.  Every filter keeps a prefix of the ranking
-// by (l descending, index ascending), so the kept set is one bound on the 64-bit
-// rank key (order of l, ~index).
+// A cluster of CTAs has a row: in shared memory, read from HBM once, or, where rows are
+// many and long, in L2.  Weights exp((l - max) / T) are fixed-point numbers of 45 bits at
+// most, so that every sum of them is exact and does not depend on the order of its terms;
+// whichever threads hold a row, the same token comes out.  Every filter keeps a prefix of
+// the ranking by (l descending, index ascending), so the kept set is one bound on the
+// 64-bit rank key (order of l, ~index).
 //
 // A top-k of few tokens needs no count: every CTA takes the j-th of its threads'
 // largest, j = k / CTAs, and at least k tokens are not below the least of these.
 // Else tokens are counted in bins of 1/32 octave of weight, which tells about where
 // a filter ends.  Where few tokens lie above, they are brought to the first CTA, which
-// settles everything; otherwise the range of values about the end is divided by 512
-// until one value is left, with exact sums (and the whole range if the end was not
-// in it).
+// settles everything.  Otherwise a pass sums what lies above a window about the end,
+// and the first CTA gets the window's tokens; where these are too many (ties, or an
+// end outside), the range of values is divided by 512 until one value is left.
 
 #include <algorithm>
 
@@ -26,8 +26,7 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;       // of a cluster (a row)
-constexpr int kMaxSlice = 49152;  // elements of a CTA
-constexpr int kMaxV = kMaxCtas * kMaxSlice;
+constexpr int kMaxV = 393216;  // sums of so many weights stay below 2^64
 constexpr float kNegInf = -INFINITY;
 
 // 2^(j / 32) in units of 2^-31, rounded.
@@ -58,13 +57,12 @@ struct Stored<MOE_F32> {
   using T = float;
 };
 
-// A logit's value: NaN as -infinity, -0 as +0 (equal values rank by index).
+// A logit's value.  NaN is never largest, has no weight and is not above or equal to anything, as
+// -infinity; -0 is turned to 0 where keys are made.
 template <int DT>
 __device__ __forceinline__ float value(typename Stored<DT>::T v) {
-  float f;
-  if constexpr (DT == MOE_F32) f = v;
-  else f = unpack2<DT>(v).x;
-  return fmaxf(f, kNegInf) + 0.0f;
+  if constexpr (DT == MOE_F32) return v;
+  else return unpack2<DT>(v).x;
 }
 
 // A row's weights.  With c = 32 log2(e) / T in two terms, l c = n + e, n the nearest
@@ -76,7 +74,7 @@ struct Weights {
   float hi, lo;   // c
   float base;     // subtracted from l first: 0, or the largest where max * c is far
   int top;        // the largest's octave, n >> 5
-  bool infinite;  // the row's largest is +infinity: those have weight 1 and the others 0
+  bool infinite;  // the row's largest is +infinity: those share it and the others have weight 0
   __device__ __forceinline__ void init(float temperature, float largest) {
     const float t = fminf(fmaxf(temperature, 1e-30f), 3.0e38f);
     constexpr float kHi = 46.166241308446828f;  // 32 log2(e) and what fp32 leaves of it
@@ -84,11 +82,13 @@ struct Weights {
     hi = __fdiv_rn(kHi, t);
     lo = __fdiv_rn(fmaf(-hi, t, kHi) + kLo, t);
     infinite = largest == INFINITY;
-    const float m = infinite ? 0.0f : largest;
-    base = fabsf(m * hi) > 131072.0f ? m : 0.0f;
+    // (infinite times a tiny c is far above every finite one, which has weight 0 below it; its
+    // rest is not a number, which no whole number comes of)
+    if (infinite) hi = 1e-36f, lo = 0.0f;
+    base = !infinite && fabsf(largest * hi) > 131072.0f ? largest : 0.0f;
     top = 0;
     float e;
-    top = split(m, e) >> 5;
+    top = split(largest, e) >> 5;
   }
   // n and e of a logit
   __device__ __forceinline__ int split(float l, float& e) const {
@@ -103,13 +103,11 @@ struct Weights {
   // The bin of a logit, 32 to an octave of weight downwards from the largest's octave; from
   // 45 * 32 on the weight is zero.  (Of d * c as it is rounded, so never rising with l.)
   __device__ __forceinline__ int bin(float l) const {
-    if (infinite) return l == INFINITY ? 31 : 1 << 20;
     const float s = fmaxf((l - base) * hi, -2097152.0f) + 12582912.0f;
     return 32 * top + 31 - (__float_as_int(s) - 0x4b400000);
   }
   // sum + the weight of l
   __device__ __forceinline__ uint64_t add(uint64_t sum, float l, const uint2* root) const {
-    if (infinite) return l == INFINITY ? sum + (1ull << 44) : sum;
     float e;
     const int n = split(l, e);
     // 2^(e / 32) - 1, |e| <= 0.51: terms of (ln 2 / 32)^i / i!
@@ -146,32 +144,51 @@ __device__ __forceinline__ uint64_t times_fraction(uint64_t x, float f, bool* mo
 constexpr int kBins = 1536;        // counted: 45 octaves of weight by 32, a multiple of the threads
 constexpr int kUsedBins = 45 * 32;
 constexpr int kSub = kBins / 3;    // a value's range is divided by this, 3 words of 15 bits a sum
-constexpr int kList = 2048;        // tokens that one CTA sorts
+constexpr int kList = 1024;        // tokens that one CTA sorts
+constexpr int kPer = kList / kThreads;
 constexpr uint32_t kHistBytes = kBins * 4, kListBytes = kList * 8;
+static_assert(kSub == kThreads && kList % kThreads == 0, "a part of a range per thread");
 
 __device__ __forceinline__ uint32_t ld_peer32(const void* p, uint32_t rank) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(smem_u32(p), rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 ld_peer128(const void* p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer_addr(smem_u32(p), rank))
+               : "memory");
+  return v;
+}
 
 // What the CTAs of a row exchange, and a CTA's warps.
 struct Shared {
-  uint64_t warp[kWarps];         // this CTA's sums by warp, of the last reduction
-  uint64_t cta[2][kMaxCtas];     // every CTA's, two reductions in turn
-  uint64_t other[2][kMaxCtas];   // of a second sum
-  uint64_t said[2][4];           // the first CTA's findings, two in turn
-  uint64_t found[2];             // a token found by one CTA
-  uint64_t best[kMaxCtas];       // the largest logit, and the key that some of the threads' largest reach
-  uint2 root[32];                // 2^(j / 32) in units of 2^-31, whole and in fp32
-  uint32_t listed;               // tokens this CTA brought
+  uint64_t warp[kWarps];               // this CTA's sums by warp, of the last reduction
   uint64_t spare[kWarps];
+  uint64_t cta[2][kMaxCtas];           // every CTA's, two reductions in turn
+  uint64_t other[2][kMaxCtas];         // of a second sum
+  uint64_t region[kMaxCtas * kWarps];  // the first CTA's: every warp's sum in the row
+  uint64_t said[2][4], finds[4];       // the first CTA's findings, two in turn; being made
+  uint64_t found[2];                   // a token found by one CTA
+  uint64_t best[kMaxCtas];             // the largest logit, and the key that some of the threads' largest reach
+  uint4 edge[2];                       // the first and last chunk where they are not whole
+  uint2 root[32];                      // 2^(j / 32) in units of 2^-31, whole and in fp32
+  uint32_t listed;                     // tokens this CTA brought
+  int middle;
 };
 
-// A CTA's part of a row: its slice lies in shared memory as in global memory about 16-byte
-// chunks, with -infinity in the places of the first and last chunk that are not its own.
-// Slot i is token first + i.  Every warp has a run of the chunks.
-template <int DT>
+__device__ __forceinline__ float value_of_key(uint64_t key) {
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ float value_of_order(uint32_t key) { return value_of_key(static_cast<uint64_t>(key) << 32); }
+
+// A CTA's part of a row, in 16-byte chunks as they lie in global memory, with -infinity in
+// the places of the first and last chunk that are not its own.  Slot i is token first + i.
+// Every warp has a run of the chunks.  HELD: the chunks are in shared memory.
+template <int DT, bool HELD>
 struct Row {
   using T = typename Stored<DT>::T;
   static constexpr int kVec = 16 / sizeof(T);
@@ -179,10 +196,10 @@ struct Row {
   Shared& sh;
   const uint4* s;
   uint32_t* hist;
-  uint64_t* list;
-  int C, rank, first, q0, q1;  // CTAs, this one, the token of slot 0, this warp's chunks
-  int turn, chunks;
-  const void* row;  // in global memory, from token 0
+  uint64_t *list, *list2;
+  int C, rank, first, off, n;  // CTAs, this one, the token of slot 0, its own slots: off to off + n
+  int chunks, per_warp;
+  int turn;
   Weights wt;
 
   __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
@@ -192,7 +209,7 @@ struct Row {
     else __syncthreads();
   }
   static __device__ __forceinline__ uint64_t key_of(float v, int i) {
-    return (static_cast<uint64_t>(order_key(v)) << 32) | static_cast<uint32_t>(~i);
+    return (static_cast<uint64_t>(order_key(v + 0.0f)) << 32) | static_cast<uint32_t>(~i);
   }
   __device__ __forceinline__ uint64_t weight(float v) const { return wt.of(v, sh.root); }
 
@@ -201,26 +218,58 @@ struct Row {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (DT == MOE_F32) {
-        v[j] = __uint_as_float(w[j]);  // (made sound when it was stored)
+        v[j] = __uint_as_float(w[j]);
       } else {
         const float2 f = unpack2<DT>(w[j]);
-        v[2 * j] = fmaxf(f.x, kNegInf) + 0.0f;
-        v[2 * j + 1] = fmaxf(f.y, kNegInf) + 0.0f;
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
       }
     }
   }
+  __device__ __forceinline__ uint4 chunk(int q) const {
+    if constexpr (HELD) return s[q];
+    if (q == 0) return sh.edge[0];
+    if (q == chunks - 1) return sh.edge[1];
+    return ld_ordered16(s + q);
+  }
   __device__ __forceinline__ float at(int slot) const {
-    return value<DT>(reinterpret_cast<const T*>(s)[slot]);
+    const uint4 c = chunk(slot / kVec);
+    float v[kVec], x = 0.0f;
+    unpack(c, v);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (j == slot % kVec) x = v[j];
+    return x;
+  }
+  // f(values, first slot) for this thread's chunks
+  template <class F>
+  __device__ __forceinline__ void chunks_of(F f) const {
+    const int q0 = min(chunks, warp() * per_warp), q1 = min(chunks, q0 + per_warp);
+    float v[kVec];
+    if constexpr (HELD) {
+      for (int q = q0 + lane(); q < q1; q += 32) {
+        unpack(s[q], v);
+        f(v, q * kVec);
+      }
+    } else {  // two loads ahead
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (q0 + lane() < q1) a = chunk(q0 + lane());
+      if (q0 + lane() + 32 < q1) b = chunk(q0 + lane() + 32);
+      for (int q = q0 + lane(); q < q1; q += 32) {
+        unpack(a, v);
+        a = b;
+        if (q + 64 < q1) b = chunk(q + 64);
+        f(v, q * kVec);
+      }
+    }
   }
   // f(value, slot) for this thread's slots
   template <class F>
   __device__ __forceinline__ void each(F f) const {
-    for (int q = q0 + lane(); q < q1; q += 32) {
-      float v[kVec];
-      unpack(s[q], v);
+    chunks_of([&](const float (&v)[kVec], int i) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f(v[j], q * kVec + j);
-    }
+      for (int j = 0; j < kVec; ++j) f(v[j], i + j);
+    });
   }
   // the whole row's sum of what its threads have
   __device__ __forceinline__ uint64_t total(uint64_t v) {
@@ -279,19 +328,10 @@ struct Row {
     if (all) *all = sum;
     return before + in - v;
   }
-  // After total() of sums of f: calls hit(value, slot) in the one thread that holds the first slot
-  // up to and with which f sums to more than `target`.  The warp's run of chunks that has it is
-  // gone through once more by all threads of its CTA.
+  // Calls hit(value, slot) in the one thread that holds the first slot of warp w's run up to and
+  // with which f sums to more than `target`.  All threads of the CTA go through the run once more.
   template <class F, class H>
-  __device__ __forceinline__ void locate(F f, uint64_t target, H hit) const {
-    for (int r = 0; r < rank; ++r) {
-      if (target < sh.cta[turn][r]) return;
-      target -= sh.cta[turn][r];
-    }
-    if (target >= sh.cta[turn][rank]) return;
-    int w = 0;
-    for (; target >= sh.warp[w]; ++w) target -= sh.warp[w];
-    const int per_warp = (chunks + kWarps - 1) / kWarps;
+  __device__ __forceinline__ void locate_in(int w, F f, uint64_t target, H hit) const {
     const int a = w * per_warp * kVec, b = min(chunks, (w + 1) * per_warp) * kVec;
     const int run = (b - a + kThreads - 1) / kThreads;
     const int i0 = min(b, a + run * static_cast<int>(threadIdx.x)), i1 = min(b, i0 + run);
@@ -308,76 +348,103 @@ struct Row {
       }
     }
   }
+  // The same of the whole row, after total() of sums of f.
+  template <class F, class H>
+  __device__ __forceinline__ void locate(F f, uint64_t target, H hit) const {
+    for (int r = 0; r < rank; ++r) {
+      if (target < sh.cta[turn][r]) return;
+      target -= sh.cta[turn][r];
+    }
+    if (target >= sh.cta[turn][rank]) return;
+    int w = 0;
+    for (; target >= sh.warp[w]; ++w) target -= sh.warp[w];
+    locate_in(w, f, target, hit);
+  }
 
-  // The first CTA's threads put what they found into sh.said[turn] of all.
-  __device__ __forceinline__ void tell(int i, uint64_t v) const {
-    for (int r = 0; r < C; ++r) st_peer64(&sh.said[turn][i], r, v);
+  // What threads of the first CTA left in sh.finds, to all CTAs; with a barrier of the row.
+  __device__ __forceinline__ void tell(int words) const {
+    if (rank == 0) {
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < C)
+        for (int i = 0; i < words; ++i) st_peer64(&sh.said[turn][i], threadIdx.x, sh.finds[i]);
+    }
+    sync_row();
   }
   __device__ __forceinline__ void clear_hist() const {
     for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
     __syncthreads();
   }
-  // A bin of every CTA's together.
-  __device__ __forceinline__ uint64_t merged(int i) const {
-    uint64_t v = hist[i];
-    for (int r = 1; r < C; ++r) v += ld_peer32(hist + i, r);
-    return v;
-  }
 
   // Counts the tokens that `stays` in their bins, and finds the first and last bin in which, by
   // those counts, the ranking's first k tokens, or the share p of the weight, may end (kUsedBins:
   // behind the last), and how many tokens lie down to the last.
-  template <class S>
+  template <bool ALL, class S>
   __device__ __forceinline__ void find_bins(S stays, bool by_k, uint64_t k, float p, int& b0, int& b1,
                                             uint64_t& tokens) {
     clear_hist();
     each([&](float v, int i) {
       const int b = wt.bin(v);
-      if (b < kUsedBins && stays(v, i)) atomicAdd(&hist[b], 1u);
+      if (b < kUsedBins && (ALL || stays(v, i))) atomicAdd(&hist[b], 1u);
     });
     turn ^= 1;
     sync_row();
     if (rank == 0) {
-      uint64_t c[3], w[3], count = 0, mass = 0;
+      uint64_t count = 0, mass = 0, w[4];
+      uint32_t c[4] = {};
+      if (threadIdx.x < kBins / 4) {
+        uint4 h = reinterpret_cast<const uint4*>(hist)[threadIdx.x];
+        for (int r = 1; r < C; ++r) {
+          const uint4 o = ld_peer128(hist + 4 * threadIdx.x, r);
+          h.x += o.x, h.y += o.y, h.z += o.z, h.w += o.w;
+        }
+        c[0] = h.x, c[1] = h.y, c[2] = h.z, c[3] = h.w;
+      }
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int i = 3 * threadIdx.x + j;
-        c[j] = merged(i);
-        w[j] = c[j] * ((static_cast<uint64_t>(sh.root[31 - (i & 31)].x) << 13) >> (i >> 5));
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * threadIdx.x + j;
+        w[j] = c[j] * ((static_cast<uint64_t>(sh.root[31 - (i & 31)].x) << 13) >> min(i >> 5, 63));
         count += c[j];
         mass += w[j];
       }
-      uint64_t tokens_all, all;
-      uint64_t n = scan(count, &tokens_all);
+      uint64_t all;
+      uint64_t n = scan(count);
       uint64_t m = scan(mass, &all);
       // a token's weight is within 2^(1 / 64) of its bin's: two sums' ratio within 2^(1 / 32)
       const auto reached = [&](uint64_t n, uint64_t m, float room) {
-        return by_k ? n >= k
-                    : static_cast<float>(m) * room * (1.0f - p) >= static_cast<float>(all - m) * p;
+        return by_k ? n >= k : static_cast<float>(m) * room * (1.0f - p) >= static_cast<float>(all - m) * p;
       };
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const uint64_t n1 = n + c[j], m1 = m + w[j];
         const bool none = n == 0;  // (the share 0 of nothing is not reached)
-        if (n1 != n) {
-          if ((none || !reached(n, m, 1.025f)) && reached(n1, m1, 1.025f)) tell(0, 3 * threadIdx.x + j);
+        if (c[j]) {
+          if ((none || !reached(n, m, 1.025f)) && reached(n1, m1, 1.025f)) {
+            sh.finds[0] = 4 * threadIdx.x + j;
+            sh.finds[3] = n;
+          }
+          if ((none || !reached(n, m, 1.0f)) && reached(n1, m1, 1.0f)) sh.middle = 4 * threadIdx.x + j;
           if ((none || !reached(n, m, 0.975f)) && reached(n1, m1, 0.975f)) {
-            tell(1, 3 * threadIdx.x + j);
-            tell(2, n1);
+            sh.finds[1] = 4 * threadIdx.x + j;
+            sh.finds[2] = n1;
           }
         }
         n = n1;
         m = m1;
       }
       if (threadIdx.x == kThreads - 1) {
-        if (!reached(n, m, 1.025f)) tell(0, kUsedBins);
+        if (!reached(n, m, 1.025f)) sh.finds[0] = kUsedBins;
         if (!reached(n, m, 0.975f)) {
-          tell(1, kUsedBins);
-          tell(2, n);
+          sh.finds[1] = kUsedBins;
+          sh.finds[2] = n;
         }
       }
+      __syncthreads();
+      // a window of more tokens than a list holds: the bin where the end lies if every weight is
+      // its bin's, which it is nearly always where tokens are many (and else found out)
+      if (threadIdx.x == 0 && sh.finds[1] < kUsedBins && sh.finds[2] - sh.finds[3] > kList * 3 / 4)
+        sh.finds[0] = sh.finds[1] = sh.middle;
     }
-    sync_row();
+    tell(3);
     b0 = static_cast<int>(sh.said[turn][0]);
     b1 = static_cast<int>(sh.said[turn][1]);
     tokens = sh.said[turn][2];
@@ -397,48 +464,49 @@ struct Row {
     if (klo > khi) klo = khi;  // (not a number: no room was left)
   }
 
-  static __device__ __forceinline__ int range_shift(uint32_t klo, uint32_t khi) {
-    return max(32 - __clz(static_cast<int>(khi - klo)) - 9, 0);  // kSub = 2^9
-  }
-  // Adds w to the sum of its part of the range, by 15 bits in three words.
-  __device__ __forceinline__ void put(uint32_t part, uint64_t w) const {
-    atomicAdd(&hist[part], static_cast<uint32_t>(w) & 0x7fffu);
-    if (w >> 15) {
-      atomicAdd(&hist[kSub + part], static_cast<uint32_t>(w >> 15) & 0x7fffu);
-      atomicAdd(&hist[2 * kSub + part], static_cast<uint32_t>(w >> 30));
-    }
-  }
+  // ------------------------------------------------------- ranges by parts
   // The rank key of the last of the ranking's first tokens, of those that `stays`, whose f sums to
-  // `need` (at least 1).  The parts of the range [klo, khi] are in hist, `above` is what lies above
-  // it; false if the end is not in the range.
+  // `need` (at least 1, and reached): the range of keys is divided until one value is left.  `above`
+  // is the sum above the range; where the end is not in it, all begins again with all keys.
   template <class S, class F>
-  __device__ __forceinline__ bool select(uint32_t klo, uint32_t khi, uint64_t above, S stays, F f, uint64_t need,
-                                         uint64_t& key) {
-    for (bool filled = true;; filled = false) {
-      const int shift = range_shift(klo, khi);
-      if (!filled) {
-        clear_hist();
-        each([&](float v, int i) {
-          const uint32_t key = order_key(v);
-          if (key >= klo && key <= khi && stays(v, i)) put((khi - key) >> shift, f(v));
-        });
-      }
+  __device__ __forceinline__ uint64_t select(uint32_t klo, uint32_t khi, uint64_t above, S stays, F f, uint64_t need) {
+    for (;;) {
+      const int shift = max(32 - __clz(static_cast<int>(khi - klo)) - 9, 0);  // kSub = 2^9
+      const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
+      clear_hist();
+      each([&](float v, int i) {
+        if (v >= v_lo && v <= v_hi && i >= off && i < off + n && stays(v, i)) {
+          const uint64_t w = f(v);  // by 15 bits in three words
+          const uint32_t part = (khi - order_key(v + 0.0f)) >> shift;
+          atomicAdd(&hist[part], static_cast<uint32_t>(w) & 0x7fffu);
+          if (w >> 15) {
+            atomicAdd(&hist[kSub + part], static_cast<uint32_t>(w >> 15) & 0x7fffu);
+            atomicAdd(&hist[2 * kSub + part], static_cast<uint32_t>(w >> 30));
+          }
+        }
+      });
       turn ^= 1;
       sync_row();
       if (rank == 0) {
         const int t = threadIdx.x;  // kThreads = kSub
-        const uint64_t v = merged(t) + (merged(kSub + t) << 15) + (merged(2 * kSub + t) << 30);
-        uint64_t all;
+        uint64_t v = 0, all;
+        for (int r = 0; r < C; ++r)
+          v += ld_peer32(hist + t, r) + (static_cast<uint64_t>(ld_peer32(hist + kSub + t, r)) << 15) +
+               (static_cast<uint64_t>(ld_peer32(hist + 2 * kSub + t, r)) << 30);
         const uint64_t at = above + scan(v, &all);
         if (at < need && at + v >= need) {
-          tell(0, t);
-          tell(1, at);
+          sh.finds[0] = t;
+          sh.finds[1] = at;
         }
-        if (t == 0 && (above >= need || above + all < need)) tell(0, kSub);
+        if (t == 0 && (above >= need || above + all < need)) sh.finds[0] = kSub;
       }
-      sync_row();
+      tell(2);
       const uint32_t t = static_cast<uint32_t>(sh.said[turn][0]);
-      if (t == kSub) return false;
+      if (t == kSub) {
+        klo = order_key(kNegInf), khi = order_key(INFINITY);
+        above = 0;
+        continue;
+      }
       above = sh.said[turn][1];
       khi -= t << shift;
       klo = max(klo, khi - ((1u << shift) - 1u));
@@ -446,77 +514,141 @@ struct Row {
     }
     // one value is left: by index
     const auto tie = [&](float v, int i) {
-      const uint32_t key = order_key(v);
-      return key >= klo && key <= khi && stays(v, i) ? f(v) : 0ull;
+      const uint32_t key = order_key(v + 0.0f);
+      return v == v && key >= klo && key <= khi && i >= off && i < off + n && stays(v, i) ? f(v) : 0ull;
     };
     sum(tie);
     locate(tie, need - above - 1, [&](float v, int i) {
       for (int r = 0; r < C; ++r) st_peer64(&sh.found[turn], r, key_of(v, first + i));
     });
     sync_row();
-    key = sh.found[turn];
-    return true;
+    return sh.found[turn];
   }
 
-  // Brings the tokens that are not below `least` to the first CTA's list; how many there are, or -1
-  // if a CTA has more than its share of the list.
-  __device__ __forceinline__ int gather(float least, int n, int off) {
-    const int share = kList / C;
+  // --------------------------------------------------------- lists of tokens
+  // A token to the first CTA's list, of which every CTA has a share.
+  __device__ __forceinline__ void bring(float v, int i) const {
+    const int share = kList / C, at = static_cast<int>(atomicAdd(&sh.listed, 1u));
+    if (at < share) st_peer64(list + rank * share + at, 0, key_of(v, first + i));
+  }
+  // Those of a chunk that lie between two values, and of the value `tie` only the slots up to `last`.
+  __device__ __forceinline__ void bring_some(const float (&v)[kVec], int i, float v_lo, float v_hi,
+                                             float tie = 0.0f, int last = INT32_MAX) const {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (v[j] >= v_lo && v[j] <= v_hi && i + j >= off && i + j < off + n && (v[j] != tie || i + j <= last))
+        bring(v[j], i + j);
+  }
+  __device__ __forceinline__ void begin_list() const {
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
-    for (int q = q0 + lane(); q < q1; q += 32) {
-      float v[kVec];
-      unpack(s[q], v);
-      float m = v[0];
-#pragma unroll
-      for (int j = 1; j < kVec; ++j) m = fmaxf(m, v[j]);
-      if (m >= least) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const int i = q * kVec + j;
-          if (v[j] >= least && i >= off && i < off + n) {
-            const int at = static_cast<int>(atomicAdd(&sh.listed, 1u));
-            if (at < share) st_peer64(list + rank * share + at, 0, key_of(v[j], first + i));
-          }
-        }
-      }
-    }
+  }
+  // How many tokens are in the list, or -1 if a CTA had more than its share; known to all.
+  __device__ __forceinline__ int end_list() {
     __syncthreads();
     turn ^= 1;
-    if (threadIdx.x < C) st_peer64(&sh.cta[turn][rank], threadIdx.x, sh.listed);
+    if (static_cast<int>(threadIdx.x) < C) st_peer64(&sh.cta[turn][rank], threadIdx.x, sh.listed);
     sync_row();
     int sum = 0;
     bool fits = true;
     for (int r = 0; r < C; ++r) {
       sum += static_cast<int>(sh.cta[turn][r]);
-      fits &= sh.cta[turn][r] <= static_cast<uint64_t>(share);
+      fits &= sh.cta[turn][r] <= static_cast<uint64_t>(kList / C);
     }
     return fits ? sum : -1;
   }
-};
+  // The first CTA, after end_list(): the shares together, into list2.
+  __device__ __forceinline__ void close_list() const {
+    int at = 0;
+    for (int c = 0; c < C; ++c) {
+      const int many = static_cast<int>(sh.cta[turn][c]);
+      for (int i = threadIdx.x; i < many; i += kThreads) list2[at + i] = list[c * (kList / C) + i];
+      at += many;
+    }
+    __syncthreads();
+  }
+  // Brings the tokens that are not below `least`.
+  __device__ __forceinline__ int gather(float least) {
+    begin_list();
+    chunks_of([&](const float (&v)[kVec], int i) {
+      float m = v[0];
+#pragma unroll
+      for (int j = 1; j < kVec; ++j) m = fmaxf(m, v[j]);
+      if (m >= least) bring_some(v, i, least, INFINITY);
+    });
+    return end_list();
+  }
 
-// Sorts keys[0 .. n) downwards in one CTA; n2: a power of two >= n, the room there is.
-__device__ __forceinline__ void sort_down(uint64_t* keys, int n, int n2) {
-  for (int i = n + threadIdx.x; i < n2; i += kThreads) keys[i] = 0;
-  for (int k = 2; k <= n2; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < n2 / 2; t += kThreads) {
-        const int a = 2 * t - (t & (j - 1)), b = a + j;
-        const uint64_t x = keys[a], y = keys[b];
-        if ((x < y) == ((a & k) == 0)) {
-          keys[a] = y;
-          keys[b] = x;
-        }
+  // Sorts the keys in list2[0 .. m) downwards, in one CTA: by their part of the range of the first
+  // words, then by comparing within a part; by exchanges where a part has many.
+  __device__ __forceinline__ void sort(int m) const {
+    uint32_t most = 0, least = 0xffffffffu;
+    uint64_t key[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      key[j] = i < m ? list2[i] : 0ull;
+      if (i < m) {
+        most = max(most, static_cast<uint32_t>(key[j] >> 32));
+        least = min(least, static_cast<uint32_t>(key[j] >> 32));
       }
     }
-  __syncthreads();
-}
-
-__device__ __forceinline__ float value_of_key(uint64_t key) {
-  const uint32_t o = static_cast<uint32_t>(key >> 32);
-  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
-}
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    __syncthreads();
+    if (lane() == 0) sh.spare[warp()] = (static_cast<uint64_t>(most) << 32) | least;
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      most = max(most, static_cast<uint32_t>(sh.spare[w] >> 32));
+      least = min(least, static_cast<uint32_t>(sh.spare[w]));
+    }
+    const int shift = max(32 - __clz(static_cast<int>(most - least)) - 9, 0);
+    int at[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (static_cast<int>(threadIdx.x) + j * kThreads < m)
+        at[j] = static_cast<int>(atomicAdd(&hist[(most - static_cast<uint32_t>(key[j] >> 32)) >> shift], 1u));
+    __syncthreads();
+    const uint32_t mine = hist[threadIdx.x];
+    if (__syncthreads_or(mine > 64u)) {
+      int n2 = 2;
+      while (n2 < m) n2 <<= 1;
+      for (int i = m + threadIdx.x; i < n2; i += kThreads) list2[i] = 0;
+      for (int k = 2; k <= n2; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+          __syncthreads();
+          for (int t = threadIdx.x; t < n2 / 2; t += kThreads) {
+            const int a = 2 * t - (t & (j - 1)), b = a + j;
+            const uint64_t x = list2[a], y = list2[b];
+            if ((x < y) == ((a & k) == 0)) {
+              list2[a] = y;
+              list2[b] = x;
+            }
+          }
+        }
+      __syncthreads();
+      return;
+    }
+    hist[kSub + threadIdx.x] = static_cast<uint32_t>(scan(mine));
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (static_cast<int>(threadIdx.x) + j * kThreads < m)
+        list[hist[kSub + ((most - static_cast<uint32_t>(key[j] >> 32)) >> shift)] + at[j]] = key[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (static_cast<int>(threadIdx.x) + j * kThreads < m) {
+        const uint32_t part = (most - static_cast<uint32_t>(key[j] >> 32)) >> shift;
+        const uint32_t from = hist[kSub + part], many = hist[part];
+        uint32_t to = from;
+        for (uint32_t i = 0; i < many; ++i) to += list[from + i] > key[j];
+        list2[to] = key[j];
+      }
+    __syncthreads();
+  }
+};
 
 // ln(weight of v / all)
 __device__ __forceinline__ float log_share(const Weights& wt, float v, uint64_t w, uint64_t all) {
@@ -536,59 +668,63 @@ struct Asked {
   float temperature, top_p, u;
   uint64_t w_min;
   int k;  // 0: all
+  __device__ __forceinline__ uint64_t needed(uint64_t sum) const {  // of a sum of weights
+    bool more;
+    if (!(top_p < 1.0f)) return sum;
+    const uint64_t n = times_fraction(sum, top_p, &more);
+    return max(n + more, static_cast<uint64_t>(1));
+  }
 };
 
 // The rest of a row by one CTA, from the m tokens that lead its ranking (their rank keys in
-// `keys`, in any order; room for kList, as in `spare`).  `sum`: of all weights, for top_p
-// without top_k.
-template <int DT>
-__device__ __forceinline__ void finish_list(const Row<DT>& r, const Asked& ask, uint64_t* keys, uint64_t* spare, int m,
-                                            uint64_t sum, int64_t* token, float* logprob) {
+// r.list2, in any order).  `sum`: of all weights, for top_p without top_k.
+template <int DT, bool HELD>
+__device__ __forceinline__ void finish_list(const Row<DT, HELD>& r, const Asked& ask, int m, uint64_t sum,
+                                            int64_t* token, float* logprob) {
   const Weights& wt = r.wt;
   const int k = ask.k ? min(m, ask.k) : m;
-  bool more;
-  const auto needed = [&](uint64_t sum) {
-    return ask.top_p < 1.0f ? max(times_fraction(sum, ask.top_p, &more) + more, static_cast<uint64_t>(1)) : sum;
-  };
-  if (m <= 256) {
-    // A thread per token: ranks and sums by comparing with every other (21 tokens: 0.5 us where
-    // two sorts took 3.4; 256: 2 us).
-    const bool in = static_cast<int>(threadIdx.x) < m;
-    const uint64_t key = in ? keys[threadIdx.x] : 0ull;
+  uint64_t *keys = r.list2, *spare = r.list;
+  if (m <= 64) {
+    // Eight threads per token: ranks and sums by comparing with every other.
+    const int t = threadIdx.x >> 3, part = threadIdx.x & 7;
+    const bool in = t < m;
+    const uint64_t key = in ? keys[t] : 0ull;
     const float v = value_of_key(key);
     const uint64_t w = in ? r.weight(v) : 0ull;
-    if (in) spare[threadIdx.x] = w;
+    if (in && part == 0) spare[t] = w;
     __syncthreads();
-    int rank = 0;
-    uint64_t before = 0;
-    if (in)
-      for (int j = 0; j < m; ++j)
-        if (keys[j] > key) {
-          ++rank;
-          before += spare[j];
-        }
-    if (ask.k) r.scan(in && rank < k ? w : 0ull, &sum);
-    const bool stays = in && rank < k && before < needed(sum) && (w >= ask.w_min || rank == 0);
+    const auto add8 = [](uint64_t v) {
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    uint64_t before = 0, ahead = 0;
+    for (int j = part; j < m; j += 8)
+      if (keys[j] > key) {
+        ++ahead;
+        before += spare[j];
+      }
+    before = add8(before);
+    const int rank = static_cast<int>(add8(ahead));
+    if (ask.k) r.scan(in && part == 0 && rank < k ? w : 0ull, &sum);
+    const bool stays = in && rank < k && before < ask.needed(sum) && (w >= ask.w_min || rank == 0);
     __syncthreads();
-    if (in) spare[threadIdx.x] = stays ? w : 0ull;
+    if (in && part == 0) spare[t] = stays ? w : 0ull;
     uint64_t whole;
-    r.scan(stays ? w : 0ull, &whole);  // (also: spare is written)
+    r.scan(stays && part == 0 ? w : 0ull, &whole);  // (also: spare is written)
     const uint64_t target = times_fraction(whole, ask.u);
-    if (!stays) return;
-    before = 0;
     const uint32_t at = static_cast<uint32_t>(key);  // ~index
-    for (int j = 0; j < m; ++j)
+    before = 0;
+    for (int j = part; j < m; j += 8)
       if (static_cast<uint32_t>(keys[j]) > at) before += spare[j];
-    if (target >= before && target < before + w) {
+    before = add8(before);
+    if (stays && part == 0 && target >= before && target < before + w) {
       *token = static_cast<int>(~at);
       if (logprob) *logprob = log_share(wt, v, w, whole);
     }
     return;
   }
-  int n2 = 512;
-  while (n2 < m) n2 <<= 1;
-  sort_down(keys, m, n2);
-  constexpr int kPer = kList / kThreads;
+  r.sort(m);
   uint64_t w[kPer], here = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -598,7 +734,7 @@ __device__ __forceinline__ void finish_list(const Row<DT>& r, const Asked& ask, 
   }
   uint64_t all;
   uint64_t before = r.scan(here, &all);
-  const uint64_t need = needed(ask.k ? all : sum);
+  const uint64_t need = ask.needed(ask.k ? all : sum);
   here = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -609,21 +745,19 @@ __device__ __forceinline__ void finish_list(const Row<DT>& r, const Asked& ask, 
   }
   uint64_t whole;
   r.scan(here, &whole);
-  // by index: sort again, on (~index, place in the ranking) downwards
+  // by index: sorted again, on (~index, order of the value, or 0 where the token does not stay)
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = kPer * threadIdx.x + j;
-    if (i < m) {
-      spare[i] = w[j];
-      keys[i] = w[j] ? (keys[i] << 32) | static_cast<uint32_t>(i) : static_cast<uint32_t>(i);
-    }
+    if (i < m) keys[i] = (keys[i] << 32) | (w[j] ? keys[i] >> 32 : 0ull);
   }
-  sort_down(keys, m, n2);
+  __syncthreads();
+  r.sort(m);
   here = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = kPer * threadIdx.x + j;
-    w[j] = i < m && (keys[i] >> 32) ? spare[static_cast<uint32_t>(keys[i])] : 0ull;
+    w[j] = i < m && static_cast<uint32_t>(keys[i]) ? r.weight(value_of_key(keys[i] << 32)) : 0ull;
     here += w[j];
   }
   before = r.scan(here);
@@ -632,20 +766,18 @@ __device__ __forceinline__ void finish_list(const Row<DT>& r, const Asked& ask, 
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (target >= before && target < before + w[j]) {
-      const int i = static_cast<int>(~static_cast<uint32_t>(keys[kPer * threadIdx.x + j] >> 32));
-      *token = i;
-      if (logprob) {
-        // (its value has left the keys: it is in the row, whose first slot may be another CTA's)
-        *logprob = log_share(wt, value<DT>(static_cast<const typename Stored<DT>::T*>(r.row)[i]), w[j], whole);
-      }
+      const uint64_t key = keys[kPer * threadIdx.x + j];
+      *token = static_cast<int>(~static_cast<uint32_t>(key >> 32));
+      if (logprob) *logprob = log_share(wt, value_of_key(key << 32), w[j], whole);
     }
     before += w[j];
   }
 }
 
-template <int DT>
+template <int DT, bool HELD>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, int C, int per, uint32_t slice_bytes) {
   using T = typename Stored<DT>::T;
+  using R = Row<DT, HELD>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -660,15 +792,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
   pdl_wait();
 
   // ---------------------------------------------------------------- the slice
-  constexpr int kVec = 16 / sizeof(T);
+  constexpr int kVec = R::kVec;
   const int first = min(a.V, rank * per), n = min(a.V, first + per) - first;
   const T* g = static_cast<const T*>(a.logits) + row * a.logits_stride + first;
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(T));
   const int chunks = n ? (off + n + kVec - 1) / kVec : 0;
   T* s = reinterpret_cast<T*>(smem);
-  float mine = kNegInf;
+  float mine = kNegInf;  // this thread's largest, and the first of its whole chunks that has it
+  int where = -1;
+  float mine_edge = kNegInf;  // and its place in the first or last chunk, where these are not whole
+  int i_edge = 0;
   {
-    const int c_lo = off ? 1 : 0, c_hi = (off + n) / kVec;  // whole chunks
+    // whole chunks; in global memory the first and last are edges whether whole or not
+    const int c_lo = HELD ? (off ? 1 : 0) : 1, c_hi = HELD ? (off + n) / kVec : chunks - 1;
     constexpr int kAhead = 4;
     for (int c0 = c_lo + threadIdx.x; c0 < c_hi; c0 += kThreads * kAhead) {
       uint4 v[kAhead];
@@ -678,30 +814,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (c0 + u * kThreads < c_hi) {
-          if constexpr (DT == MOE_F32) {  // NaN to -infinity, -0 to 0
-            v[u].x = __float_as_uint(value<DT>(__uint_as_float(v[u].x)));
-            v[u].y = __float_as_uint(value<DT>(__uint_as_float(v[u].y)));
-            v[u].z = __float_as_uint(value<DT>(__uint_as_float(v[u].z)));
-            v[u].w = __float_as_uint(value<DT>(__uint_as_float(v[u].w)));
-          }
-          *reinterpret_cast<uint4*>(s + (c0 + u * kThreads) * kVec) = v[u];
           float f[kVec];
-          Row<DT>::unpack(v[u], f);
+          if constexpr (HELD) *reinterpret_cast<uint4*>(s + (c0 + u * kThreads) * kVec) = v[u];
+          R::unpack(v[u], f);
+          float m = f[0];
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) mine = fmaxf(mine, f[j]);
+          for (int j = 1; j < kVec; ++j) m = fmaxf(m, f[j]);
+          if (m > mine) {
+            mine = m;
+            where = c0 + u * kThreads;
+          }
         }
     }
-    // the first and last chunk where they are not whole: 2 * kVec places
-    if (threadIdx.x < 2 * kVec) {
-      const int i = threadIdx.x < kVec ? threadIdx.x : (chunks - 1) * kVec + threadIdx.x - kVec;
-      const bool whole = i / kVec >= c_lo && i / kVec < c_hi;
-      if (chunks && !whole && (threadIdx.x < kVec || chunks > 1)) {
+    // the first and last chunk: 2 * kVec places
+    if (threadIdx.x < 2 * kVec && chunks) {
+      const int e = threadIdx.x >= kVec, c = e ? chunks - 1 : 0, i = c * kVec + (threadIdx.x & (kVec - 1));
+      if (!(c >= c_lo && c < c_hi)) {  // (one chunk alone is written twice, alike)
         const bool own = i >= off && i < off + n;
+        T raw;
         float f = kNegInf;
-        if (own) f = value<DT>(g[i - off]);
-        if constexpr (DT == MOE_F32) s[i] = f;
-        else s[i] = own ? g[i - off] : (DT == MOE_BF16 ? 0xff80u : 0xfc00u);
-        mine = fmaxf(mine, f);
+        if constexpr (DT == MOE_F32) raw = kNegInf;
+        else raw = DT == MOE_BF16 ? 0xff80u : 0xfc00u;
+        if (own) {
+          raw = g[i - off];
+          f = value<DT>(raw);
+        }
+        if constexpr (HELD) s[i] = raw;
+        else reinterpret_cast<T*>(&sh.edge[e])[threadIdx.x & (kVec - 1)] = raw;
+        mine_edge = f;
+        i_edge = i;
       }
     }
   }
@@ -713,24 +854,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
   ask.u = a.uniforms[row];
   ask.u = ask.u > 0.0f ? fminf(ask.u, 0.99999994f) : 0.0f;
   const bool greedy = ask.temperature <= 0.0f;
-  if (greedy || min_p > 1.0f || ask.top_p <= 0.0f) k = 1;
-  if (k <= 0 || k >= a.V) k = 0;
-  if (a.V == 1) k = 1;
+  if (greedy || min_p > 1.0f || ask.top_p <= 0.0f || a.V == 1) k = 1;
+  else if (k <= 0 || k >= a.V) k = 0;
   const bool by_k = k > 0, by_p = ask.top_p < 1.0f;
   ask.k = k;
 
   // ------------------------------------------- the largest, and what some threads' largest reach
   __syncthreads();
+  const float mine_whole = mine;
+  mine = fmaxf(mine, mine_edge);
   float best = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) sh.warp[warp] = __float_as_uint(best);
   const int ctas = (a.V - 1) / per + 1;  // that have tokens
   const int share = (k - 1) / ctas + 1;
-  const bool few = k > 1 && 3 * share <= kThreads;
+  const bool few = k > 1 && 3 * share <= kThreads && 2 * k <= kList;
   uint32_t reach = 0;
   if (few) {  // to 18 bits of the key, at most
-    const uint32_t key = order_key(mine);
+    const uint32_t key = order_key(mine + 0.0f);
     for (int bit = 31; bit >= 14; --bit) {
       const uint32_t mid = reach | (1u << bit);
       if (__syncthreads_count(key >= mid) >= share) reach = mid;
@@ -762,151 +904,233 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
     return;
   }
 
-  Row<DT> r{sh, reinterpret_cast<const uint4*>(smem), reinterpret_cast<uint32_t*>(smem + slice_bytes),
-            reinterpret_cast<uint64_t*>(smem + slice_bytes + kHistBytes), C, rank, first - off};
-  r.chunks = chunks;
-  const int per_warp = (chunks + kWarps - 1) / kWarps;
-  r.q0 = min(chunks, warp * per_warp);
-  r.q1 = min(chunks, r.q0 + per_warp);
-  r.turn = 0;
-  r.row = static_cast<const T*>(a.logits) + row * a.logits_stride;
+  uint8_t* behind = smem + slice_bytes;
+  R r{sh, HELD ? reinterpret_cast<const uint4*>(smem) : reinterpret_cast<const uint4*>(g - off),
+      reinterpret_cast<uint32_t*>(behind), reinterpret_cast<uint64_t*>(behind + kHistBytes),
+      reinterpret_cast<uint64_t*>(behind + kHistBytes + kListBytes), C, rank, first - off, off, n, chunks,
+      (chunks + kWarps - 1) / kWarps, 0};
   r.wt.init(greedy || !(ask.temperature == ask.temperature) ? 1.0f : ask.temperature, best);
 
   if (k == 1) {  // rank 0: the first of the largest
-    const auto is = [&](float v, int) { return static_cast<uint64_t>(v == best); };
-    r.sum(is);
-    r.locate(is, 0, [&](float, int i) {
-      *token = r.first + i;
+    int i = INT32_MAX;
+    if (mine_whole == best) {
+      float v[kVec];
+      R::unpack(r.chunk(where), v);
+#pragma unroll
+      for (int j = kVec - 1; j >= 0; --j)
+        if (v[j] == best) i = where * kVec + j;
+    }
+    if (mine_edge == best) i = min(i, i_edge);
+    i = __reduce_min_sync(0xffffffffu, i);
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = static_cast<uint64_t>(i);
+    __syncthreads();
+    if (warp == 0) {
+      i = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<int>(sh.warp[lane]) : INT32_MAX);
+      if (lane == 0) st_peer64(&sh.cta[0][rank], 0, i == INT32_MAX ? ~0ull : static_cast<uint64_t>(r.first + i));
+    }
+    r.sync_row();
+    if (rank == 0 && threadIdx.x == 0) {
+      uint64_t least = ~0ull;
+      for (int c = 0; c < C; ++c) least = min(least, sh.cta[0][c]);
+      *token = static_cast<int64_t>(least);
       if (logprob) *logprob = 0.0f;
-    });
+    }
     return;
   }
-  bool more;
   ask.w_min = 0;  // weights below it do not stay
   if (min_p > 0.0f) {
+    bool more;
     const uint64_t w = r.weight(best);
     ask.w_min = min_p >= 1.0f ? w : times_fraction(w, min_p, &more) + more;
   }
 
   // ------------------------------------------------------------ the filters
   uint64_t cut = 0;  // smallest rank key that stays
-  const auto stays = [&](float v, int i) { return Row<DT>::key_of(v, r.first + i) >= cut; };
+  float v_cut = kNegInf;
+  const auto stays = [&](float v, int i) { return v > v_cut || (v == v_cut && R::key_of(v, r.first + i) >= cut); };
   const auto any = [](float, int) { return true; };
-  const auto one = [](float) { return static_cast<uint64_t>(1); };
-  const auto weigh = [&](float v) { return r.weight(v); };
-  const auto needed = [&](uint64_t sum) { return max(times_fraction(sum, ask.top_p, &more) + more, static_cast<uint64_t>(1)); };
-  uint64_t kept_above = 0;  // this thread's tokens above a range, if they are known to stay
-  float v_hi = INFINITY;
+  const auto set_cut = [&](uint64_t key) {
+    cut = key;
+    v_cut = value_of_key(key);
+  };
+  const auto kept = [&](float v, int i) {
+    const uint64_t w = r.weight(v);
+    return w >= ask.w_min && stays(v, i) ? w : static_cast<uint64_t>(0);
+  };
+  const auto write = [&](float v, int i, uint64_t all) {
+    *token = r.first + i;
+    if (logprob) *logprob = log_share(r.wt, v, r.weight(v), all);
+  };
   if (by_k || by_p) {
-    int m = -1;
+    int m = -1, b0, b1;
     uint64_t sum = 0, tokens;
-    int b0, b1;
     uint32_t klo, khi;
-    if (few) m = r.gather(reach > 0x007fffffu ? value_of_key(static_cast<uint64_t>(reach) << 32) : kNegInf, n, off);
+    if (few) m = r.gather(reach > 0x007fffffu ? value_of_order(reach) : kNegInf);
     if (m < 0) {
-      r.find_bins(any, by_k, k, ask.top_p, b0, b1, tokens);
-      r.key_range(b0, b1, klo, khi);
+      r.template find_bins<true>(any, by_k, k, ask.top_p, b0, b1, tokens);
       if (tokens <= kList) {
         if (!by_k) sum = r.sum([&](float v, int) { return r.weight(v); });
-        uint32_t least, none;  // (tokens without weight are not wanted, nor those masked)
-        r.key_range(b0, min(b1, kUsedBins - 1), least, none);
-        m = r.gather(value_of_key(static_cast<uint64_t>(least) << 32), n, off);
+        r.key_range(b0, min(b1, kUsedBins - 1), klo, khi);  // (tokens without weight are not wanted)
+        m = r.gather(value_of_order(klo));
       }
     }
     if (m >= 0) {  // the first CTA does the rest
       if (rank != 0) return;
-      // its list lies in the CTAs' shares: together, over the slice, which is not read again
-      uint64_t* keys = reinterpret_cast<uint64_t*>(smem);
-      int at = 0;
-      for (int c = 0; c < C; ++c) {
-        const int many = static_cast<int>(sh.cta[r.turn][c]);
-        for (int i = threadIdx.x; i < many; i += kThreads) keys[at + i] = r.list[c * (kList / C) + i];
-        at += many;
-      }
-      __syncthreads();
-      finish_list<DT>(r, ask, keys, r.list, m, sum, token, logprob);
+      r.close_list();
+      finish_list<DT, HELD>(r, ask, m, sum, token, logprob);
       return;
     }
     if (by_k && b1 < kUsedBins) {
-      for (;;) {
-        const int shift = Row<DT>::range_shift(klo, khi);
-        r.clear_hist();
-        const uint64_t above = r.sum([&](float v, int) {
-          const uint32_t key = order_key(v);
-          if (key >= klo && key <= khi) r.put((khi - key) >> shift, 1);
-          return static_cast<uint64_t>(key > khi);
-        });
-        if (r.select(klo, khi, above, any, one, k, cut)) break;
-        klo = 0x007fffffu, khi = order_key(INFINITY);
+      // what lies above the window is counted, its tokens are brought and sorted
+      r.key_range(b0, b1, klo, khi);
+      const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
+      r.begin_list();
+      uint64_t above = 0;
+      r.chunks_of([&](const float (&v)[R::kVec], int i) {
+        bool near = false;
+#pragma unroll
+        for (int j = 0; j < R::kVec; ++j) {
+          above += v[j] > v_hi;
+          near |= v[j] >= v_lo && v[j] <= v_hi;
+        }
+        if (near) r.bring_some(v, i, v_lo, v_hi);
+      });
+      above = r.total(above);
+      m = r.end_list();
+      if (m >= 0) {
+        r.turn ^= 1;
+        if (rank == 0) {
+          r.turn ^= 1;
+          r.close_list();
+          r.turn ^= 1;
+          r.sort(m);
+          if (threadIdx.x == 0) {
+            const uint64_t at = static_cast<uint64_t>(k) - above - 1;  // (past the end: wraps, is not below m)
+            sh.finds[0] = at < static_cast<uint64_t>(m) ? r.list2[at] : 0ull;
+          }
+        }
+        r.tell(1);
+        set_cut(sh.said[r.turn][0]);
       }
+      if (m < 0 || cut == 0)
+        set_cut(r.select(klo, khi, above, any, [](float) { return static_cast<uint64_t>(1); }, k));
     }
     if (by_p) {
-      if (by_k) {
-        r.find_bins(stays, false, 0, ask.top_p, b0, b1, tokens);
-        r.key_range(b0, b1, klo, khi);
-      }
-      for (;;) {
-        const int shift = Row<DT>::range_shift(klo, khi);
-        r.clear_hist();
-        sum = 0;
-        kept_above = 0;
-        r.each([&](float v, int i) {
-          if (!stays(v, i)) return;
-          const uint32_t key = order_key(v);
-          const uint64_t w = r.weight(v);
-          sum += w;
-          if (key > khi) kept_above += w;
-          else if (key >= klo) r.put((khi - key) >> shift, w);
+      if (by_k) r.template find_bins<false>(stays, false, 0, ask.top_p, b0, b1, tokens);
+      // the same with weights; what stays above the window is kept by warp as well
+      r.key_range(b0, b1, klo, khi);
+      const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
+      uint64_t high = 0, low = 0;  // low: all
+      const int i_cut = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) - r.first : INT32_MAX;
+      r.begin_list();
+      if (cut == 0) {  // (every weight is computed, whatever becomes of it: no branches in between)
+        r.chunks_of([&](const float (&v)[R::kVec], int i) {
+          bool near = false;
+#pragma unroll
+          for (int j = 0; j < R::kVec; ++j) {
+            const uint64_t w = r.weight(v[j]);
+            low += w;
+            if (v[j] > v_hi) high += w;
+            near |= v[j] >= v_lo && v[j] <= v_hi;
+          }
+          if (near) r.bring_some(v, i, v_lo, v_hi);
         });
-        uint64_t above = kept_above;
-        sum = r.total2(sum, above);
-        v_hi = value_of_key(static_cast<uint64_t>(khi) << 32);
-        uint64_t key;
-        if (r.select(klo, khi, above, stays, weigh, needed(sum), key)) {
-          cut = key;
-          break;
-        }
-        klo = 0x007fffffu, khi = order_key(INFINITY);
+      } else {
+        r.chunks_of([&](const float (&v)[R::kVec], int i) {
+          bool near = false;
+#pragma unroll
+          for (int j = 0; j < R::kVec; ++j) {
+            const bool in = v[j] > v_cut || (v[j] == v_cut && i + j <= i_cut);
+            const uint64_t w = r.weight(v[j]) & (in ? ~0ull : 0ull);
+            low += w;
+            if (v[j] > v_hi) high += w;
+            near |= in && v[j] >= v_lo && v[j] <= v_hi;
+          }
+          if (near) r.bring_some(v, i, fmaxf(v_lo, v_cut), v_hi, v_cut, i_cut);
+        });
       }
+      const uint64_t stay = warp_sum64(high);
+      uint64_t above = high;
+      sum = r.total2(low, above);
+      if (lane == 0) st_peer64(&sh.region[rank * kWarps + warp], 0, stay);
+      m = r.end_list();
+      const uint64_t need = ask.needed(sum);
+      if (m >= 0) {
+        uint64_t* said = sh.said[r.turn ^ 1];
+        if (rank == 0) {
+          r.close_list();
+          r.sort(m);
+          uint64_t w[kPer], here = 0, all, keep = 0;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int i = kPer * threadIdx.x + j;
+            w[j] = i < m ? r.weight(value_of_key(r.list2[i])) : 0ull;
+            here += w[j];
+          }
+          uint64_t before = above + r.scan(here, &all);
+          const bool inside = above < need && above + all >= need;
+          if (threadIdx.x == 0) sh.finds[0] = 0;
+          r.clear_hist();
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int i = kPer * threadIdx.x + j;
+            if (inside && i < m && before < need) {
+              const uint64_t key = r.list2[i];
+              if (w[j] && before + w[j] >= need) sh.finds[0] = key;
+              {  // to the sum of the warp that has it
+                const int at = static_cast<int>(~static_cast<uint32_t>(key)), c = at / per;
+                const int o = static_cast<int>((reinterpret_cast<uintptr_t>(g) / sizeof(T) + c * per) % kVec);
+                const int its = min(a.V, (c + 1) * per) - c * per;
+                const int pw = ((o + its + kVec - 1) / kVec + kWarps - 1) / kWarps;
+                const int at3 = 3 * (c * kWarps + (at - c * per + o) / kVec / pw);  // by 15 bits, as no
+                atomicAdd(&r.hist[at3], static_cast<uint32_t>(w[j]) & 0x7fffu);    // 64-bit sums are made there
+                atomicAdd(&r.hist[at3 + 1], static_cast<uint32_t>(w[j] >> 15) & 0x7fffu);
+                atomicAdd(&r.hist[at3 + 2], static_cast<uint32_t>(w[j] >> 30));
+              }
+            }
+            before += w[j];
+          }
+          __syncthreads();
+          // the warp that has the token drawn
+          const int regions = C * kWarps;
+          if (static_cast<int>(threadIdx.x) < regions)
+            keep = sh.region[threadIdx.x] + r.hist[3 * threadIdx.x] + (static_cast<uint64_t>(r.hist[3 * threadIdx.x + 1]) << 15) +
+                   (static_cast<uint64_t>(r.hist[3 * threadIdx.x + 2]) << 30);
+          const uint64_t from = r.scan(keep, &all);
+          const uint64_t target = times_fraction(all, ask.u);
+          if (target >= from && target < from + keep) {
+            sh.finds[1] = threadIdx.x;
+            sh.finds[2] = target - from;
+          }
+          if (threadIdx.x == 0) sh.finds[3] = all;
+        }
+        r.turn ^= 1;
+        r.tell(4);
+        if (said[0]) set_cut(said[0]);
+        if (said[0] && ask.w_min == 0) {
+          const int region = static_cast<int>(said[1]);
+          if (region / kWarps != rank) return;
+          const uint64_t all = said[3];
+          r.locate_in(region % kWarps, kept, said[2], [&](float v, int i) { write(v, i, all); });
+          return;
+        }
+      }
+      if (m < 0 || sh.said[r.turn][0] == 0)
+        set_cut(r.select(klo, khi, above, stays, [&](float v) { return r.weight(v); }, need));
     }
   }
 
   // --------------------------------------------------------------- the draw
-  const auto kept = [&](float v, int i) {
-    if (!stays(v, i)) return static_cast<uint64_t>(0);
-    const uint64_t w = r.weight(v);
-    return w >= ask.w_min ? w : static_cast<uint64_t>(0);
-  };
-  uint64_t all = 0;
-  if (v_hi < INFINITY && ask.w_min == 0) {  // what lies above the range was summed there
-    all = kept_above;
-    r.each([&](float v, int i) {
-      if (v <= v_hi) all += kept(v, i);
-    });
-    all = r.total(all);
-  } else {
-    all = r.sum(kept);
-  }
-  r.locate(kept, times_fraction(all, ask.u), [&](float v, int i) {
-    *token = r.first + i;
-    if (logprob) *logprob = log_share(r.wt, v, r.weight(v), all);
-  });
+  const uint64_t all = r.sum(kept);
+  r.locate(kept, times_fraction(all, ask.u), [&](float v, int i) { write(v, i, all); });
 }
 
-template <int DT>
-moe_status_t launch(const moe_sampling_t& a, cudaStream_t st) {
-  // a row's CTAs: slices of at most 16384 elements where 8 of them do, and shorter ones
-  // while SMs would be left without any
-  const auto slice = [&](int C) { return ((a.V - 1) / C + 1 + kThreads - 1) / kThreads * kThreads; };
-  int C = 1;
-  while (C < kMaxCtas && (slice(C) > 16384 || (static_cast<int64_t>(a.B) * C * 2 <= sm_count() && slice(C) > 2048)))
-    C *= 2;
-  const int per = slice(C);
-  // the slice with room for its alignment, or a list over it; the bins; a list
-  const uint32_t slice_bytes =
-      std::max(static_cast<uint32_t>(per * sizeof(typename Stored<DT>::T)) + 32u, kListBytes);
-  const size_t smem = slice_bytes + kHistBytes + kListBytes;
-  if (raise_smem_limit(sample_kernel<DT>, smem) != cudaSuccess) return check_launch("sample_kernel (smem)");
+template <int DT, bool HELD>
+moe_status_t launch_as(const moe_sampling_t& a, int C, int per, cudaStream_t st) {
+  const uint32_t slice_bytes = HELD ? static_cast<uint32_t>(per * sizeof(typename Stored<DT>::T)) + 32u : 0u;
+  const size_t smem = slice_bytes + kHistBytes + 2 * kListBytes;
+  if (raise_smem_limit(sample_kernel<DT, HELD>, smem) != cudaSuccess) return check_launch("sample_kernel (smem)");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * C);
   cfg.blockDim = dim3(kThreads);
@@ -919,9 +1143,24 @@ moe_status_t launch(const moe_sampling_t& a, cudaStream_t st) {
   attr[1].val.clusterDim = {static_cast<unsigned>(C), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, sample_kernel<DT>, a, C, per, slice_bytes) != cudaSuccess) return check_launch("sample_kernel");
+  if (cudaLaunchKernelEx(&cfg, sample_kernel<DT, HELD>, a, C, per, slice_bytes) != cudaSuccess)
+    return check_launch("sample_kernel");
   stat_kernels(1);
   return MOE_OK;
+}
+
+template <int DT>
+moe_status_t launch(const moe_sampling_t& a, cudaStream_t st) {
+  const auto slice = [&](int C) { return ((a.V - 1) / C + 1 + kThreads - 1) / kThreads * kThreads; };
+  // A row's CTAs: about the two that an SM holds of every SM, or half as many again (rows differ in
+  // what they ask for: 64 rows of all kinds take 90 us by 4 CTAs, 72 by 8), of slices that are worth it.
+  int C = 1;
+  while (C < kMaxCtas && static_cast<int64_t>(a.B) * C * 10 <= 17 * sm_count() && slice(C) > 2048) C *= 2;
+  const int per = slice(C);
+  // Held in shared memory where two CTAs still fit an SM, or one where there are no more CTAs.
+  constexpr int size = sizeof(typename Stored<DT>::T);
+  const int64_t held = static_cast<int64_t>(per) * size, fits = a.B * static_cast<int64_t>(C) <= sm_count() ? 200000 : 90000;
+  return held <= fits ? launch_as<DT, true>(a, C, per, st) : launch_as<DT, false>(a, C, per, st);
 }
 
 }  // namespace

@@ -156,6 +156,32 @@ def test_a_rows_result_depends_on_no_other_row(m):
         assert t1[0] == tokens[b] and l1[0] == lp[b]
 
 
+@pytest.mark.parametrize("dtype,V", [(F32, 30000), (BF, 60001), (F32, 2049), (FP, 50007)])
+def test_many_long_rows(m, dtype, V):
+    """More rows than SMs: a CTA per row, which does not hold a long one in shared memory."""
+    g = torch.Generator().manual_seed(V)
+    B = 180
+    logits = torch.randn(B, V + 3, generator=g) * torch.linspace(0.05, 4.0, B)[:, None]
+    logits[::7] = (logits[::7] * 4).round() / 4  # ties
+    logits = logits.to(dtype)
+    asks = (ASKS[:9] * 20)[:B]
+    view = logits[:, 3:]
+    us, refs = _refs(view, asks, g)
+    _same(_run(m, logits.to(DEV)[:, 3:], asks, us), refs)
+
+
+@pytest.mark.parametrize("spread", [1e-6, 0.01, 0.3])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_nearly_flat_rows(m, dtype, spread):
+    """Every filter ends among thousands of tokens of almost the same weight."""
+    g = torch.Generator().manual_seed(3)
+    logits = (torch.randn(10, 90000, generator=g) * spread + 5).to(dtype)
+    asks = [OFF, (1.0, 0, 0.9, 0.0), (1.0, 45000, 1.0, 0.0), (1.0, 45000, 0.5, 0.0), (0.3, 0, 0.1, 0.0), (1.0, 3000, 0.7, 0.5),
+            (1.0, 0, 0.5, 0.999), (1.0, 600, 1.0, 0.0), (1.0, 1, 1.0, 0.0), (9.0, 89999, 0.99999, 0.0)]
+    us, refs = _refs(logits, asks, g)
+    _same(_run(m, logits.to(DEV), asks, us), refs)
+
+
 def test_draws_follow_the_weights(m):
     """Every token of a small row as often as its weight says: uniforms on a grid."""
     n = 4096
