@@ -155,22 +155,28 @@ def _load():
 # The compiled form of the layer operators' checks (csrc/fast_call.cpp): returns
 # the entry's status, or -1 for arguments that the Python form is to explain.
 _fast = None
+_fast_projections = None  # the same of the quantisation, the 8-bit product and the drawing of tokens
 
 
 def _bind_fast_call(lib):
-    global _fast
+    global _fast, _fast_projections
     try:
         from . import _fast_call
     except ImportError:  # not built here: the Python form does the same
         return
     entries = (lib.moe_add_rmsnorm, lib.moe_rope_append, lib.moe_paged_attention)
     structs = (_NORM_T, _CACHE_T, _ROPE_T, _ATTN_T)
+    at = lambda fs: (ctypes.cast(f, ctypes.c_void_p).value for f in fs)  # noqa: E731
     if getattr(_fast_call, "built_for", None) != torch.__version__ or not _fast_call.bind(
-            *(ctypes.cast(f, ctypes.c_void_p).value for f in entries), *(t.size for t in structs)):
+            *at(entries), *(t.size for t in structs)):
         warnings.warn("the compiled argument checks were built for another PyTorch or header and are not used: "
                       "build them with __graft_entry__.build()")
         return
     _fast = _fast_call
+    bind = getattr(_fast_call, "bind_projections", None)
+    if bind is not None and bind(*at((lib.moe_quantize_e4m3, lib.moe_linear_e4m3, lib.moe_sample)), _QUANT_T.size,
+                                 _LINEAR_T.size, _SAMPLING_T.size):
+        _fast_projections = _fast_call
 
 
 def library():
@@ -623,6 +629,12 @@ def moe_quantize_e4m3(x, out, scales, rows=1, stream=None):
     """``x`` [T, H] (float16 or bfloat16) to float8_e4m3fn ``out`` [T, H] with one
     fp32 scale per block of ``rows`` (1: activations, 128: weights) by 128 elements
     in ``scales`` [ceil(T / rows), ceil(H / 128)].  Rows may be strided."""
+    if _fast_projections is not None:
+        rc = _fast_projections.quant(x, out, scales, rows, stream)
+        if rc == 0:
+            return
+        if rc > 0:
+            _check(rc)
     shape, dt, dev = _tensor(x, "x").shape, x.dtype, x.get_device()
     if len(shape) != 2:
         raise ValueError(f"x: shape {tuple(shape)}, expected [T, H]")
@@ -656,6 +668,12 @@ def moe_linear_e4m3(x, x_scales, w, w_scales, out, ws, stream=None):
     128)], ``w`` with ``w_scales`` [ceil(N / 128), ceil(K / 128)] fp32, as
     moe_quantize_e4m3 (rows 1 and 128) and moe_add_rmsnorm (group 128) leave
     them.  Row strides of x and w are multiples of 16; those of out are free."""
+    if _fast_projections is not None:
+        rc = _fast_projections.linear(x, x_scales, w, w_scales, out, ws, stream)
+        if rc == 0:
+            return
+        if rc > 0:
+            _check(rc)
     dev = _tensor(x, "x").get_device()
     if x.dim() != 2 or _tensor(w, "w").dim() != 2:
         raise ValueError(f"x and w: shapes {tuple(x.shape)} and {tuple(w.shape)}, expected [M, K] and [N, K]")
@@ -686,6 +704,12 @@ def moe_sample(logits, uniforms, tokens, temperature=None, top_k=None, top_p=Non
     what each row's ``temperature``, ``top_p``, ``min_p`` [B] fp32 and ``top_k`` [B]
     int32 leave (None: temperature 1, no filter), and its log-probability there
     into ``logprobs`` [B] fp32.  A row of -infinity gives token -1."""
+    if _fast_projections is not None:
+        rc = _fast_projections.sample(logits, uniforms, tokens, temperature, top_k, top_p, min_p, logprobs, stream)
+        if rc == 0:
+            return
+        if rc > 0:
+            _check(rc)
     shape, dev = _tensor(logits, "logits").shape, logits.get_device()
     if len(shape) != 2 or not shape[1]:
         raise ValueError(f"logits: shape {tuple(shape)}, expected [B, V]")

@@ -23,6 +23,12 @@ namespace {
 using NormFn = moe_status_t (*)(const moe_norm_t*, void*);
 using RopeFn = moe_status_t (*)(const moe_kv_cache_t*, const moe_rope_t*, void*, size_t, void*);
 using AttnFn = moe_status_t (*)(const moe_kv_cache_t*, const moe_attention_t*, void*, size_t, void*);
+using QuantFn = moe_status_t (*)(const moe_quant_t*, void*);
+using LinearFn = moe_status_t (*)(const moe_linear_t*, void*, size_t, void*);
+using SampleFn = moe_status_t (*)(const moe_sampling_t*, void*);
+QuantFn quant_entry = nullptr;
+LinearFn linear_entry = nullptr;
+SampleFn sample_entry = nullptr;
 NormFn norm_entry = nullptr;
 RopeFn rope_entry = nullptr;
 AttnFn attn_entry = nullptr;
@@ -218,6 +224,127 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(attn_entry(c, &m, ws->data_ptr(), ws->nbytes(), st));
 }
 
+// quant(x, out, scales, rows, stream)
+PyObject* quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const at::Tensor *x, *out, *sc;
+  if (n != 5 || !quant_entry || !(x = tensor(a[0])) || !(out = tensor(a[1])) || !(sc = tensor(a[2]))) return leave_it();
+  const long rows_of = PyLong_AsLong(a[3]);
+  if (PyErr_Occurred() || !x->is_cuda() || x->dim() != 2 || (rows_of != 1 && rows_of != 128)) return leave_it();
+  const int dev = x->get_device();
+  const int64_t T = x->size(0), H = x->size(1);
+  const at::ScalarType dt = x->scalar_type();
+  const int code = float_code(dt);
+  if (!code || T > kIntMax || H > kIntMax || !rows(x, {T, H}, dt, dev) || !rows(out, {T, H}, at::kFloat8_e4m3fn, dev) ||
+      !flat(sc, {(T + rows_of - 1) / rows_of, (H + 127) / 128}, at::kFloat, dev))
+    return leave_it();
+  moe_quant_t m;
+  m.x = x->data_ptr();
+  m.out = out->data_ptr();
+  m.scales = static_cast<float*>(sc->data_ptr());
+  m.x_stride = x->stride(0);
+  m.out_stride = out->stride(0);
+  m.T = static_cast<int32_t>(T);
+  m.H = static_cast<int32_t>(H);
+  m.rows = static_cast<int32_t>(rows_of);
+  m.dtype = code;
+  void* st;
+  if (!stream_of(a[4], dev, &st)) return leave_it();
+  return PyLong_FromLong(quant_entry(&m, st));
+}
+
+// linear(x, x_scales, w, w_scales, out, ws, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const at::Tensor* t[6];
+  if (n != 7 || !linear_entry) return leave_it();
+  for (int i = 0; i < 6; ++i)
+    if (!(t[i] = tensor(a[i]))) return leave_it();
+  const at::Tensor &x = *t[0], &w = *t[2], &out = *t[4], &ws = *t[5];
+  if (!x.is_cuda() || x.dim() != 2 || w.dim() != 2) return leave_it();
+  const int dev = x.get_device();
+  const int64_t M = x.size(0), K = x.size(1), N = w.size(0), kb = (K + 127) / 128;
+  const at::ScalarType dt = out.scalar_type();
+  const int code = dt == at::kFloat ? MOE_F32 : float_code(dt);
+  if (!code || M > kIntMax || N > kIntMax || K > kIntMax || !rows(&x, {M, K}, at::kFloat8_e4m3fn, dev) ||
+      !flat(t[1], {M, kb}, at::kFloat, dev) || !rows(&w, {N, K}, at::kFloat8_e4m3fn, dev) ||
+      !flat(t[3], {(N + 127) / 128, kb}, at::kFloat, dev) || !rows(&out, {M, N}, dt, dev) || !workspace(ws, dev))
+    return leave_it();
+  moe_linear_t m;
+  m.x = x.data_ptr();
+  m.x_scales = static_cast<const float*>(t[1]->data_ptr());
+  m.w = w.data_ptr();
+  m.w_scales = static_cast<const float*>(t[3]->data_ptr());
+  m.out = out.data_ptr();
+  m.x_stride = x.stride(0);
+  m.w_stride = w.stride(0);
+  m.out_stride = out.stride(0);
+  m.M = static_cast<int32_t>(M);
+  m.N = static_cast<int32_t>(N);
+  m.K = static_cast<int32_t>(K);
+  m.out_dtype = code;
+  void* st;
+  if (!stream_of(a[6], dev, &st)) return leave_it();
+  return PyLong_FromLong(linear_entry(&m, ws.data_ptr(), ws.nbytes(), st));
+}
+
+// sample(logits, uniforms, tokens, temperature, top_k, top_p, min_p, logprobs, stream)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const at::Tensor *l, *u, *tok;
+  if (n != 9 || !sample_entry || !(l = tensor(a[0])) || !(u = tensor(a[1])) || !(tok = tensor(a[2])) || !l->is_cuda() ||
+      l->dim() != 2)
+    return leave_it();
+  const int dev = l->get_device();
+  const int64_t B = l->size(0), V = l->size(1);
+  const at::ScalarType dt = l->scalar_type();
+  const int code = dt == at::kFloat ? MOE_F32 : float_code(dt);
+  if (!code || !V || B > kIntMax || V > kIntMax || !rows(l, {B, V}, dt, dev) || !flat(u, {B}, at::kFloat, dev) ||
+      !flat(tok, {B}, at::kLong, dev))
+    return leave_it();
+  void* p[5];  // temperature top_k top_p min_p logprobs
+  for (int i = 0; i < 5; ++i) {
+    p[i] = nullptr;
+    if (a[3 + i] == Py_None) continue;
+    const at::Tensor* t = tensor(a[3 + i]);
+    if (!flat(t, {B}, i == 1 ? at::kInt : at::kFloat, dev)) return leave_it();
+    p[i] = t->data_ptr();
+  }
+  moe_sampling_t m;
+  m.logits = l->data_ptr();
+  m.uniforms = static_cast<const float*>(u->data_ptr());
+  m.temperature = static_cast<const float*>(p[0]);
+  m.top_k = static_cast<const int32_t*>(p[1]);
+  m.top_p = static_cast<const float*>(p[2]);
+  m.min_p = static_cast<const float*>(p[3]);
+  m.tokens = static_cast<int64_t*>(tok->data_ptr());
+  m.logprobs = static_cast<float*>(p[4]);
+  m.logits_stride = l->stride(0);
+  m.B = static_cast<int32_t>(B);
+  m.V = static_cast<int32_t>(V);
+  m.dtype = code;
+  void* st;
+  if (!stream_of(a[8], dev, &st)) return leave_it();
+  return PyLong_FromLong(sample_entry(&m, st));
+}
+
+// bind_projections(moe_quantize_e4m3, moe_linear_e4m3, moe_sample, sizes of moe_quant_t, moe_linear_t,
+// moe_sampling_t): as bind().
+PyObject* bind_projections(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "three addresses and three sizes expected");
+    return nullptr;
+  }
+  void* entries[3];
+  for (int i = 0; i < 3; ++i) entries[i] = PyLong_AsVoidPtr(a[i]);
+  const size_t sizes[3] = {sizeof(moe_quant_t), sizeof(moe_linear_t), sizeof(moe_sampling_t)};
+  bool same = true;
+  for (int i = 0; i < 3; ++i) same &= PyLong_AsSize_t(a[3 + i]) == sizes[i];
+  if (PyErr_Occurred()) return nullptr;
+  if (!same) Py_RETURN_FALSE;
+  quant_entry = reinterpret_cast<QuantFn>(entries[0]);
+  linear_entry = reinterpret_cast<LinearFn>(entries[1]);
+  sample_entry = reinterpret_cast<SampleFn>(entries[2]);
+  Py_RETURN_TRUE;
+}
+
 // bind(moe_add_rmsnorm, moe_rope_append, moe_paged_attention: the loaded library's entries,
 // sizes of moe_norm_t, moe_kv_cache_t, moe_rope_t, moe_attention_t): False, and nothing
 // bound, where the structs compiled here are others.
@@ -255,7 +382,9 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<norm>("norm"), method<rope>("rope"), method<attention>("attention"),
-                         method<bind>("bind"), {nullptr, nullptr, 0, nullptr}};
+                         method<bind>("bind"), method<quant>("quant"), method<linear>("linear"),
+                         method<sample>("sample"), method<bind_projections>("bind_projections"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
