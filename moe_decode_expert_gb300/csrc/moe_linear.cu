@@ -317,21 +317,25 @@ __global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
 }
 
 // =========================================================== many rows
-// Tiles of 256 tokens by 256 weight rows, each of a pair of CTAs: the tokens are the
-// MMA's M (128 per CTA), the weight rows its N, and each CTA stages half of both (32 KB
-// a block), so that a pair reads every byte once.  The sums of a token's 256 columns
-// are in 4 threads' registers, 64 each; 16 warps read a block's product from tensor
-// memory (two accumulators of 256 columns) while the next is made.
+// Tiles of 256 tokens by 128 weight rows, each of a pair of CTAs: the tokens are the
+// MMA's M (128 per CTA), the weight rows its N, and each CTA stages half of both (24 KB
+// a block), so that a pair reads every byte once.  Four accumulators of 128 columns fill
+// the tensor memory: what a block costs is the way from its product to the epilogue and
+// back (two of 256 columns: 204 us for 8192 x 5120 x 4096).  The sums of a token's 128
+// columns are in 2 threads' registers, 64 each.
 struct Many {
-  static constexpr uint32_t kStage = 2 * kTile;
-  static constexpr int kStages = 5;
-  static constexpr int kWarps = 16;  // of the epilogue
+  static constexpr int kN = 128;
+  static constexpr uint32_t kStage = kTile + kN / 2 * kBlock;
+  static constexpr int kStages = 7;
+  static constexpr int kAcc = 4;
+  // Threads that issue MMAs, block by block in turn: what one does for a block (two waits, four
+  // MMAs, two commits) takes it about 1000 cycles, a block's MMAs 256 (one: 272 us, two: XXX).
+  static constexpr int kIssuers = 2;
+  static constexpr int kWarps = 8;  // of the epilogue
   static constexpr int kThreads = 128 + 32 * kWarps;
-  // registers per thread: 96 at launch (five warps on each of the SM's quarters); the first four
-  // warps give up what the others take, 128 * 56 + 512 * 104 <= 640 * 96
-  static constexpr int kChunk = 16;                        // blocks whose scales are staged at a time,
-  static constexpr int kScales = kChunk * (128 + 2);       // floats: the rows' and the two weight blocks'
-  static constexpr uint32_t kTurn = 32 * 64;               // bytes a warp turns its results in
+  static constexpr int kChunk = 16;                   // blocks whose scales are staged at a time,
+  static constexpr int kScales = kChunk * 128 + kChunk;  // floats: the rows' and the weight block's
+  static constexpr uint32_t kTurn = 32 * 64;          // bytes a warp turns its results in
   static constexpr size_t kSmem = kStages * kStage + 2 * kScales * 4 + kWarps * kTurn + 1024;
 };
 
@@ -349,6 +353,12 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, u
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // Arrives on the barrier at this offset in both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
@@ -415,17 +425,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
   using G = Many;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], tfull[2], tempty[2], done;
+  __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], tfull[G::kAcc], tempty[G::kAcc], sfull[2], sempty[2],
+      done[G::kIssuers];
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int s_abort;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x & 1u);  // in the pair; 0 issues the MMAs
   const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < G::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * G::kWarps); }
-    mbar_init(&done, 1);
+    for (int b = 0; b < G::kAcc; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * G::kWarps); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&sfull[b], 32); mbar_init(&sempty[b], G::kWarps); }
+    for (int i = 0; i < G::kIssuers; ++i) mbar_init(&done[i], 1);
     mbar_fence_init();
     s_abort = 0;
     tensormap_prefetch(&mapX);
@@ -446,13 +458,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
   pdl_wait();
   const uint32_t tbase = tmem_base_s;
 
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     if (lane == 0) {  // ---------------------------------------------- TMA producer
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
       for (int t = first; t < tiles && !s_abort; t += step) {
-        const int m0 = t % mtiles * 256 + rank * 128, n0 = t / mtiles * 256 + rank * 128;
+        const int m0 = t % mtiles * 256 + rank * 128, n0 = t / mtiles * G::kN + rank * (G::kN / 2);
         for (int kb = 0; kb < KB; ++kb) {
           if (!tc_wait_polled(&empty[stage], phase ^ 1u, timeout, &s_abort)) {
             s_abort = 1;
@@ -475,108 +486,125 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
           if (issued_mask & (1u << s)) mbar_wait_until(&full[s], (issued_phase >> s) & 1u, global_ns() + timeout);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {  // --------------------------------- MMA issuer
-      constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(256 >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
-      int stage = 0, b = 0;
+  } else if (warp <= G::kIssuers) {
+    if (rank == 0) {  // ---------------------------------------------- MMA issuers
+      // (the whole warp goes through the loop and one thread of it issues: with the others gone, an
+      // MMA's descriptors are moved to the uniform registers it takes them from one by one)
+      constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(G::kN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
+      const int blocks = first < tiles ? ((tiles - 1 - first) / step + 1) * KB : 0;
+      const uint64_t adesc = sw128_desc(smem_u32(smem)), bdesc = sw128_desc(smem_u32(smem) + kTile);
+      int stage = warp - 1, b = warp - 1;
       uint32_t phase = 0, bphase = 0;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += step)
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!tc_wait_polled(&tempty[b], bphase ^ 1u, timeout, &s_abort) ||
-              !tc_wait_polled(&full[stage], phase, timeout, &s_abort)) {
-            s_abort = 1;
-            report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sA = smem_u32(smem + stage * G::kStage), sB = sA + kTile;
+      for (int i = warp - 1; i < blocks; i += G::kIssuers) {
+        if (!__all_sync(0xffffffffu, tc_wait_polled(&tempty[b], bphase ^ 1u, timeout, &s_abort) &&
+                                         tc_wait_polled(&full[stage], phase, timeout, &s_abort))) {
+          s_abort = 1;
+          if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+          break;
+        }
+        tc_fence_after();
+        const uint64_t at = static_cast<uint64_t>(stage) * (G::kStage >> 4);  // of a descriptor's address
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_e4m3_pair(tbase + static_cast<uint32_t>(b * 256), sw128_desc(sA + 32 * k), sw128_desc(sB + 32 * k), idesc,
-                          k != 0);
+            mma_e4m3_pair(tbase + static_cast<uint32_t>(b * G::kN), adesc + at + 2 * k, bdesc + at + 2 * k, idesc, k != 0);
           tc_commit_pair(&empty[stage]);
           tc_commit_pair(&tfull[b]);
-          if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-          b ^= 1;
-          bphase ^= b == 0;
         }
-      // completes once every MMA issued above has completed
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done))
-                   : "memory");
-      mbar_wait_until(&done, 0, global_ns() + timeout);
+        __syncwarp();
+        stage += G::kIssuers;
+        if (stage >= G::kStages) { stage -= G::kStages; phase ^= 1u; }
+        b += G::kIssuers;
+        if (b >= G::kAcc) { b -= G::kAcc; bphase ^= 1u; }
+      }
+      if (elect_one()) {
+        // completes once every MMA that this thread issued has completed
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(&done[warp - 1]))
+                     : "memory");
+        mbar_wait_until(&done[warp - 1], 0, global_ns() + timeout);
+      }
     }
     __syncwarp();
-  } else if (warp >= 4) {  // ------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    const int q = warp & 3, g = (warp - 4) >> 2;  // quarter of the TMEM lanes, quarter of the columns
-    const int etid = threadIdx.x - 128;
+  } else if (warp < 4) {  // ------------------------------------------- scales
+    // A chunk's scales, two chunks in turn: four rows a thread, and the weight block's.  (Loaded by each
+    // thread of the epilogue for its own row they missed L1, which 128 rows a line apart overflow.)
+    float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage);
+    int buf = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const int m0 = t % mtiles * 256 + rank * 128, nb = t / mtiles;
+      for (int kb0 = 0; kb0 < KB; kb0 += G::kChunk) {
+        ok = __all_sync(0xffffffffu, tc_wait_polled(&sempty[buf], phase ^ 1u, timeout, &s_abort));
+        if (!ok) break;
+        float* sc = scales + buf * G::kScales;
+        if (lane < G::kChunk && kb0 + lane < KB)
+          sc[G::kChunk * 128 + lane] = a.w_scales[static_cast<int64_t>(nb) * KB + kb0 + lane];
+#pragma unroll 1
+        for (int r = lane; r < 128; r += 32) {
+          const float* from = a.x_scales + static_cast<int64_t>(min(m0 + r, a.M - 1)) * KB + kb0;
+          float v[G::kChunk];
+#pragma unroll
+          for (int i = 0; i < G::kChunk; ++i) v[i] = kb0 + i < KB ? from[i] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < G::kChunk; ++i) sc[i * 128 + r] = v[i];
+        }
+        mbar_arrive(&sfull[buf]);
+        buf ^= 1;
+        phase ^= buf == 0;
+      }
+    }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+    }
+  } else {  // ------------------------------------------------------- epilogue
+    const int q = warp & 3, g = (warp - 4) >> 2;  // quarter of the TMEM lanes, half of the columns
     const uint32_t lane0 = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(64 * g);
     const uint32_t free_bar = peer_addr(smem_u32(&tempty[0]), 0);
     float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage);
     uint8_t* turn = reinterpret_cast<uint8_t*>(scales + 2 * G::kScales) + (warp - 4) * G::kTurn;
-    // A chunk's scales go through registers one chunk ahead: 4 blocks of a row per thread, and
-    // one of a weight block in 32 of them.  (Loaded by each thread for its own row they missed
-    // L1, which 128 rows 4 KB / 32 apart overflow: 1.15 us per block.)
-    float next[4], next_w = 0.0f;
-    const auto fetch = [&](int t, int kb0) {
-      const int m = min(t % mtiles * 256 + rank * 128 + (etid >> 2), a.M - 1);
-      const int kb = kb0 + (etid & 3) * 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) next[j] = kb + j < KB ? a.x_scales[static_cast<int64_t>(m) * KB + kb + j] : 0.0f;
-      if (etid < 2 * G::kChunk && kb0 + (etid >> 1) < KB)
-        next_w = a.w_scales[static_cast<int64_t>(min(t / mtiles * 256 + 128 * (etid & 1), a.N - 1) / 128) * KB + kb0 +
-                            (etid >> 1)];
-    };
-    int b = 0, buf = 0;
-    uint32_t bphase = 0;
+    int b = 0, buf = 0, in = 0;  // accumulator; chunk of scales and block in it
+    uint32_t bphase = 0, sphase = 0;
     bool ok = true;
-    if (first < tiles) fetch(first, 0);
     for (int t = first; t < tiles; t += step) {
       float acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0.0f;
-      for (int kb0 = 0; kb0 < KB; kb0 += G::kChunk) {
-        float* sc = scales + buf * G::kScales;
-        buf ^= 1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc[((etid & 3) * 4 + j) * 128 + (etid >> 2)] = next[j];
-        if (etid < 2 * G::kChunk) sc[G::kChunk * 128 + etid] = next_w;
-        named_bar_sync(1, 32 * G::kWarps);  // (also: every warp is past the chunk before the last, whose place this was)
-        if (kb0 + G::kChunk < KB) fetch(t, kb0 + G::kChunk);
-        else if (t + step < tiles) fetch(t + step, 0);
-        const int n = min(G::kChunk, KB - kb0);
-        for (int i = 0; i < n; ++i) {
-          // (a wait that ran out leaves the loops running without it, so that all warps meet at the barriers)
-          ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], bphase, timeout, &s_abort));
-          if (!ok) {
-            s_abort = 1;
-            continue;
-          }
-          tc_fence_after();
-          const float s = sc[i * 128 + 32 * q + lane] * sc[G::kChunk * 128 + 2 * i + (g >> 1)];
-          const uint32_t ta = lane0 + static_cast<uint32_t>(b * 256);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t v[16];
-            tmem_ld16_issue(ta + 16 * h, v);
-            tmem_ld_wait();
-            tmem_ld_tie(v);
-            if (h == 3) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[16 * h + j] = fmaf(__uint_as_float(v[j]), s, acc[16 * h + j]);
-          }
-          b ^= 1;
-          bphase ^= b == 0;
+      for (int kb = 0; kb < KB; ++kb) {
+        // (a wait that ran out leaves the loops running without it, so that all warps end together)
+        if (in == 0) ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&sfull[buf], sphase, timeout, &s_abort));
+        const float* sc = scales + buf * G::kScales;
+        const float s = sc[in * 128 + 32 * q + lane] * sc[G::kChunk * 128 + in];
+        if (++in == G::kChunk || kb + 1 == KB) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[buf]);
+          in = 0;
+          buf ^= 1;
+          sphase ^= buf == 0;
         }
+        ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], bphase, timeout, &s_abort));
+        if (!ok) {
+          s_abort = 1;
+          continue;
+        }
+        tc_fence_after();
+        uint32_t v[2][32];
+        tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * G::kN), v[0]);
+        tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * G::kN + 32), v[1]);
+        tmem_ld_wait();
+        tmem_ld_tie(v[0]);
+        tmem_ld_tie(v[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
+#pragma unroll
+        for (int j = 0; j < 64; ++j) acc[j] = fmaf(__uint_as_float(v[j / 32][j % 32]), s, acc[j]);
+        if (++b == G::kAcc) { b = 0; bphase ^= 1u; }
       }
       if (!ok) continue;
-      const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * 256 + 64 * g;
+      const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * G::kN + 64 * g;
       if (m0 >= a.M || n0 >= a.N) continue;
       if (a.out_dtype == MOE_F32) many_store<4>(a, acc, turn, m0, n0, lane, wide);
       else many_store<2>(a, acc, turn, m0, n0, lane, wide);
@@ -640,9 +668,9 @@ moe_status_t launch_few(const moe_linear_t& l, int KB, Control* ctrl, cudaStream
 
 moe_status_t launch_many(const moe_linear_t& l, int KB, Control* ctrl, cudaStream_t st) {
   const int mtiles = (l.M - 1) / 256 + 1;
-  const int tiles = mtiles * ((l.N - 1) / 256 + 1);
+  const int tiles = mtiles * ((l.N - 1) / Many::kN + 1);
   CUtensorMap mx, mw;
-  if (!byte_map(&mx, l.x, l.K, l.M, l.x_stride, 128) || !byte_map(&mw, l.w, l.K, l.N, l.w_stride, 128))
+  if (!byte_map(&mx, l.x, l.K, l.M, l.x_stride, 128) || !byte_map(&mw, l.w, l.K, l.N, l.w_stride, Many::kN / 2))
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
   if (raise_smem_limit(linear_many_kernel, Many::kSmem) != cudaSuccess) return check_launch("linear_many_kernel (smem)");
   const int per = l.out_dtype == MOE_F32 ? 4 : 8;
