@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kBlock = 128;               // columns (and weight rows) of a scale
 constexpr uint32_t kTile = 128 * kBlock;  // bytes of 128 rows of a block
-constexpr int kFewRows = 128;             // up to here the weight is the MMA's M
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, A and B e4m3, both
 // K-major, M = 128, N.
@@ -53,6 +52,8 @@ __device__ __forceinline__ uint32_t pack2(int dt, float a, float b) {
 
 // Cluster-wide barrier in two halves; every thread of every CTA takes part in both.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// (after the fence of set-up barriers, which is all that it has to order)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // The address in CTA `rank`'s shared memory that `addr` is in this one's.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
@@ -60,43 +61,50 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// Copy of this CTA's shared memory into another's, counted on a barrier there.
-__device__ __forceinline__ void bulk_to_peer(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
-      : "memory");
+// 8 or 16 bytes into another CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void send8(uint32_t dst, float a, float b, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1,%2}, [%3];" ::"r"(dst), "f"(a),
+               "f"(b), "r"(bar)
+               : "memory");
 }
-// Writes of this thread to shared memory, made visible to copies.
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void send16(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(dst),
+               "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
+               : "memory");
+}
 
 // ============================================================ few rows
 // The weight's rows are the MMA's M (128 per tile) and NT tokens its N, so the
 // weight, the larger operand, is streamed once for them.  S CTAs of a cluster share
 // a tile's blocks of K; each then adds the S partial sums (in the order of K) of 1 / S
-// of the columns, which the others send it as one copy each.  (Plain stores to
-// another CTA's shared memory took 0.35 us per column.)
+// of the columns, which the others send from their registers to its shared memory.
 template <int NT>
 struct Few {
   static constexpr uint32_t kStage = kTile + NT * kBlock;
-  static constexpr int kMaxStages = NT == 128 ? 4 : 5;
   static constexpr int kAcc = NT <= 32 ? 4 : 2;  // accumulators in tensor memory
   static constexpr uint32_t kCols = NT * kAcc;
   static constexpr int kChunk = 16;       // blocks whose scales are staged at a time
   static constexpr int kPitch = NT + 4;   // floats per block of staged scales
   static constexpr uint32_t kScales = kChunk * kPitch * 4;
-  // Of a CTA's shared memory: the ring, one or two chunks of scales, and the others' sums of
-  // its columns.  At least the share that its columns are of the SM's 512, so that no CTA
-  // waits for columns that another holds.
+  static constexpr uint32_t kParts = NT * 512;  // sums of this CTA's columns, S > 1
+  static constexpr int kMaxStages = 5;
+  // Of a CTA's shared memory: the ring, one or two chunks of scales, the sums.  At least the
+  // share that its columns are of the SM's 512, so that no CTA waits for columns that another
+  // holds.
   static size_t smem(int stages, int nkb, int S) {
-    const size_t n = stages * kStage + (nkb > kChunk ? 2 : 1) * kScales + (S > 1 ? (NT + S) * 512 : 0) + 1024;
+    const size_t n = stages * kStage + (nkb > kChunk ? 2 : 1) * kScales + (S > 1 ? kParts : 0) + 1024;
     const size_t least = static_cast<size_t>(kCols) * 227 * 1024 / 512;
     return n < least ? least : n;
+  }
+  static int stages(int nkb, int S) {
+    int n = std::min(kMaxStages, std::max(nkb, 2));
+    while (n > 2 && smem(n, nkb, S) > 113 * 1024) --n;  // two CTAs fit an SM
+    return n;
   }
 };
 
 template <int NT>
-__global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
+__global__ void __launch_bounds__(192, 2)
     linear_few_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
                       moe_linear_t a, int KB, int S, int mtiles, int stages, Control* ctrl, uint64_t timeout) {
   using F = Few<NT>;
@@ -114,7 +122,9 @@ __global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
   const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / S);
   const int nkb = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / S) - kb0;
   float* parts = scales + ((KB + S - 1) / S > F::kChunk ? 2 : 1) * (F::kScales / 4);
-  const int width = (NT + S - 1) / S;  // columns whose sums this CTA adds
+  const int width = NT / S;  // columns whose sums this CTA adds: fours, or two
+  constexpr int kMinVec = NT == 16 ? 2 : 4;
+  const int vec = NT == 16 && width == 2 ? 2 : 4;
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int b = 0; b < F::kAcc; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 4); }
@@ -122,9 +132,9 @@ __global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
     mbar_init(&inbox, 1);
     mbar_fence_init();
     s_abort = 0;
-    // (others' sums of this CTA's columns that there are tokens for)
+    // (others' sums of this CTA's columns, fours or twos with a token)
     if (S > 1)
-      mbar_arrive_expect_tx(&inbox, static_cast<uint32_t>(max(min(min(NT, a.M - m0) - rank * width, width), 0) * (S - 1)) * 512u);
+      mbar_arrive_expect_tx(&inbox, static_cast<uint32_t>((max(min(a.M - m0 - rank * width, width), 0) + vec - 1) / vec * (S - 1) * vec) * 512u);
     tensormap_prefetch(&mapW);
     tensormap_prefetch(&mapX);
     for (int i = 0; i < min(nkb, stages); ++i) tma_prefetch_2d(&mapW, (kb0 + i) * kBlock, n0);
@@ -139,7 +149,7 @@ __global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
   // (after the allocation: a CTA of the next kernel that got its columns first would wait for
   // this one, and this one for those columns)
   pdl_launch_dependents();
-  if (S > 1) cluster_arrive();
+  if (S > 1) cluster_arrive_relaxed();
   pdl_wait();
   const uint32_t tbase = tmem_base_s;
 
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
     const int q = warp & 3;
     const int row = 32 * q + lane;      // weight row of the tile = TMEM lane
     const int etid = threadIdx.x - 64;  // 0..127
-    constexpr int kPer = NT * F::kChunk / 128, kStep = NT == 32 || NT == 64 ? 32 : 16;
+    constexpr int kPer = NT * F::kChunk / 128, kStep = NT == 16 ? 16 : 32;
     float acc[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
@@ -269,73 +279,90 @@ __global__ void __launch_bounds__(192, NT == 128 ? 1 : 2)
           if (m0 + c < a.M) store_out(a.out, static_cast<size_t>((m0 + c) * a.out_stride + n), acc[c], a.out_dtype);
       }
     } else {
-      // into the ring, which nothing fills or reads any more (every product was waited for)
-      float* own = reinterpret_cast<float*>(smem);
-#pragma unroll
-      for (int c = 0; c < NT; ++c) own[c * 128 + row] = acc[c];
-      fence_async();
-      named_bar_sync(1, 128);
       cluster_wait();  // every CTA of the cluster runs
-      const int cols = min(NT, a.M - m0);  // with tokens
-      if (etid < S && etid != rank && !s_abort) {
-        const int many = min(cols - etid * width, width);
-        if (many > 0)
-          bulk_to_peer(peer_addr(smem_u32(parts + rank * width * 128), etid), own + etid * width * 128, many * 512u,
-                       peer_addr(smem_u32(&inbox), etid));
+      // sums as [CTA that has them][fours or twos of columns][row] in the CTA whose columns they are
+      const uint32_t bar = smem_u32(&inbox);
+      const uint32_t mine = smem_u32(parts) + static_cast<uint32_t>((rank * width * 128 + row * vec) * 4);
+#pragma unroll
+      for (int c = 0; c < NT; c += kMinVec) {
+        if (m0 + c >= a.M) break;
+        const int to = c / width;
+        const uint32_t at = mine + static_cast<uint32_t>((c - to * width) * 512);
+        float* here = parts + (rank * width + c - to * width) * 128 + row * vec;
+        if (kMinVec == 2 && vec == 2) {
+          if (to == rank) *reinterpret_cast<float2*>(here) = make_float2(acc[c], acc[c + 1]);
+          else if (!s_abort) send8(peer_addr(at, to), acc[c], acc[c + 1], peer_addr(bar, to));
+        } else if (c % 4 == 0) {
+          if (to == rank) *reinterpret_cast<float4*>(here) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+          else if (!s_abort) send16(peer_addr(at, to), acc[c], acc[c + 1], acc[c + 2], acc[c + 3], peer_addr(bar, to));
+        }
       }
       const bool here = tc_wait_polled(&inbox, 0, timeout, &s_abort);
-      if (!here) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
-      const int c0 = rank * width, many = here && n < a.N ? min(cols - c0, width) : 0;
-      for (int j0 = 0; j0 < many; j0 += 8) {  // 8 columns at a time: a load's latency per part, not per value
-        float sum[8] = {};
+      if (!here) {
+        s_abort = 1;
+        report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+      }
+      const int c0 = m0 + rank * width, many = here && n < a.N ? min(a.M - c0, width) : 0;
+      const auto write = [&](int j, float v) {
+        if (j < many) store_out(a.out, static_cast<size_t>((c0 + j) * a.out_stride + n), v, a.out_dtype);
+      };
+      if (kMinVec == 2 && vec == 2) {
+        float2 sum = make_float2(0.0f, 0.0f);
         for (int r = 0; r < S; ++r) {
-          const float* from = (r == rank ? own + c0 * 128 : parts + r * width * 128) + j0 * 128 + row;
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = j0 + j < many ? from[j * 128] : 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+          const float2 v = reinterpret_cast<const float2*>(parts)[r * 128 + row];
+          sum.x += v.x, sum.y += v.y;
         }
+        write(0, sum.x), write(1, sum.y);
+      } else {
+        for (int j = 0; j < many; j += 4) {
+          const float4* from = reinterpret_cast<const float4*>(parts) + j / 4 * 128 + row;
+          float4 sum = from[0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j0 + j < many)
-            store_out(a.out, static_cast<size_t>((m0 + c0 + j0 + j) * a.out_stride + n), sum[j], a.out_dtype);
+          for (int r = 1; r < 8; ++r)
+            if (r < S) {
+              const float4 v = from[r * (width / 4) * 128];
+              sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+          write(j, sum.x), write(j + 1, sum.y), write(j + 2, sum.z), write(j + 3, sum.w);
+        }
       }
     }
   }
-  if (S > 1) {
-    if (warp < 2) cluster_wait();
-    cluster_arrive();  // this CTA's copies have arrived, and it is not left before those it sent have
-    cluster_wait();
-  }
+  if (S > 1 && warp < 2) cluster_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, F::kCols);
   }
+  // A CTA that gave up is not left before the others have: what they sent may be on its way.
+  if (S > 1 && s_abort) {
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // =========================================================== many rows
-// Tiles of 256 tokens by 128 weight rows, each of a pair of CTAs: the tokens are the
-// MMA's M (128 per CTA), the weight rows its N, and each CTA stages half of both (24 KB
-// a block), so that a pair reads every byte once.  Four accumulators of 128 columns fill
-// the tensor memory: what a block costs is the way from its product to the epilogue and
-// back (two of 256 columns: 204 us for 8192 x 5120 x 4096).  The sums of a token's 128
-// columns are in 2 threads' registers, 64 each.
+// Tiles of 256 tokens by N weight rows, each of a pair of CTAs: the tokens are the
+// MMA's M (128 per CTA), the weight rows its N, and each CTA stages half of both, so that
+// a pair reads every byte once.  Accumulators fill the tensor memory.  A row's sums of a
+// tile are in N / 64 threads' registers, 64 each.
+template <int N>
 struct Many {
-  static constexpr int kN = 128;
-  static constexpr uint32_t kStage = kTile + kN / 2 * kBlock;
-  static constexpr int kStages = 7;
-  static constexpr int kAcc = 4;
-  // Threads that issue MMAs, block by block in turn: what one does for a block (two waits, four
-  // MMAs, two commits) takes it about 1000 cycles, a block's MMAs 256 (one: 272 us, two: XXX).
+  static constexpr uint32_t kStage = kTile + N / 2 * kBlock;
+  static constexpr int kStages = N == 256 ? 5 : 7;
+  static constexpr int kAcc = 512 / N;
+  // Warps that issue MMAs, block by block in turn: what one does for a block (two waits, four
+  // MMAs, two commits) takes longer than the block's MMAs (N = 128: 272 us with one warp, 202
+  // with two, for 8192 x 5120 x 4096).
   static constexpr int kIssuers = 2;
-  static constexpr int kWarps = 8;  // of the epilogue
+  static constexpr int kWarps = N / 16;  // of the epilogue
   static constexpr int kThreads = 128 + 32 * kWarps;
-  static constexpr int kChunk = 16;                   // blocks whose scales are staged at a time,
-  static constexpr int kScales = kChunk * 128 + kChunk;  // floats: the rows' and the weight block's
-  static constexpr uint32_t kTurn = 32 * 64;          // bytes a warp turns its results in
+  static constexpr int kLoad = N == 256 ? 16 : 32;       // columns of a load from tensor memory, and
+  static constexpr int kLoads = N == 256 ? 1 : 2;        // loads in flight: what registers allow
+  static constexpr int kChunk = 16;                      // blocks whose scales are staged at a time,
+  static constexpr int kScales = kChunk * (128 + N / 128);  // floats: the rows' and the weight blocks'
+  static constexpr uint32_t kTurn = 32 * 64;             // bytes a warp turns its results in
   static constexpr size_t kSmem = kStages * kStage + 2 * kScales * 4 + kWarps * kTurn + 1024;
 };
 
@@ -419,10 +446,11 @@ __device__ __forceinline__ void many_store(const moe_linear_t& a, const float (&
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
+template <int N>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
                        moe_linear_t a, int KB, int mtiles, int tiles, int wide, Control* ctrl, uint64_t timeout) {
-  using G = Many;
+  using G = Many<N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], tfull[G::kAcc], tempty[G::kAcc], sfull[2], sempty[2],
@@ -457,13 +485,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
   const uint32_t tbase = tmem_base_s;
+  // (N = 256: 640 threads of 96 registers at launch, 128 * 56 + 512 * 104 then)
+  if constexpr (N == 256)
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 
   if (warp == 0) {
     if (lane == 0) {  // ---------------------------------------------- TMA producer
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
       for (int t = first; t < tiles && !s_abort; t += step) {
-        const int m0 = t % mtiles * 256 + rank * 128, n0 = t / mtiles * G::kN + rank * (G::kN / 2);
+        const int m0 = t % mtiles * 256 + rank * 128, n0 = t / mtiles * N + rank * (N / 2);
         for (int kb = 0; kb < KB; ++kb) {
           if (!tc_wait_polled(&empty[stage], phase ^ 1u, timeout, &s_abort)) {
             s_abort = 1;
@@ -490,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
     if (rank == 0) {  // ---------------------------------------------- MMA issuers
       // (the whole warp goes through the loop and one thread of it issues: with the others gone, an
       // MMA's descriptors are moved to the uniform registers it takes them from one by one)
-      constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(G::kN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
+      constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
       const int blocks = first < tiles ? ((tiles - 1 - first) / step + 1) * KB : 0;
       const uint64_t adesc = sw128_desc(smem_u32(smem)), bdesc = sw128_desc(smem_u32(smem) + kTile);
       int stage = warp - 1, b = warp - 1;
@@ -507,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_e4m3_pair(tbase + static_cast<uint32_t>(b * G::kN), adesc + at + 2 * k, bdesc + at + 2 * k, idesc, k != 0);
+            mma_e4m3_pair(tbase + static_cast<uint32_t>(b * N), adesc + at + 2 * k, bdesc + at + 2 * k, idesc, k != 0);
           tc_commit_pair(&empty[stage]);
           tc_commit_pair(&tfull[b]);
         }
@@ -534,13 +565,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
-      const int m0 = t % mtiles * 256 + rank * 128, nb = t / mtiles;
+      const int m0 = t % mtiles * 256 + rank * 128, nb = t / mtiles * (N / 128);
       for (int kb0 = 0; kb0 < KB; kb0 += G::kChunk) {
         ok = __all_sync(0xffffffffu, tc_wait_polled(&sempty[buf], phase ^ 1u, timeout, &s_abort));
         if (!ok) break;
         float* sc = scales + buf * G::kScales;
-        if (lane < G::kChunk && kb0 + lane < KB)
-          sc[G::kChunk * 128 + lane] = a.w_scales[static_cast<int64_t>(nb) * KB + kb0 + lane];
+        if (lane % G::kChunk + kb0 < KB && lane < N / 128 * G::kChunk)  // (past the last weight block: any)
+          sc[G::kChunk * 128 + lane] =
+              a.w_scales[static_cast<int64_t>(min(nb + lane / G::kChunk, (a.N - 1) / 128)) * KB + kb0 + lane % G::kChunk];
 #pragma unroll 1
         for (int r = lane; r < 128; r += 32) {
           const float* from = a.x_scales + static_cast<int64_t>(min(m0 + r, a.M - 1)) * KB + kb0;
@@ -560,7 +592,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
       if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
     }
   } else {  // ------------------------------------------------------- epilogue
-    const int q = warp & 3, g = (warp - 4) >> 2;  // quarter of the TMEM lanes, half of the columns
+    if constexpr (N == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int q = warp & 3, g = (warp - 4) >> 2;  // quarter of the TMEM lanes, 64 of the columns
     const uint32_t lane0 = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(64 * g);
     const uint32_t free_bar = peer_addr(smem_u32(&tempty[0]), 0);
     float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage);
@@ -576,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
         // (a wait that ran out leaves the loops running without it, so that all warps end together)
         if (in == 0) ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&sfull[buf], sphase, timeout, &s_abort));
         const float* sc = scales + buf * G::kScales;
-        const float s = sc[in * 128 + 32 * q + lane] * sc[G::kChunk * 128 + in];
+        const float s = sc[in * 128 + 32 * q + lane] * sc[G::kChunk * (128 + (g >> 1)) + in];
         if (++in == G::kChunk || kb + 1 == KB) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sempty[buf]);
@@ -590,21 +623,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many::kThreads, 1)
           continue;
         }
         tc_fence_after();
-        uint32_t v[2][32];
-        tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * G::kN), v[0]);
-        tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * G::kN + 32), v[1]);
-        tmem_ld_wait();
-        tmem_ld_tie(v[0]);
-        tmem_ld_tie(v[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
 #pragma unroll
-        for (int j = 0; j < 64; ++j) acc[j] = fmaf(__uint_as_float(v[j / 32][j % 32]), s, acc[j]);
+        for (int c = 0; c < 64; c += G::kLoad * G::kLoads) {
+          uint32_t v[G::kLoads][G::kLoad];
+#pragma unroll
+          for (int u = 0; u < G::kLoads; ++u) {
+            const uint32_t ta = lane0 + static_cast<uint32_t>(b * N + c + u * G::kLoad);
+            if constexpr (G::kLoad == 32) tmem_ld32_issue(ta, v[u]);
+            else tmem_ld16_issue(ta, v[u]);
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < G::kLoads; ++u) tmem_ld_tie(v[u]);
+          if (c + G::kLoad * G::kLoads == 64) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
+          }
+#pragma unroll
+          for (int j = 0; j < G::kLoad * G::kLoads; ++j)
+            acc[c + j] = fmaf(__uint_as_float(v[j / G::kLoad][j % G::kLoad]), s, acc[c + j]);
+        }
         if (++b == G::kAcc) { b = 0; bphase ^= 1u; }
       }
       if (!ok) continue;
-      const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * G::kN + 64 * g;
+      const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * N + 64 * g;
       if (m0 >= a.M || n0 >= a.N) continue;
       if (a.out_dtype == MOE_F32) many_store<4>(a, acc, turn, m0, n0, lane, wide);
       else many_store<2>(a, acc, turn, m0, n0, lane, wide);
@@ -641,8 +684,9 @@ template <int NT>
 moe_status_t launch_few(const moe_linear_t& l, int KB, Control* ctrl, cudaStream_t st) {
   const int mtiles = (l.M - 1) / NT + 1;
   const int64_t tiles = static_cast<int64_t>(mtiles) * ((l.N - 1) / 128 + 1);
-  const int S = static_cast<int>(tiles >= sm_count() ? 1 : std::min<int64_t>({4, (KB + 1) / 2, sm_count() / tiles}));
-  const int nkb = (KB + S - 1) / S, stages = std::min(Few<NT>::kMaxStages, std::max(nkb, 2));
+  int S = 1;
+  while (S < 8 && tiles * S <= sm_count() && KB >= 4 * S) S *= 2;
+  const int nkb = (KB + S - 1) / S, stages = Few<NT>::stages(nkb, S);
   CUtensorMap mw, mx;
   if (!byte_map(&mw, l.w, l.K, l.N, l.w_stride, 128) || !byte_map(&mx, l.x, l.K, l.M, l.x_stride, NT))
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
@@ -666,18 +710,20 @@ moe_status_t launch_few(const moe_linear_t& l, int KB, Control* ctrl, cudaStream
   return MOE_OK;
 }
 
+template <int N>
 moe_status_t launch_many(const moe_linear_t& l, int KB, Control* ctrl, cudaStream_t st) {
   const int mtiles = (l.M - 1) / 256 + 1;
-  const int tiles = mtiles * ((l.N - 1) / Many::kN + 1);
+  const int tiles = mtiles * ((l.N - 1) / N + 1);
   CUtensorMap mx, mw;
-  if (!byte_map(&mx, l.x, l.K, l.M, l.x_stride, 128) || !byte_map(&mw, l.w, l.K, l.N, l.w_stride, Many::kN / 2))
+  if (!byte_map(&mx, l.x, l.K, l.M, l.x_stride, 128) || !byte_map(&mw, l.w, l.K, l.N, l.w_stride, N / 2))
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
-  if (raise_smem_limit(linear_many_kernel, Many::kSmem) != cudaSuccess) return check_launch("linear_many_kernel (smem)");
+  if (raise_smem_limit(linear_many_kernel<N>, Many<N>::kSmem) != cudaSuccess)
+    return check_launch("linear_many_kernel (smem)");
   const int per = l.out_dtype == MOE_F32 ? 4 : 8;
   const int wide = (reinterpret_cast<uintptr_t>(l.out) & 15u) == 0 && l.out_stride % per == 0;
   const int pairs = sm_count() / 2;
-  if (launch_pdl(linear_many_kernel, dim3(2 * (tiles < pairs ? tiles : pairs)), dim3(Many::kThreads), Many::kSmem, st, mx,
-                 mw, l, KB, mtiles, tiles, wide, ctrl, wait_timeout_ns()) != cudaSuccess)
+  if (launch_pdl(linear_many_kernel<N>, dim3(2 * (tiles < pairs ? tiles : pairs)), dim3(Many<N>::kThreads), Many<N>::kSmem,
+                 st, mx, mw, l, KB, mtiles, tiles, wide, ctrl, wait_timeout_ns()) != cudaSuccess)
     return check_launch("linear_many_kernel");
   stat_kernels(1);
   return MOE_OK;
@@ -727,9 +773,15 @@ extern "C" moe_status_t moe_linear_e4m3(const moe_linear_t* l, void* ws, size_t 
     return set_error(MOE_ERR_INVALID_ARG, "out must not overlap the other tensors");
   Control* ctrl = static_cast<Control*>(ws);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Few rows, or so few tiles of many that most pairs of SMs would have none (256 x 2048 x 4096,
+  // 16 tiles for 76 pairs: 14.7 us, 10.5 by tiles of 64 rows and parts of K).
+  const int64_t pairs = sm_count() / 2, m256 = (a.M - 1) / 256 + 1;
   if (a.M <= 16) return launch_few<16>(a, KB, ctrl, st);
   if (a.M <= 32) return launch_few<32>(a, KB, ctrl, st);
-  if (a.M <= 64) return launch_few<64>(a, KB, ctrl, st);
-  if (a.M <= kFewRows) return launch_few<128>(a, KB, ctrl, st);
-  return launch_many(a, KB, ctrl, st);
+  if (a.M <= 128 || m256 * nb * 4 <= pairs) return launch_few<64>(a, KB, ctrl, st);
+  // Wider tiles take a block in 0.52 us, where two narrower take 0.69: 8192 x 5120 x 4096 151 us
+  // against 188, but 256 x 5120 x 2048, 20 tiles or 40 for 76 pairs, 13.6 against 11.0.
+  const auto rounds = [&](int n) { return (m256 * ((a.N - 1) / n + 1) + pairs - 1) / pairs; };
+  if (3 * rounds(256) <= 2 * rounds(128)) return launch_many<256>(a, KB, ctrl, st);
+  return launch_many<128>(a, KB, ctrl, st);
 }
