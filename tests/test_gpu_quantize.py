@@ -51,7 +51,8 @@ def test_values_and_scales(m, T, H, rows, dtype):
 
 
 @pytest.mark.parametrize("rows", [1, 128])
-@pytest.mark.parametrize("H,pad,off", [(256, 8, 8), (256, 3, 0), (256, 8, 3), (131, 5, 1), (1000, 24, 16)])
+@pytest.mark.parametrize("H,pad,off", [(256, 8, 8), (256, 3, 0), (256, 8, 3), (131, 5, 1), (1000, 24, 16), (9, 0, 1),
+                                       (127, 1, 0), (133, 3, 0), (134, 2, 8), (135, 1, 2), (250, 6, 5), (255, 4, 7)])
 def test_strides_offsets_and_nothing_beside(m, H, pad, off, rows):
     g = torch.Generator().manual_seed(H + pad)
     T = 133
