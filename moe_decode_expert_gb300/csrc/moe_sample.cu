@@ -402,7 +402,8 @@ struct Row {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * threadIdx.x + j;
-        w[j] = c[j] * ((static_cast<uint64_t>(sh.root[31 - (i & 31)].x) << 13) >> min(i >> 5, 63));
+        // (rounded up: what lies behind the end is not to be taken for less than it is)
+        w[j] = c[j] * (((static_cast<uint64_t>(sh.root[31 - (i & 31)].x) << 13) >> min(i >> 5, 63)) + 1);
         count += c[j];
         mass += w[j];
       }
@@ -567,15 +568,22 @@ struct Row {
     }
     __syncthreads();
   }
-  // Brings the tokens that are not below `least`.
-  __device__ __forceinline__ int gather(float least) {
+  // Brings the tokens that are not below `least`; with SUM, the sum of all weights into `sum`.
+  template <bool SUM>
+  __device__ __forceinline__ int gather(float least, uint64_t& sum) {
     begin_list();
+    uint64_t all = 0;
     chunks_of([&](const float (&v)[kVec], int i) {
       float m = v[0];
 #pragma unroll
       for (int j = 1; j < kVec; ++j) m = fmaxf(m, v[j]);
+      if constexpr (SUM) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) all = wt.add(all, v[j], sh.root);
+      }
       if (m >= least) bring_some(v, i, least, INFINITY);
     });
+    if constexpr (SUM) sum = total(all);
     return end_list();
   }
 
@@ -706,18 +714,28 @@ __device__ __forceinline__ void finish_list(const Row<DT, HELD>& r, const Asked&
       }
     before = add8(before);
     const int rank = static_cast<int>(add8(ahead));
-    if (ask.k) r.scan(in && part == 0 && rank < k ? w : 0ull, &sum);
+    if (ask.k) {  // the sum of the first k: every eight threads add it up for themselves
+      if (in && part == 0) r.hist[t] = static_cast<uint32_t>(rank);
+      __syncthreads();
+      sum = 0;
+      for (int j = part; j < m; j += 8)
+        if (static_cast<int>(r.hist[j]) < k) sum += spare[j];
+      sum = add8(sum);
+    }
     const bool stays = in && rank < k && before < ask.needed(sum) && (w >= ask.w_min || rank == 0);
     __syncthreads();
     if (in && part == 0) spare[t] = stays ? w : 0ull;
-    uint64_t whole;
-    r.scan(stays && part == 0 ? w : 0ull, &whole);  // (also: spare is written)
-    const uint64_t target = times_fraction(whole, ask.u);
+    __syncthreads();
     const uint32_t at = static_cast<uint32_t>(key);  // ~index
+    uint64_t whole = 0;
     before = 0;
-    for (int j = part; j < m; j += 8)
+    for (int j = part; j < m; j += 8) {
+      whole += spare[j];
       if (static_cast<uint32_t>(keys[j]) > at) before += spare[j];
+    }
+    whole = add8(whole);
     before = add8(before);
+    const uint64_t target = times_fraction(whole, ask.u);
     if (stays && part == 0 && target >= before && target < before + w) {
       *token = static_cast<int>(~at);
       if (logprob) *logprob = log_share(wt, v, w, whole);
@@ -966,13 +984,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
     int m = -1, b0, b1;
     uint64_t sum = 0, tokens;
     uint32_t klo, khi;
-    if (few) m = r.gather(reach > 0x007fffffu ? value_of_order(reach) : kNegInf);
+    if (few) {
+      m = r.template gather<false>(reach > 0x007fffffu ? value_of_order(reach) : kNegInf, sum);
+    } else if (a.V <= kList / C) {  // all that have weight
+      r.key_range(0, kUsedBins - 1, klo, khi);
+      m = by_p && !by_k ? r.template gather<true>(value_of_order(klo), sum) : r.template gather<false>(value_of_order(klo), sum);
+    }
     if (m < 0) {
       r.template find_bins<true>(any, by_k, k, ask.top_p, b0, b1, tokens);
       if (tokens <= kList) {
-        if (!by_k) sum = r.sum([&](float v, int) { return r.weight(v); });
         r.key_range(b0, min(b1, kUsedBins - 1), klo, khi);  // (tokens without weight are not wanted)
-        m = r.gather(value_of_order(klo));
+        m = by_k ? r.template gather<false>(value_of_order(klo), sum) : r.template gather<true>(value_of_order(klo), sum);
       }
     }
     if (m >= 0) {  // the first CTA does the rest
