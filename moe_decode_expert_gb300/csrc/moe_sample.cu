@@ -106,8 +106,8 @@ struct Weights {
     const float s = fmaxf((l - base) * hi, -2097152.0f) + 12582912.0f;
     return 32 * top + 31 - (__float_as_int(s) - 0x4b400000);
   }
-  // sum + the weight of l
-  __device__ __forceinline__ uint64_t add(uint64_t sum, float l, const uint2* root) const {
+  // The weight of l is m * f.
+  __device__ __forceinline__ void parts(float l, const uint2* root, uint32_t& m, uint32_t& f) const {
     float e;
     const int n = split(l, e);
     // 2^(e / 32) - 1, |e| <= 0.51: terms of (ln 2 / 32)^i / i!
@@ -115,10 +115,16 @@ struct Weights {
         e * fmaf(e, fmaf(e, fmaf(e, 9.1725e-9f, 1.69386395e-6f), 2.34607166e-4f), 2.16608494e-2f);
     const uint2 r = root[n & 31];
     const uint32_t mant = r.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(r.y) * p));
-    // mant * 2^(13 - down): the shift right on 32 bits, the shift left in the product
+    // mant * 2^(13 - down): a shift right on 32 bits, or a factor
     const int t = top - (n >> 5) - 13;
-    const uint32_t m = __funnelshift_rc(mant, 0u, max(t, 0));  // (0 from 32 on: weights below 2^-44)
-    return sum + static_cast<uint64_t>(m) * (1u << max(-t, 0));
+    m = __funnelshift_rc(mant, 0u, max(t, 0));  // (0 from 32 on: weights below 2^-44)
+    f = 1u << max(-t, 0);
+  }
+  // sum + the weight of l
+  __device__ __forceinline__ uint64_t add(uint64_t sum, float l, const uint2* root) const {
+    uint32_t m, f;
+    parts(l, root, m, f);
+    return sum + static_cast<uint64_t>(m) * f;
   }
   __device__ __forceinline__ uint64_t of(float l, const uint2* root) const { return add(0, l, root); }
 };
@@ -393,9 +399,16 @@ struct Row {
       uint32_t c[4] = {};
       if (threadIdx.x < kBins / 4) {
         uint4 h = reinterpret_cast<const uint4*>(hist)[threadIdx.x];
-        for (int r = 1; r < C; ++r) {
-          const uint4 o = ld_peer128(hist + 4 * threadIdx.x, r);
-          h.x += o.x, h.y += o.y, h.z += o.z, h.w += o.w;
+#pragma unroll
+        for (int r0 = 1; r0 < kMaxCtas; r0 += 4) {  // several on their way: one takes most of a microsecond
+          uint4 o[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            o[u] = make_uint4(0, 0, 0, 0);
+            if (r0 + u < C) o[u] = ld_peer128(hist + 4 * threadIdx.x, r0 + u);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) h.x += o[u].x, h.y += o[u].y, h.z += o[u].z, h.w += o[u].w;
         }
         c[0] = h.x, c[1] = h.y, c[2] = h.z, c[3] = h.w;
       }
@@ -410,21 +423,26 @@ struct Row {
       uint64_t all;
       uint64_t n = scan(count);
       uint64_t m = scan(mass, &all);
-      // a token's weight is within 2^(1 / 64) of its bin's: two sums' ratio within 2^(1 / 32)
-      const auto reached = [&](uint64_t n, uint64_t m, float room) {
-        return by_k ? n >= k : static_cast<float>(m) * room * (1.0f - p) >= static_cast<float>(all - m) * p;
-      };
+      // the share p is reached where m (1 - p) >= (all - m) p: where at most this lies behind; a
+      // token's weight is within 2^(1 / 64) of its bin's, so two sums' ratio within 2^(1 / 32)
+      uint64_t behind[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const float room = (j == 0 ? 1.025f : j == 1 ? 1.0f : 0.975f) * (1.0f - p);
+        behind[j] = by_k ? 0 : times_fraction(all, fminf(__fdividef(room, room + p), 0.99999994f));
+      }
+      const auto reached = [&](uint64_t n, uint64_t m, int j) { return by_k ? n >= k : all - m <= behind[j]; };
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint64_t n1 = n + c[j], m1 = m + w[j];
         const bool none = n == 0;  // (the share 0 of nothing is not reached)
         if (c[j]) {
-          if ((none || !reached(n, m, 1.025f)) && reached(n1, m1, 1.025f)) {
+          if ((none || !reached(n, m, 0)) && reached(n1, m1, 0)) {
             sh.finds[0] = 4 * threadIdx.x + j;
             sh.finds[3] = n;
           }
-          if ((none || !reached(n, m, 1.0f)) && reached(n1, m1, 1.0f)) sh.middle = 4 * threadIdx.x + j;
-          if ((none || !reached(n, m, 0.975f)) && reached(n1, m1, 0.975f)) {
+          if ((none || !reached(n, m, 1)) && reached(n1, m1, 1)) sh.middle = 4 * threadIdx.x + j;
+          if ((none || !reached(n, m, 2)) && reached(n1, m1, 2)) {
             sh.finds[1] = 4 * threadIdx.x + j;
             sh.finds[2] = n1;
           }
@@ -433,8 +451,8 @@ struct Row {
         m = m1;
       }
       if (threadIdx.x == kThreads - 1) {
-        if (!reached(n, m, 1.025f)) sh.finds[0] = kUsedBins;
-        if (!reached(n, m, 0.975f)) {
+        if (!reached(n, m, 0)) sh.finds[0] = kUsedBins;
+        if (!reached(n, m, 2)) {
           sh.finds[1] = kUsedBins;
           sh.finds[2] = n;
         }
@@ -491,9 +509,18 @@ struct Row {
       if (rank == 0) {
         const int t = threadIdx.x;  // kThreads = kSub
         uint64_t v = 0, all;
-        for (int r = 0; r < C; ++r)
-          v += ld_peer32(hist + t, r) + (static_cast<uint64_t>(ld_peer32(hist + kSub + t, r)) << 15) +
-               (static_cast<uint64_t>(ld_peer32(hist + 2 * kSub + t, r)) << 30);
+#pragma unroll
+        for (int r0 = 0; r0 < kMaxCtas; r0 += 4) {
+          uint32_t o[4][3] = {};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              if (r0 + u < C) o[u][j] = ld_peer32(hist + j * kSub + t, r0 + u);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            v += o[u][0] + (static_cast<uint64_t>(o[u][1]) << 15) + (static_cast<uint64_t>(o[u][2]) << 30);
+        }
         const uint64_t at = above + scan(v, &all);
         if (at < need && at + v >= need) {
           sh.finds[0] = t;
@@ -527,10 +554,10 @@ struct Row {
   }
 
   // --------------------------------------------------------- lists of tokens
-  // A token to the first CTA's list, of which every CTA has a share.
+  // A token to this CTA's part of a list.
   __device__ __forceinline__ void bring(float v, int i) const {
-    const int share = kList / C, at = static_cast<int>(atomicAdd(&sh.listed, 1u));
-    if (at < share) st_peer64(list + rank * share + at, 0, key_of(v, first + i));
+    const int at = static_cast<int>(atomicAdd(&sh.listed, 1u));
+    if (at < kList) list2[at] = key_of(v, first + i);
   }
   // Those of a chunk that lie between two values, and of the value `tie` only the slots up to `last`.
   __device__ __forceinline__ void bring_some(const float (&v)[kVec], int i, float v_lo, float v_hi,
@@ -544,28 +571,27 @@ struct Row {
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
   }
-  // How many tokens are in the list, or -1 if a CTA had more than its share; known to all.
+  // The parts together, in the first CTA's list; how many tokens there are, or -1 for more than
+  // kList, known to all.
   __device__ __forceinline__ int end_list() {
     __syncthreads();
+    const int mine = static_cast<int>(sh.listed);
     turn ^= 1;
-    if (static_cast<int>(threadIdx.x) < C) st_peer64(&sh.cta[turn][rank], threadIdx.x, sh.listed);
+    if (static_cast<int>(threadIdx.x) < C) st_peer64(&sh.cta[turn][rank], threadIdx.x, static_cast<uint64_t>(mine));
     sync_row();
-    int sum = 0;
-    bool fits = true;
+    uint64_t before = 0, sum = 0;
     for (int r = 0; r < C; ++r) {
-      sum += static_cast<int>(sh.cta[turn][r]);
-      fits &= sh.cta[turn][r] <= static_cast<uint64_t>(kList / C);
+      if (r < rank) before += sh.cta[turn][r];
+      sum += sh.cta[turn][r];
     }
-    return fits ? sum : -1;
+    if (sum > kList) return -1;
+    for (int i = threadIdx.x; i < mine; i += kThreads) st_peer64(list + before + i, 0, list2[i]);
+    sync_row();
+    return static_cast<int>(sum);
   }
-  // The first CTA, after end_list(): the shares together, into list2.
-  __device__ __forceinline__ void close_list() const {
-    int at = 0;
-    for (int c = 0; c < C; ++c) {
-      const int many = static_cast<int>(sh.cta[turn][c]);
-      for (int i = threadIdx.x; i < many; i += kThreads) list2[at + i] = list[c * (kList / C) + i];
-      at += many;
-    }
+  // The first CTA, after end_list(): into list2, which sort() takes.
+  __device__ __forceinline__ void close_list(int m) const {
+    for (int i = threadIdx.x; i < m; i += kThreads) list2[i] = list[i];
     __syncthreads();
   }
   // Brings the tokens that are not below `least`; with SUM, the sum of all weights into `sum`.
@@ -986,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
     uint32_t klo, khi;
     if (few) {
       m = r.template gather<false>(reach > 0x007fffffu ? value_of_order(reach) : kNegInf, sum);
-    } else if (a.V <= kList / C) {  // all that have weight
+    } else if (a.V <= kList) {  // all that have weight
       r.key_range(0, kUsedBins - 1, klo, khi);
       m = by_p && !by_k ? r.template gather<true>(value_of_order(klo), sum) : r.template gather<false>(value_of_order(klo), sum);
     }
@@ -999,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
     }
     if (m >= 0) {  // the first CTA does the rest
       if (rank != 0) return;
-      r.close_list();
+      r.close_list(m);
       finish_list<DT, HELD>(r, ask, m, sum, token, logprob);
       return;
     }
@@ -1023,9 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
       if (m >= 0) {
         r.turn ^= 1;
         if (rank == 0) {
-          r.turn ^= 1;
-          r.close_list();
-          r.turn ^= 1;
+          r.close_list(m);
           r.sort(m);
           if (threadIdx.x == 0) {
             const uint64_t at = static_cast<uint64_t>(k) - above - 1;  // (past the end: wraps, is not below m)
@@ -1051,9 +1075,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
           bool near = false;
 #pragma unroll
           for (int j = 0; j < R::kVec; ++j) {
-            const uint64_t w = r.weight(v[j]);
-            low += w;
-            if (v[j] > v_hi) high += w;
+            uint32_t m, f;
+            r.wt.parts(v[j], sh.root, m, f);
+            low += static_cast<uint64_t>(m) * f;
+            high += static_cast<uint64_t>(v[j] > v_hi ? m : 0u) * f;
             near |= v[j] >= v_lo && v[j] <= v_hi;
           }
           if (near) r.bring_some(v, i, v_lo, v_hi);
@@ -1064,9 +1089,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
 #pragma unroll
           for (int j = 0; j < R::kVec; ++j) {
             const bool in = v[j] > v_cut || (v[j] == v_cut && i + j <= i_cut);
-            const uint64_t w = r.weight(v[j]) & (in ? ~0ull : 0ull);
-            low += w;
-            if (v[j] > v_hi) high += w;
+            uint32_t m, f;
+            r.wt.parts(v[j], sh.root, m, f);
+            low += static_cast<uint64_t>(in ? m : 0u) * f;
+            high += static_cast<uint64_t>(v[j] > v_hi ? m : 0u) * f;  // (above the window all stay)
             near |= in && v[j] >= v_lo && v[j] <= v_hi;
           }
           if (near) r.bring_some(v, i, fmaxf(v_lo, v_cut), v_hi, v_cut, i_cut);
@@ -1081,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
       if (m >= 0) {
         uint64_t* said = sh.said[r.turn ^ 1];
         if (rank == 0) {
-          r.close_list();
+          r.close_list(m);
           r.sort(m);
           uint64_t w[kPer], here = 0, all, keep = 0;
 #pragma unroll
@@ -1144,7 +1170,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
   }
 
   // --------------------------------------------------------------- the draw
-  const uint64_t all = r.sum(kept);
+  uint64_t all = 0;
+  if (cut != 0) {
+    r.each([&](float v, int i) { all += kept(v, i); });
+  } else if (ask.w_min != 0) {
+    r.each([&](float v, int) {
+      const uint64_t w = r.weight(v);
+      all += w >= ask.w_min ? w : 0ull;
+    });
+  } else {
+    r.each([&](float v, int) { all = r.wt.add(all, v, sh.root); });
+  }
+  all = r.total(all);
   r.locate(kept, times_fraction(all, ask.u), [&](float v, int i) { write(v, i, all); });
 }
 
