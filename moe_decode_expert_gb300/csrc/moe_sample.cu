@@ -183,6 +183,7 @@ struct Shared {
   uint2 root[32];                      // 2^(j / 32) in units of 2^-31, whole and in fp32
   uint32_t listed;                     // tokens this CTA brought
   int middle;
+  float place[2];
 };
 
 __device__ __forceinline__ float value_of_key(uint64_t key) {
@@ -381,11 +382,23 @@ struct Row {
     __syncthreads();
   }
 
-  // Counts the tokens that `stays` in their bins, and finds the first and last bin in which, by
-  // those counts, the ranking's first k tokens, or the share p of the weight, may end (kUsedBins:
-  // behind the last), and how many tokens lie down to the last.
+  // The key of the value n / 32 octaves of weight up from weight 1, with some room to either side.
+  __device__ __forceinline__ uint32_t key_at(float n, float room) const {
+    if (wt.infinite || n == INFINITY) return order_key(INFINITY);
+    if (n == -INFINITY) return order_key(kNegInf);
+    const float x = n / wt.hi, v = wt.base + x;
+    return order_key(fmaf(fabsf(wt.base) + fabsf(x), room, v + room * 1e-30f));
+  }
+  // The least value that a token with some weight, down to bin b, has.
+  __device__ __forceinline__ float least_of(int b) const {
+    return value_of_order(key_at(static_cast<float>(32 * wt.top + 31 - min(b, kUsedBins - 1)) - 0.5f, -0x1p-20f));
+  }
+
+  // Counts the tokens that `stays` in their bins, and finds by those counts a window of keys in which
+  // the ranking's first k tokens, or the share p of the weight, should end; the last bin where they
+  // may (kUsedBins: behind the last), and how many tokens lie down to it.
   template <bool ALL, class S>
-  __device__ __forceinline__ void find_bins(S stays, bool by_k, uint64_t k, float p, int& b0, int& b1,
+  __device__ __forceinline__ void find_bins(S stays, bool by_k, uint64_t k, float p, uint32_t& klo, uint32_t& khi, int& b1,
                                             uint64_t& tokens) {
     clear_hist();
     each([&](float v, int i) {
@@ -441,7 +454,13 @@ struct Row {
             sh.finds[0] = 4 * threadIdx.x + j;
             sh.finds[3] = n;
           }
-          if ((none || !reached(n, m, 1)) && reached(n1, m1, 1)) sh.middle = 4 * threadIdx.x + j;
+          if ((none || !reached(n, m, 1)) && reached(n1, m1, 1)) {
+            sh.middle = 4 * threadIdx.x + j;
+            // where in the bin, if its tokens are spread evenly, and half of a window for 512 of them
+            sh.place[0] = by_k ? __fdividef(static_cast<float>(k - n), static_cast<float>(c[j]))
+                               : __fdividef(static_cast<float>(all - behind[1] - m), static_cast<float>(w[j]));
+            sh.place[1] = __fdividef(256.0f, static_cast<float>(c[j]));
+          }
           if ((none || !reached(n, m, 2)) && reached(n1, m1, 2)) {
             sh.finds[1] = 4 * threadIdx.x + j;
             sh.finds[2] = n1;
@@ -458,29 +477,29 @@ struct Row {
         }
       }
       __syncthreads();
-      // a window of more tokens than a list holds: the bin where the end lies if every weight is
-      // its bin's, which it is nearly always where tokens are many (and else found out)
-      if (threadIdx.x == 0 && sh.finds[1] < kUsedBins && sh.finds[2] - sh.finds[3] > kList * 3 / 4)
-        sh.finds[0] = sh.finds[1] = sh.middle;
+      // Fewer tokens than a list holds, or about as many, are all taken; of more, those about the
+      // place where the end lies if every weight is its bin's, as it nearly always does where
+      // tokens are many (and else it is found out).
+      if (threadIdx.x == 0) {
+        const int n0 = 32 * wt.top + 31;
+        float hi = INFINITY, lo = -INFINITY;
+        if (sh.finds[1] < kUsedBins && sh.finds[2] - sh.finds[3] > kList * 3 / 4) {
+          const float at = static_cast<float>(n0 - sh.middle) + 0.5f - sh.place[0];
+          hi = at + sh.place[1];
+          lo = at - sh.place[1];
+        } else {
+          if (sh.finds[0] > 0) hi = static_cast<float>(n0 - static_cast<int>(sh.finds[0])) + 0.5f;
+          if (sh.finds[1] < kUsedBins) lo = static_cast<float>(n0 - static_cast<int>(sh.finds[1])) - 0.5f;
+        }
+        sh.finds[0] = __float_as_uint(hi);
+        sh.finds[3] = __float_as_uint(lo);
+      }
     }
-    tell(3);
-    b0 = static_cast<int>(sh.said[turn][0]);
+    tell(4);
     b1 = static_cast<int>(sh.said[turn][1]);
     tokens = sh.said[turn][2];
-  }
-
-  // The keys between which the values of bins b0 to b1 lie, with some room.
-  __device__ __forceinline__ void key_range(int b0, int b1, uint32_t& klo, uint32_t& khi) const {
-    klo = khi = order_key(INFINITY);
-    if (wt.infinite) return;
-    const auto edge = [&](float n, float room) {
-      const float x = n / wt.hi, v = wt.base + x;
-      return order_key(fmaf(fabsf(wt.base) + fabsf(x), room, v + room * 1e-30f));
-    };
-    const int n0 = 32 * wt.top + 31;
-    if (b0 > 0) khi = edge(static_cast<float>(n0 - b0) + 0.5f, 0x1p-20f);
-    klo = b1 < kUsedBins ? edge(static_cast<float>(n0 - b1) - 0.5f, -0x1p-20f) : order_key(kNegInf);
-    if (klo > khi) klo = khi;  // (not a number: no room was left)
+    klo = key_at(__uint_as_float(static_cast<uint32_t>(sh.said[turn][3])), -0x1p-20f);
+    khi = max(klo, key_at(__uint_as_float(static_cast<uint32_t>(sh.said[turn][0])), 0x1p-20f));
   }
 
   // ------------------------------------------------------- ranges by parts
@@ -1006,21 +1025,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
     *token = r.first + i;
     if (logprob) *logprob = log_share(r.wt, v, r.weight(v), all);
   };
+  uint64_t known = 0;  // this thread's weights above v_known, which all stay
+  float v_known = INFINITY;
   if (by_k || by_p) {
-    int m = -1, b0, b1;
+    int m = -1, b1;
     uint64_t sum = 0, tokens;
     uint32_t klo, khi;
     if (few) {
       m = r.template gather<false>(reach > 0x007fffffu ? value_of_order(reach) : kNegInf, sum);
     } else if (a.V <= kList) {  // all that have weight
-      r.key_range(0, kUsedBins - 1, klo, khi);
-      m = by_p && !by_k ? r.template gather<true>(value_of_order(klo), sum) : r.template gather<false>(value_of_order(klo), sum);
+      const float least = r.least_of(kUsedBins);
+      m = by_p && !by_k ? r.template gather<true>(least, sum) : r.template gather<false>(least, sum);
     }
     if (m < 0) {
-      r.template find_bins<true>(any, by_k, k, ask.top_p, b0, b1, tokens);
+      r.template find_bins<true>(any, by_k, k, ask.top_p, klo, khi, b1, tokens);
       if (tokens <= kList) {
-        r.key_range(b0, min(b1, kUsedBins - 1), klo, khi);  // (tokens without weight are not wanted)
-        m = by_k ? r.template gather<false>(value_of_order(klo), sum) : r.template gather<true>(value_of_order(klo), sum);
+        const float least = r.least_of(b1);
+        m = by_k ? r.template gather<false>(least, sum) : r.template gather<true>(least, sum);
       }
     }
     if (m >= 0) {  // the first CTA does the rest
@@ -1031,7 +1052,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
     }
     if (by_k && b1 < kUsedBins) {
       // what lies above the window is counted, its tokens are brought and sorted
-      r.key_range(b0, b1, klo, khi);
       const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
       r.begin_list();
       uint64_t above = 0;
@@ -1063,9 +1083,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
         set_cut(r.select(klo, khi, above, any, [](float) { return static_cast<uint64_t>(1); }, k));
     }
     if (by_p) {
-      if (by_k) r.template find_bins<false>(stays, false, 0, ask.top_p, b0, b1, tokens);
+      if (by_k) {
+        r.template find_bins<false>(stays, false, 0, ask.top_p, klo, khi, b1, tokens);
+        khi = max(khi, order_key(v_cut));  // (so that all above the window stay)
+      }
       // the same with weights; what stays above the window is kept by warp as well
-      r.key_range(b0, b1, klo, khi);
       const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
       uint64_t high = 0, low = 0;  // low: all
       const int i_cut = cut ? static_cast<int>(~static_cast<uint32_t>(cut)) - r.first : INT32_MAX;
@@ -1164,14 +1186,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
           return;
         }
       }
-      if (m < 0 || sh.said[r.turn][0] == 0)
+      if (m < 0 || sh.said[r.turn][0] == 0) {
         set_cut(r.select(klo, khi, above, stays, [&](float v) { return r.weight(v); }, need));
+        if (v_cut <= v_hi) {  // all above the window stay, and were added up
+          known = high;
+          v_known = v_hi;
+        }
+      }
     }
   }
 
   // --------------------------------------------------------------- the draw
   uint64_t all = 0;
-  if (cut != 0) {
+  if (ask.w_min == 0 && v_known < INFINITY) {
+    all = known;
+    r.each([&](float v, int i) {
+      if (v <= v_known && v >= v_cut) all += kept(v, i);
+    });
+  } else if (cut != 0) {
     r.each([&](float v, int i) { all += kept(v, i); });
   } else if (ask.w_min != 0) {
     r.each([&](float v, int) {
@@ -1211,10 +1243,13 @@ moe_status_t launch_as(const moe_sampling_t& a, int C, int per, cudaStream_t st)
 template <int DT>
 moe_status_t launch(const moe_sampling_t& a, cudaStream_t st) {
   const auto slice = [&](int C) { return ((a.V - 1) / C + 1 + kThreads - 1) / kThreads * kThreads; };
-  // A row's CTAs: about the two that an SM holds of every SM, or half as many again (rows differ in
-  // what they ask for: 64 rows of all kinds take 90 us by 4 CTAs, 72 by 8), of slices that are worth it.
+  // A row's CTAs, of slices that are worth it: about the two that an SM holds of every SM, or, of long
+  // slices, half as many again, as rows that ask for different things end at different times (64
+  // mixed rows of 151936 take 87 us by 4 CTAs, 67 by 8; 64 of 32000 take 26 by 4, 34 by 8).
   int C = 1;
-  while (C < kMaxCtas && static_cast<int64_t>(a.B) * C * 10 <= 17 * sm_count() && slice(C) > 2048) C *= 2;
+  while (C < kMaxCtas && slice(C) > 2048 &&
+         static_cast<int64_t>(a.B) * C * 10 <= (slice(C) > 32768 ? 17 : 10) * sm_count())
+    C *= 2;
   const int per = slice(C);
   // Held in shared memory where two CTAs still fit an SM, or one where there are no more CTAs.
   constexpr int size = sizeof(typename Stored<DT>::T);

@@ -182,6 +182,18 @@ def test_nearly_flat_rows(m, dtype, spread):
     _same(_run(m, logits.to(DEV), asks, us), refs)
 
 
+@pytest.mark.parametrize("spread", [0.005, 0.05, 0.5])
+@pytest.mark.parametrize("V", [20000, 131072])
+def test_both_borders_among_tokens_of_one_weight(m, V, spread):
+    """top_k ends inside a crowd of tokens of nearly one weight, and top_p of what it leaves as well."""
+    g = torch.Generator().manual_seed(V)
+    asks = [(1.0, V // 2, 0.97, 0.0), (1.0, V // 2, 0.5, 0.0), (0.5, V // 5, 0.999, 0.0), (1.0, V - 9, 0.9, 0.5),
+            (2.0, 5000, 0.7, 0.0), (1.0, 3 * V // 4, 0.01, 0.0)]
+    logits = torch.randn(len(asks), V, generator=g) * spread
+    us, refs = _refs(logits, asks, g)
+    _same(_run(m, logits.to(DEV), asks, us), refs)
+
+
 def test_draws_follow_the_weights(m):
     """Every token of a small row as often as its weight says: uniforms on a grid."""
     n = 4096
