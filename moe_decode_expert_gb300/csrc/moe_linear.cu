@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(192, 2)
 template <int N>
 struct Many {
   static constexpr uint32_t kStage = kTile + N / 2 * kBlock;
-  static constexpr int kStages = N == 256 ? 5 : 7;
+  static constexpr int kStages = N == 256 ? 4 : 7;
   static constexpr int kAcc = 512 / N;
   // Warps that issue MMAs, block by block in turn: what one does for a block (two waits, four
   // MMAs, two commits) takes longer than the block's MMAs (N = 128: 272 us with one warp, 202
@@ -358,11 +358,10 @@ struct Many {
   static constexpr int kIssuers = 2;
   static constexpr int kWarps = N / 16;  // of the epilogue
   static constexpr int kThreads = 128 + 32 * kWarps;
-  static constexpr int kLoad = N == 256 ? 16 : 32;       // columns of a load from tensor memory, and
-  static constexpr int kLoads = N == 256 ? 1 : 2;        // loads in flight: what registers allow
+  static constexpr int kLoads = N == 256 ? 1 : 2;        // loads of 32 columns in flight: what registers allow
   static constexpr int kChunk = 16;                      // blocks whose scales are staged at a time,
   static constexpr int kScales = kChunk * (128 + N / 128);  // floats: the rows' and the weight blocks'
-  static constexpr uint32_t kTurn = 32 * 64;             // bytes a warp turns its results in
+  static constexpr uint32_t kTurn = 32 * 128;            // bytes a warp turns its results in
   static constexpr size_t kSmem = kStages * kStage + 2 * kScales * 4 + kWarps * kTurn + 1024;
 };
 
@@ -402,40 +401,56 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// A warp's 32 rows of 64 results to memory, 64 bytes of each row at a time: through shared
-// memory (16-byte pieces, their order turned by the row against bank conflicts), so that
-// neighbouring lanes write neighbouring bytes.  SIZE: bytes of an output.
+// (a, b) += (x, y) * s, in one instruction (in two: 140 us for 8192 x 5120 x 4096, 136)
+__device__ __forceinline__ void fma2(float& a, float& b, uint32_t x, uint32_t y, float s) {
+  asm("{\n\t.reg .b64 c, d, e;\n\tmov.b64 c, {%2, %3};\n\tmov.b64 d, {%4, %4};\n\tmov.b64 e, {%0, %1};\n\t"
+      "fma.rn.f32x2 e, c, d, e;\n\tmov.b64 {%0, %1}, e;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(x), "r"(y), "f"(s));
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(smem_u32(src)),
+               "r"(c0), "r"(c1)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// A warp's 32 rows of 64 results to memory, 128 bytes of each row at a time: through shared
+// memory, in 16-byte pieces whose order is turned by the row as the 128-byte swizzle has it, and
+// from there by a bulk copy that goes on while the next tile is summed (stores of the warps' own
+// took 2.7 us of a tile's 17: 8192 x 5120 x 4096 151 us, so 136).  Rows that do not begin on 16 bytes, and their ends, are
+// written by the warp.
+// SIZE: bytes of an output.
 template <int SIZE>
-__device__ __forceinline__ void many_store(const moe_linear_t& a, const float (&acc)[64], uint8_t* turn, int m0, int n0,
-                                           int lane, int wide) {
-  constexpr int kCols = 64 / SIZE, kPiece = 16 / SIZE;  // of a pass, of a piece
+__device__ __forceinline__ void many_store(const moe_linear_t& a, const CUtensorMap* map, const float (&acc)[64],
+                                           uint8_t* turn, int m0, int n0, int lane, int bulk) {
+  constexpr int kCols = 128 / SIZE, kPiece = 16 / SIZE;  // of a pass, of a piece
 #pragma unroll
   for (int c0 = 0; c0 < 64; c0 += kCols) {
+    const int n = n0 + c0;
+    if (n >= a.N) break;
+    if (bulk && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < 8; ++p) {
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (SIZE == 4) w[j] = __float_as_uint(acc[c0 + 4 * p + j]);
-        else w[j] = pack2(a.out_dtype, acc[c0 + 8 * p + 2 * j], acc[c0 + 8 * p + 2 * j + 1]);
+        else w[j] = pack2(a.out_dtype, acc[8 * p + 2 * j], acc[8 * p + 2 * j + 1]);
       }
-      *reinterpret_cast<uint4*>(turn + lane * 64 + ((p ^ (lane >> 1)) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(turn + lane * 128 + ((p ^ lane) & 7) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __syncwarp();
-    const int n = n0 + c0;
-    if (wide && n + kCols <= a.N) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 2), p = lane & 3;
-        const uint4 v = *reinterpret_cast<const uint4*>(turn + r * 64 + ((p ^ (r >> 1)) & 3) * 16);
-        if (m0 + r < a.M)
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + ((m0 + r) * a.out_stride + n + p * kPiece) * SIZE) = v;
-      }
+    if (bulk && n + kCols <= a.N) {  // (the copy would fill up the last 16 bytes of a row)
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tma_store_2d(map, turn, n, m0);
     } else {
+      __syncwarp();
       for (int i = lane; i < 32 * kCols; i += 32) {
         const int r = i / kCols, c = i % kCols;
-        const uint8_t* at = turn + r * 64 + ((c / kPiece ^ (r >> 1)) & 3) * 16 + c % kPiece * SIZE;
+        const uint8_t* at = turn + r * 128 + ((c / kPiece ^ r) & 7) * 16 + c % kPiece * SIZE;
         if (m0 + r < a.M && n + c < a.N) {
           uint8_t* o = static_cast<uint8_t*>(a.out) + ((m0 + r) * a.out_stride + n + c) * SIZE;
           if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(at);
@@ -449,7 +464,7 @@ __device__ __forceinline__ void many_store(const moe_linear_t& a, const float (&
 template <int N>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1)
     linear_many_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
-                       moe_linear_t a, int KB, int mtiles, int tiles, int wide, Control* ctrl, uint64_t timeout) {
+                       const __grid_constant__ CUtensorMap mapOut, moe_linear_t a, int KB, int mtiles, int tiles, int bulk, Control* ctrl, uint64_t timeout) {
   using G = Many<N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -485,9 +500,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
   pdl_launch_dependents();
   pdl_wait();
   const uint32_t tbase = tmem_base_s;
-  // (N = 256: 640 threads of 96 registers at launch, 128 * 56 + 512 * 104 then)
+  // (N = 256: 640 threads of 96 registers at launch, 128 * 32 + 512 * 112 then)
   if constexpr (N == 256)
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
 
   if (warp == 0) {
     if (lane == 0) {  // ---------------------------------------------- TMA producer
@@ -560,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
   } else if (warp < 4) {  // ------------------------------------------- scales
     // A chunk's scales, two chunks in turn: four rows a thread, and the weight block's.  (Loaded by each
     // thread of the epilogue for its own row they missed L1, which 128 rows a line apart overflow.)
-    float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage);
+    float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage + G::kWarps * G::kTurn);
     int buf = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -592,12 +607,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
       if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
     }
   } else {  // ------------------------------------------------------- epilogue
-    if constexpr (N == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if constexpr (N == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     const int q = warp & 3, g = (warp - 4) >> 2;  // quarter of the TMEM lanes, 64 of the columns
     const uint32_t lane0 = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(64 * g);
     const uint32_t free_bar = peer_addr(smem_u32(&tempty[0]), 0);
-    float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage);
-    uint8_t* turn = reinterpret_cast<uint8_t*>(scales + 2 * G::kScales) + (warp - 4) * G::kTurn;
+    float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage + G::kWarps * G::kTurn);
+    uint8_t* turn = smem + G::kStages * G::kStage + (warp - 4) * G::kTurn;
     int b = 0, buf = 0, in = 0;  // accumulator; chunk of scales and block in it
     uint32_t bphase = 0, sphase = 0;
     bool ok = true;
@@ -624,34 +639,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
         }
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 64; c += G::kLoad * G::kLoads) {
-          uint32_t v[G::kLoads][G::kLoad];
+        for (int c = 0; c < 64; c += 32 * G::kLoads) {
+          uint32_t v[G::kLoads][32];
 #pragma unroll
-          for (int u = 0; u < G::kLoads; ++u) {
-            const uint32_t ta = lane0 + static_cast<uint32_t>(b * N + c + u * G::kLoad);
-            if constexpr (G::kLoad == 32) tmem_ld32_issue(ta, v[u]);
-            else tmem_ld16_issue(ta, v[u]);
-          }
+          for (int u = 0; u < G::kLoads; ++u) tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * N + c + 32 * u), v[u]);
           tmem_ld_wait();
 #pragma unroll
           for (int u = 0; u < G::kLoads; ++u) tmem_ld_tie(v[u]);
-          if (c + G::kLoad * G::kLoads == 64) {
+          if (c + 32 * G::kLoads == 64) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
           }
 #pragma unroll
-          for (int j = 0; j < G::kLoad * G::kLoads; ++j)
-            acc[c + j] = fmaf(__uint_as_float(v[j / G::kLoad][j % G::kLoad]), s, acc[c + j]);
+          for (int j = 0; j < 32 * G::kLoads; j += 2)
+            fma2(acc[c + j], acc[c + j + 1], v[j / 32][j % 32], v[j / 32][j % 32 + 1], s);
         }
         if (++b == G::kAcc) { b = 0; bphase ^= 1u; }
       }
       if (!ok) continue;
       const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * N + 64 * g;
       if (m0 >= a.M || n0 >= a.N) continue;
-      if (a.out_dtype == MOE_F32) many_store<4>(a, acc, turn, m0, n0, lane, wide);
-      else many_store<2>(a, acc, turn, m0, n0, lane, wide);
+      if (a.out_dtype == MOE_F32) many_store<4>(a, &mapOut, acc, turn, m0, n0, lane, bulk);
+      else many_store<2>(a, &mapOut, acc, turn, m0, n0, lane, bulk);
     }
+    if (bulk && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok) {
       s_abort = 1;
       if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
@@ -668,16 +680,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
 }
 
 // ================================================================ host
-// 2-D K-major map of bytes: `inner` per row, `outer` rows `stride` apart; box of
-// 128 x box_rows, 128-byte swizzle; zeros outside.
-bool byte_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_rows) {
+// 2-D map of `outer` rows of `inner` elements of `size` bytes, `stride` bytes apart; box of
+// 128 bytes x box_rows, 128-byte swizzle; zeros outside.
+bool map_2d(CUtensorMap* m, CUtensorMapDataType type, uint32_t size, const void* base, uint64_t inner, uint64_t outer,
+            uint64_t stride, uint32_t box_rows) {
   const auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, outer}, strides[1] = {stride};
-  cuuint32_t box[2] = {kBlock, box_rows}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint32_t box[2] = {128 / size, box_rows}, estr[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool byte_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_rows) {
+  return map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, inner, outer, stride, box_rows);
 }
 
 template <int NT>
@@ -719,11 +736,16 @@ moe_status_t launch_many(const moe_linear_t& l, int KB, Control* ctrl, cudaStrea
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
   if (raise_smem_limit(linear_many_kernel<N>, Many<N>::kSmem) != cudaSuccess)
     return check_launch("linear_many_kernel (smem)");
-  const int per = l.out_dtype == MOE_F32 ? 4 : 8;
-  const int wide = (reinterpret_cast<uintptr_t>(l.out) & 15u) == 0 && l.out_stride % per == 0;
+  const int size = l.out_dtype == MOE_F32 ? 4 : 2;
+  const int bulk = (reinterpret_cast<uintptr_t>(l.out) & 15u) == 0 && l.out_stride * size % 16 == 0 &&
+                   l.out_stride * size < int64_t(1) << 40;
+  CUtensorMap mo = mx;
+  if (bulk && !map_2d(&mo, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, size, l.out, l.N, l.M,
+                      l.out_stride * size, 32))
+    return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
   const int pairs = sm_count() / 2;
   if (launch_pdl(linear_many_kernel<N>, dim3(2 * (tiles < pairs ? tiles : pairs)), dim3(Many<N>::kThreads), Many<N>::kSmem,
-                 st, mx, mw, l, KB, mtiles, tiles, wide, ctrl, wait_timeout_ns()) != cudaSuccess)
+                 st, mx, mw, mo, l, KB, mtiles, tiles, bulk, ctrl, wait_timeout_ns()) != cudaSuccess)
     return check_launch("linear_many_kernel");
   stat_kernels(1);
   return MOE_OK;
@@ -774,13 +796,13 @@ extern "C" moe_status_t moe_linear_e4m3(const moe_linear_t* l, void* ws, size_t 
   Control* ctrl = static_cast<Control*>(ws);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Few rows, or so few tiles of many that most pairs of SMs would have none (256 x 2048 x 4096,
-  // 16 tiles for 76 pairs: 14.7 us, 10.5 by tiles of 64 rows and parts of K).
+  // 16 tiles for 76 pairs: 14.0 us, 10.3 by tiles of 64 rows and parts of K).
   const int64_t pairs = sm_count() / 2, m256 = (a.M - 1) / 256 + 1;
   if (a.M <= 16) return launch_few<16>(a, KB, ctrl, st);
   if (a.M <= 32) return launch_few<32>(a, KB, ctrl, st);
   if (a.M <= 128 || m256 * nb * 4 <= pairs) return launch_few<64>(a, KB, ctrl, st);
-  // Wider tiles take a block in 0.52 us, where two narrower take 0.69: 8192 x 5120 x 4096 151 us
-  // against 188, but 256 x 5120 x 2048, 20 tiles or 40 for 76 pairs, 13.6 against 11.0.
+  // A wider tile takes about 1.5 times as long as a narrower: 8192 x 5120 x 4096 136 us against
+  // 173, but 256 x 5120 x 2048, 20 tiles or 40 for 76 pairs, 12.7 against 10.3.
   const auto rounds = [&](int n) { return (m256 * ((a.N - 1) / n + 1) + pairs - 1) / pairs; };
   if (3 * rounds(256) <= 2 * rounds(128)) return launch_many<256>(a, KB, ctrl, st);
   return launch_many<128>(a, KB, ctrl, st);

@@ -85,6 +85,22 @@ def test_strided_rows_and_nothing_beside(m, ws, M, stride):
         assert (out == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+@pytest.mark.parametrize("M,N,K,stride,offset", [
+    (600, 2999, 144, 3000, 0), (600, 2999, 300, 3024, 8), (1100, 4111, 272, 4112, 0), (1100, 4111, 130, 4111, 0),
+    (1100, 4111, 700, 4128, 16), (2100, 2567, 16, 2570, 1)])
+def test_many_rows_of_many_tiles(m, ws, M, N, K, stride, offset, dtype):
+    """Several tiles for each pair of SMs, rows that begin on 16 bytes and that do not, nothing beside."""
+    a = _inputs(M, N, K, M + K)
+    out = torch.full((M + 3, stride), 7.0, device=DEV, dtype=dtype)
+    got = out[:M, offset:offset + N]
+    m.moe_linear_e4m3(*_to(a, None), got, ws)
+    m.moe_query_status(ws)
+    _check(got, a)
+    got.fill_(7.0)
+    assert (out == 7).all()
+
+
 @pytest.mark.parametrize("M", [3, 20, 64, 100, 200])
 def test_nan_and_infinity_reach_only_what_they_are_factors_of(m, ws, M):
     N, K = 300, 384
