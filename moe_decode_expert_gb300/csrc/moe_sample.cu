@@ -15,6 +15,10 @@
 // settles everything.  Otherwise a pass sums what lies above a window about the end,
 // and the first CTA gets the window's tokens; where these are too many (ties, or an
 // end outside), the range of values is divided by 512 until one value is left.
+//
+// One row is a chain of latencies (151936 logits 9 us); many rows are bound by their
+// instructions, about 50 a warp for 32 tokens where weights are summed: 256 rows of
+// 131072, fp32, 81 us without filters, 154 with a top-p that ends among thousands.
 
 #include <algorithm>
 
