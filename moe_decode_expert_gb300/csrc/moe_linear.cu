@@ -41,6 +41,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // Fetch a tile into L2 (may come before griddepcontrol.wait: L2 is where writes meet).
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1) : "memory");
@@ -120,14 +126,14 @@ __global__ void __launch_bounds__(192, 2)
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int s_abort;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x % S);
   const int tile = static_cast<int>(blockIdx.x / S);
   const int m0 = tile % mtiles * NT, nt = tile / mtiles, n0 = nt * 128;
   const int kb0 = static_cast<int>(static_cast<int64_t>(KB) * rank / S);
   const int nkb = static_cast<int>(static_cast<int64_t>(KB) * (rank + 1) / S) - kb0;
   float* parts = scales + ((KB + S - 1) / S > F::kChunk ? 2 : 1) * (F::kScales / 4);
-  const int width = NT / S;  // columns whose sums this CTA adds: fours, or two
+  const int width = NT / S, wshift = __ffs(width) - 1;  // columns whose sums this CTA adds: fours, or two
   constexpr int kMinVec = NT == 16 ? 2 : 4;
   const int vec = NT == 16 && width == 2 ? 2 : 4;
   if (threadIdx.x == 0) {
@@ -144,6 +150,8 @@ __global__ void __launch_bounds__(192, 2)
     tensormap_prefetch(&mapX);
     for (int i = 0; i < min(nkb, stages); ++i) tma_prefetch_2d(&mapW, (kb0 + i) * kBlock, n0);
   }
+  if (threadIdx.x == 64)  // (the weight's scales to L2, as the weight; of a row of scales' 128 bytes)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.w_scales + static_cast<int64_t>(nt) * KB + kb0));
   if (warp == 1) {
     tmem_alloc(&tmem_base_s, F::kCols);
     tmem_relinquish();
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(192, 2)
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
       for (int i = 0; i < nkb; ++i) {
-        if (!tc_wait_polled(&empty[stage], phase ^ 1u, timeout, &s_abort)) {
+        if (i >= stages && !tc_wait_polled(&empty[stage], phase ^ 1u, timeout, &s_abort)) {
           s_abort = 1;
           report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
           break;
@@ -182,27 +190,34 @@ __global__ void __launch_bounds__(192, 2)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {  // ---------------------------------------------- MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3<NT>();
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int i = 0; i < nkb; ++i) {
-        const int b = i % F::kAcc;
-        if (!tc_wait_polled(&tempty[b], ((i / F::kAcc) & 1) ^ 1u, timeout, &s_abort) ||
-            !tc_wait_polled(&full[stage], phase, timeout, &s_abort)) {
-          s_abort = 1;
-          report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sA = smem_u32(smem + stage * F::kStage), sB = sA + kTile;
+    // ----------------------------------------------------------------- MMA issuer
+    // (the whole warp goes through the loop and one thread of it issues: with the others gone, an
+    // MMA's descriptors are moved to the uniform registers it takes them from one by one)
+    constexpr uint32_t idesc = idesc_e4m3<NT>();
+    const uint64_t adesc = sw128_desc(smem_u32(smem)), bdesc = sw128_desc(smem_u32(smem) + kTile);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < nkb; ++i) {
+      const int b = i % F::kAcc;
+      if (!__all_sync(0xffffffffu, (i < F::kAcc || tc_wait_polled(&tempty[b], ((i / F::kAcc) & 1) ^ 1u, timeout, &s_abort)) &&
+                                       tc_wait_polled(&full[stage], phase, timeout, &s_abort))) {
+        s_abort = 1;
+        if (lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
+        break;
+      }
+      tc_fence_after();
+      const uint64_t at = static_cast<uint64_t>(stage) * (F::kStage >> 4);  // of a descriptor's address
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_e4m3(tbase + static_cast<uint32_t>(b * NT), sw128_desc(sA + 32 * k), sw128_desc(sB + 32 * k), idesc, k != 0);
+          mma_e4m3(tbase + static_cast<uint32_t>(b * NT), adesc + at + 2 * k, bdesc + at + 2 * k, idesc, k != 0);
         tc_commit(&empty[stage]);
         tc_commit(&tfull[b]);
-        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
+      __syncwarp();
+      if (++stage == stages) { stage = 0; phase ^= 1u; }
+    }
+    if (elect_one()) {
       tc_commit(&done);  // completes once every MMA issued above has completed
       mbar_wait_until(&done, 0, global_ns() + timeout);
     }
@@ -211,18 +226,21 @@ __global__ void __launch_bounds__(192, 2)
     const int q = warp & 3;
     const int row = 32 * q + lane;      // weight row of the tile = TMEM lane
     const int etid = threadIdx.x - 64;  // 0..127
-    constexpr int kPer = NT * F::kChunk / 128, kStep = NT == 16 ? 16 : 32;
+    constexpr int kPer = NT * F::kChunk / 128, kChunkBits = 4, kStep = NT == 16 ? 16 : 32;
+    static_assert(F::kChunk == 1 << kChunkBits, "chunks of a power of two");
     float acc[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
     float next[kPer];
-    // products of both scales for blocks [c * kChunk, ..), zero beyond M and the last block
+    // A chunk's blocks are 2^cb, of kChunk at most: where there are few, no thread asks for others.
+    const int cb = min(32 - __clz(nkb - 1), kChunkBits), cmask = (1 << cb) - 1;
+    // products of both scales for blocks [c << cb, ..), zero beyond M and the last block
     const auto fetch = [&](int chunk) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
-        const int at = etid + 128 * u, t = at / F::kChunk, i = chunk * F::kChunk + at % F::kChunk;
+        const int at = etid + 128 * u, t = at >> cb, i = (chunk << cb) + (at & cmask);
         next[u] = 0.0f;
-        if (i < nkb && m0 + t < a.M)
+        if (t < NT && i < nkb && m0 + t < a.M)
           next[u] = a.x_scales[static_cast<int64_t>(m0 + t) * KB + kb0 + i] *
                     a.w_scales[static_cast<int64_t>(nt) * KB + kb0 + i];
       }
@@ -230,18 +248,18 @@ __global__ void __launch_bounds__(192, 2)
     const auto stage_scales = [&](int buf) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
-        const int at = etid + 128 * u;
-        scales[(buf * F::kChunk + at % F::kChunk) * F::kPitch + at / F::kChunk] = next[u];
+        const int at = etid + 128 * u, t = at >> cb;
+        if (t < NT) scales[(buf * F::kChunk + (at & cmask)) * F::kPitch + t] = next[u];
       }
     };
     fetch(0);
     bool ok = true;
     for (int i = 0; i < nkb; ++i) {
-      const int chunk = i / F::kChunk, in = i % F::kChunk;
+      const int chunk = i >> cb, in = i & cmask;
       if (in == 0) {
         stage_scales(chunk & 1);
         named_bar_sync(1, 128);  // (also: every warp is past the chunk before the last, whose place this was)
-        if ((chunk + 1) * F::kChunk < nkb) fetch(chunk + 1);
+        if ((chunk + 1) << cb < nkb) fetch(chunk + 1);
       }
       const int b = i % F::kAcc;
       // (a wait that ran out leaves the loop running without it, so that all warps meet at the barriers)
@@ -291,7 +309,7 @@ __global__ void __launch_bounds__(192, 2)
 #pragma unroll
       for (int c = 0; c < NT; c += kMinVec) {
         if (m0 + c >= a.M) break;
-        const int to = c / width;
+        const int to = c >> wshift;
         const uint32_t at = mine + static_cast<uint32_t>((c - to * width) * 512);
         float* here = parts + (rank * width + c - to * width) * 128 + row * vec;
         if (kMinVec == 2 && vec == 2) {
@@ -384,12 +402,6 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, u
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// One thread of a converged warp, always the same.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
 }
 // Arrives on the barrier at this offset in both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
