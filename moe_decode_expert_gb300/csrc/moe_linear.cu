@@ -816,7 +816,9 @@ extern "C" moe_status_t moe_linear_e4m3(const moe_linear_t* l, void* ws, size_t 
   // 16 tiles for 76 pairs: 14.0 us, 10.3 by tiles of 64 rows and parts of K).
   const int64_t pairs = sm_count() / 2, m256 = (a.M - 1) / 256 + 1;
   if (a.M <= 16) return launch_few<16>(a, KB, ctrl, st);
-  if (a.M <= 32) return launch_few<32>(a, KB, ctrl, st);
+  // (Tiles of 64 rows exchange twice the sums, and of 32 read the weight from L2 twice as often: 64 x
+  // 5120 x 2048 7.4 us by 64, 6.7 by 32; 64 x 5120 x 8192 13.7 by 64, 14.9 by 32.)
+  if (a.M <= 32 || (a.M <= 128 && static_cast<int64_t>(nb) * KB <= 8 * sm_count())) return launch_few<32>(a, KB, ctrl, st);
   if (a.M <= 128 || m256 * nb * 4 <= pairs) return launch_few<64>(a, KB, ctrl, st);
   // A wider tile takes about 1.5 times as long as a narrower: 8192 x 5120 x 4096 136 us against
   // 173, but 256 x 5120 x 2048, 20 tiles or 40 for 76 pairs, 12.7 against 10.3.
