@@ -10,8 +10,8 @@
 // in another accumulator.  A block of K is 128 bytes, one row of the 128-byte
 // swizzle, so a stage of the ring is one block of both operands.
 //
-// Few rows stream the weight: 8 x 151936 x 2048 53 us, 5920 GB/s, 89 % of the copy;
-// one row x 5120 x 2048 4.5 us in a graph, launch and latency.  Many rows are bound by
+// Few rows stream the weight: 8 x 151936 x 2048 51 us, 6150 GB/s, 92 % of the copy;
+// one row x 5120 x 2048 3.9 us in a graph, launch and latency.  Many rows are bound by
 // the sums: reading a 256 x 256 accumulator and adding it takes as long as the MMAs
 // that make it (8192 x 5120 x 4096 136 us, 2525 TFLOP/s; 116 with no accumulator read).
 

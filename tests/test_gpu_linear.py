@@ -62,7 +62,8 @@ def _check(out, a):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (1, 128, 128), (2, 129, 130), (7, 5120, 512), (16, 300, 2000), (17, 127, 640), (32, 1000, 4096),
     (33, 257, 48), (64, 520, 1040), (65, 200, 272), (128, 384, 2176), (129, 1, 16), (130, 700, 384), (257, 255, 2100),
-    (512, 1447, 256), (777, 256, 2000), (1, 40000, 256), (3, 64, 20000), (300, 64, 5008)])
+    (512, 1447, 256), (777, 256, 2000), (1, 40000, 256), (3, 64, 20000), (300, 64, 5008), (70, 20480, 1024),
+    (128, 40001, 512), (90, 300, 70000)])
 def test_products(m, ws, M, N, K, dtype):
     a = _inputs(M, N, K, M + N + K)
     out = torch.full((M, N), math.nan, device=DEV, dtype=dtype)
