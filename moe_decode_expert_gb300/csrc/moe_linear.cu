@@ -813,7 +813,7 @@ extern "C" moe_status_t moe_linear_e4m3(const moe_linear_t* l, void* ws, size_t 
   Control* ctrl = static_cast<Control*>(ws);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Few rows, or so few tiles of many that most pairs of SMs would have none (256 x 2048 x 4096,
-  // 16 tiles for 76 pairs: 14.0 us, 10.3 by tiles of 64 rows and parts of K).
+  // 16 tiles for 76 pairs: 14.0 us, 9.6 by tiles of 64 rows and parts of K).
   const int64_t pairs = sm_count() / 2, m256 = (a.M - 1) / 256 + 1;
   if (a.M <= 16) return launch_few<16>(a, KB, ctrl, st);
   // (Tiles of 64 rows exchange twice the sums, and of 32 read the weight from L2 twice as often: 64 x

@@ -194,6 +194,16 @@ def test_both_borders_among_tokens_of_one_weight(m, V, spread):
     _same(_run(m, logits.to(DEV), asks, us), refs)
 
 
+@pytest.mark.parametrize("dtype,copies", [(F32, 1), (BF, 7), (FP, 40)])
+def test_the_longest_rows(m, dtype, copies):
+    """Few rows over a cluster each, and so many that they are read from memory again."""
+    g = torch.Generator().manual_seed(copies)
+    asks = [OFF, (0.7, 20, 0.8, 0.0), (1.0, 0, 0.95, 0.0), (1.3, 90000, 0.9, 1e-4)]
+    logits = (torch.randn(len(asks), 393216, generator=g) * 2).to(dtype)
+    us, refs = _refs(logits, asks, g)
+    _same(_run(m, logits.to(DEV).repeat(copies, 1), asks * copies, us.repeat(copies)), refs * copies)
+
+
 def test_draws_follow_the_weights(m):
     """Every token of a small row as often as its weight says: uniforms on a grid."""
     n = 4096
