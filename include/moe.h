@@ -394,9 +394,8 @@ MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_
 
 /* Quantisation: x [T, H] in blocks of `rows` (1 or 128) rows by 128 columns,
  *   s = max(max |x|, 2^-96) / 448 over the block;  out = e4m3(x / s)
- * (x times the reciprocal of s, both rounded to fp32; the last block of a row or
- * column may be smaller).  rows = 1 is the form of
- * activations, rows = 128 that of weights.  A NaN makes its block's scale and
+ * (s and the quotient each rounded to fp32; the last block of a row or column may
+ * be smaller).  rows = 1 is the form of activations, rows = 128 that of weights.  A NaN makes its block's scale and
  * values NaN; an infinity its scale infinite, itself NaN and the others zero.
  * Any T >= 0, H >= 1 and row strides >= H; rows whose pointers and strides are
  * multiples of 16 bytes (8 for out) with H % 8 == 0 take the wide loads.

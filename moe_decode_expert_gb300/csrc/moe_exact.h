@@ -1,0 +1,61 @@
+// moe_exact.h — arithmetic of the kernels whose results are exact by an argument about their bits:
+// plain C++, so that the host can try it at every value it depends on.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#ifdef __CUDACC__
+#define MOE_HD __host__ __device__ __forceinline__
+#else
+#define MOE_HD inline
+#endif
+
+namespace moe {
+
+// -x / s in fp32 as a division rounds it, for many x of 16-bit types and one s = rn(a / 448), a of
+// the same type and at least |x|: a product with the reciprocal, and one correction by what the
+// product leaves over.  Codes where x / s is halfway between two e4m3 values would else go by the
+// reciprocal's rounding (4 in 10^4 of bf16 rows).  What is left over has bits 58 places below s, so
+// where s is tiny x is scaled up as it is (UP; never so in fp16, whose s is from 2^-33 on or a zero
+// block's).  Where x / s is below 2^-11, a code of zero, it may be off.
+// Negated, a zero keeps its sign without an operation for it: a sum of two zeros is +0 unless both
+// are -0.  Two values an instruction (by one: 8192 x 4096 18.9 us).
+struct Quotient {
+  float minus_inv, s;
+  bool tiny;
+  MOE_HD explicit Quotient(float scale) {
+    tiny = scale < 0x1p-80f;
+    s = tiny ? scale * 0x1p64f : scale;
+#ifdef __CUDA_ARCH__
+    minus_inv = -__frcp_rn(s);
+#else
+    minus_inv = -(1.0f / s);
+#endif
+    if (s == INFINITY) s = 0.0f;  // (finite x: zero, as the reciprocal is; infinite: not a number)
+  }
+  MOE_HD void divide2(float& x, float& y) const {
+#ifdef __CUDA_ARCH__
+    asm("{\n\t.reg .b64 v, i, s, q, r;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 i, {%2, %2};\n\tmov.b64 s, {%3, %3};\n\t"
+        "mul.rn.f32x2 q, v, i;\n\tfma.rn.f32x2 r, q, s, v;\n\tfma.rn.f32x2 q, r, i, q;\n\tmov.b64 {%0, %1}, q;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(minus_inv), "f"(s));
+#else
+    for (float* v : {&x, &y}) {
+      const float q = *v * minus_inv;
+      *v = fmaf(fmaf(q, s, *v), minus_inv, q);
+    }
+#endif
+  }
+  template <bool UP, int N>
+  MOE_HD void divide(float (&x)[N]) const {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      if (UP) x[j] *= 0x1p64f, x[j + 1] *= 0x1p64f;
+      divide2(x[j], x[j + 1]);
+    }
+  }
+};
+
+}  // namespace moe

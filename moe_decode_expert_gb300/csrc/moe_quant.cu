@@ -3,16 +3,20 @@
 //
 //   s = max(max|x|, 2^-96) / 448 over the block;  out = e4m3(x / s)
 //
+// with the quotient rounded to fp32 first.
 // A block's values stay in registers between its largest magnitude and the
-// output, so every input is read once.  Magnitudes are reduced as unsigned bit
-// patterns: their order is that of the floats, with NaN above infinity, so a NaN
-// reaches its block's scale.
+// output, so every input is read once.  Magnitudes are reduced as unsigned 16-bit
+// patterns, two an instruction: their order is that of the floats, with NaN above
+// infinity, so a NaN reaches its block's scale.
 //
-// HBM bounds it: 8192 rows of 4096 in bf16 16.9 us, 5970 GB/s, 89 % of the copy.
+// HBM bounds it: 8192 rows of 4096 in bf16 16.9 us, 6020 GB/s, 90 % of the copy.
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "moe_common.cuh"
+#include "moe_exact.h"
 #include "moe_internal.h"
 #include "moe_kv.h"
 
@@ -27,7 +31,16 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   const float a = __uint_as_float(amax);
   return __fdiv_rn(a < kAmaxFloor ? kAmaxFloor : a, kE4m3Max);
 }
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+// fp32 bits of a 16-bit magnitude
+template <int DT>
+__device__ __forceinline__ uint32_t wide(uint32_t m) {
+  return __float_as_uint(unpack2<DT>(m).x);
+}
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -35,22 +48,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-template <int DT>
+// The largest magnitudes of the even and of the odd values.
 __device__ __forceinline__ uint32_t amax8(const uint4& v) {
-  float f[8];
-  unpack8<DT>(v, f);
-  uint32_t m = 0u;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, magnitude(f[j]));
-  return m;
+  return max16x2(max16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), max16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
 }
-template <int DT>
-__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
+// f, of a constant: whether the block's values are scaled up to be divided.
+template <int DT, class F>
+__device__ __forceinline__ void by_size(const Quotient& by, F f) {
+  if (DT == MOE_BF16 && by.tiny) f(std::true_type());
+  else f(std::false_type());
+}
+__device__ __forceinline__ uint32_t either(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+template <int DT, bool UP>
+__device__ __forceinline__ uint2 codes8(const uint4& v, const Quotient& by) {
   float f[8];
   unpack8<DT>(v, f);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] *= inv;
-  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+  by.divide<UP>(f);
+  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]) ^ 0x80808080u, e4m3x4(f[4], f[5], f[6], f[7]) ^ 0x80808080u);
 }
 
 // Blocks of one row, 16-byte loads: 8 neighbouring lanes hold a block, 16 columns
@@ -76,14 +90,19 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(moe_quant_t a, int
   }
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    uint32_t m = max(amax8<DT>(v[u][0]), amax8<DT>(v[u][1]));
+    uint32_t m = max16x2(amax8(v[u][0]), amax8(v[u][1]));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = scale_of(m), inv = __frcp_rn(s);
+    for (int o = 1; o < 8; o <<= 1) m = max16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = scale_of(wide<DT>(either(m)));
+    const Quotient by(s);
     if (first + 32 * u >= total) break;
     if (sub == 0) a.scales[first + 32 * u] = s;
     uint8_t* o = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row[u]) * a.out_stride + col[u];
-    const uint2 lo = codes8<DT>(v[u][0], inv), hi = codes8<DT>(v[u][1], inv);
+    uint2 lo, hi;
+    by_size<DT>(by, [&](auto up) {
+      lo = codes8<DT, up>(v[u][0], by);
+      hi = codes8<DT, up>(v[u][1], by);
+    });
     if (EVEN && col[u] + 8 < a.H) {
       *reinterpret_cast<uint4*>(o) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     } else {
@@ -95,7 +114,7 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(moe_quant_t a, int
 
 // At any alignment a warp has a row's part of a block, lane l its columns l, l + 32, l + 64 and
 // l + 96: neighbouring lanes write neighbouring bytes.  Bound by the memory instructions, one per
-// 32 elements: 5120 x 2003 by blocks of 128 rows 10.6 us, 49 % of the 6680 GB/s copy.  (Eight columns a
+// 32 elements: 5120 x 2003 by blocks of 128 rows 9.9 us, 47 % of the 6680 GB/s copy.  (Eight columns a
 // lane, stored in words put together from two lanes' bytes: 20 us.)
 // (The four stay apart until all loads are out: put together at once, each load was waited for, 28 us.)
 struct Spread {
@@ -104,19 +123,29 @@ struct Spread {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = 32 * j < n ? p[32 * j] : 0;
   }
+  // The largest magnitude's fp32 bits, or what gives them to wide().  (Of bf16 as it is stored: through
+  // fp32 the loads were waited for one by one, 5120 x 2003 25.2 us, so 11.6; of fp16 by its
+  // conversions, which keep the loads together: 11.2 us, as it is stored 11.6.)
   template <int DT>
   __device__ __forceinline__ uint32_t amax() const {
     uint32_t m = 0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, magnitude(unpack2<DT>(v[j]).x));
+    for (int j = 0; j < 4; ++j) m = max(m, DT == MOE_BF16 ? v[j] & 0x7fffu : __float_as_uint(unpack2<DT>(v[j]).x) & 0x7fffffffu);
     return m;
   }
   template <int DT>
-  __device__ __forceinline__ void store(uint8_t* o, int n, float inv) const {
+  static __device__ __forceinline__ uint32_t bits(uint32_t amax) {
+    return DT == MOE_BF16 ? wide<DT>(amax) : amax;
+  }
+  template <int DT, bool UP>
+  __device__ __forceinline__ void store(uint8_t* o, int n, const Quotient& by) const {
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = unpack2<DT>(v[j]).x;
+    by.divide<UP>(f);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (32 * j < n)
-        o[32 * j] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(unpack2<DT>(v[j]).x * inv, __NV_SATFINITE, __NV_E4M3));
+      if (32 * j < n) o[32 * j] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(f[j], __NV_SATFINITE, __NV_E4M3) ^ 0x80);
   }
 };
 
@@ -139,10 +168,11 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(moe_quant_t a, int bloc
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     if (first + 8 * u >= total) break;
-    const float s = scale_of(__reduce_max_sync(0xffffffffu, v[u].template amax<DT>()));
+    const float s = scale_of(Spread::bits<DT>(__reduce_max_sync(0xffffffffu, v[u].template amax<DT>())));
     if (lane == 0) a.scales[first + 8 * u] = s;
-    v[u].template store<DT>(static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row[u]) * a.out_stride + col[u], a.H - col[u],
-                            __frcp_rn(s));
+    uint8_t* o = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row[u]) * a.out_stride + col[u];
+    const Quotient by(s);
+    by_size<DT>(by, [&](auto up) { v[u].template store<DT, up>(o, a.H - col[u], by); });
   }
 }
 
@@ -176,22 +206,25 @@ __global__ void __launch_bounds__(WIDE ? 256 : 512) quant_blocks_kernel(moe_quan
   }
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
-    if constexpr (WIDE) m = max(m, amax8<DT>(v[p]));
+    if constexpr (WIDE) m = max16x2(m, amax8(v[p]));
     else m = max(m, e[p].template amax<DT>());
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  m = __reduce_max_sync(0xffffffffu, WIDE ? either(m) : m);
   if (lane == 0) s_max[warp] = m;
   __syncthreads();
-  const float s = scale_of(__reduce_max_sync(0xffffffffu, s_max[lane & (kWarps - 1)]));
-  const float inv = __frcp_rn(s);
+  m = __reduce_max_sync(0xffffffffu, s_max[lane & (kWarps - 1)]);
+  const float s = scale_of(WIDE ? wide<DT>(m) : Spread::bits<DT>(m));
+  const Quotient by(s);
   if (threadIdx.x == 0) a.scales[at] = s;
+  by_size<DT>(by, [&](auto up) {
 #pragma unroll
-  for (int p = 0; p < kPass; ++p) {
-    const int64_t row = r0 + kPer * p;
-    if (row >= a.T || c0 >= a.H) continue;
-    if constexpr (WIDE) *reinterpret_cast<uint2*>(o + row * a.out_stride + c0) = codes8<DT>(v[p], inv);
-    else e[p].template store<DT>(o + row * a.out_stride + c0, a.H - c0, inv);
-  }
+    for (int p = 0; p < kPass; ++p) {
+      const int64_t row = r0 + kPer * p;
+      if (row >= a.T || c0 >= a.H) continue;
+      if constexpr (WIDE) *reinterpret_cast<uint2*>(o + row * a.out_stride + c0) = codes8<DT, up>(v[p], by);
+      else e[p].template store<DT, up>(o + row * a.out_stride + c0, a.H - c0, by);
+    }
+  });
 }
 
 template <int DT>
