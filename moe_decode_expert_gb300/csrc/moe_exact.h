@@ -58,4 +58,17 @@ struct Quotient {
   }
 };
 
+// Sums of the draw's weights in 32-bit words, kWordBits of every weight in each: a CTA may have every
+// token of the longest row, all in one sum.
+constexpr int kMaxLogits = 393216;  // of a row
+constexpr int kWeightBits = 45;     // a weight is below 2^this, so a row's sum below 2^64
+constexpr int kWordBits = 12, kWords = 4;
+static_assert(kWords * kWordBits >= kWeightBits, "every bit of a weight is in a word");
+static_assert(static_cast<uint64_t>(kMaxLogits) * ((1u << kWordBits) - 1) <= UINT32_MAX, "a word holds a row's sum");
+static_assert(kMaxLogits <= UINT64_MAX >> kWeightBits, "64 bits hold a row's sum");
+MOE_HD uint32_t word_of(uint64_t weight, int j) {
+  return static_cast<uint32_t>(weight >> (kWordBits * j)) & ((1u << kWordBits) - 1u);
+}
+MOE_HD uint64_t of_word(uint32_t sum, int j) { return static_cast<uint64_t>(sum) << (kWordBits * j); }
+
 }  // namespace moe

@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "moe_common.cuh"
+#include "moe_exact.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -30,7 +31,6 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;       // of a cluster (a row)
-constexpr int kMaxV = 393216;  // sums of so many weights stay below 2^64
 constexpr float kNegInf = -INFINITY;
 
 // 2^(j / 32) in units of 2^-31, rounded.
@@ -152,12 +152,13 @@ __device__ __forceinline__ uint64_t times_fraction(uint64_t x, float f, bool* mo
 }
 
 constexpr int kBins = 1536;        // counted: 45 octaves of weight by 32, a multiple of the threads
-constexpr int kUsedBins = 45 * 32;
-constexpr int kSub = kBins / 3;    // a value's range is divided by this, 3 words of 15 bits a sum
+constexpr int kUsedBins = kWeightBits * 32;
+constexpr int kSub = 512;          // a value's range is divided by this
 constexpr int kList = 1024;        // tokens that one CTA sorts
 constexpr int kPer = kList / kThreads;
 constexpr uint32_t kHistBytes = kBins * 4, kListBytes = kList * 8;
 static_assert(kSub == kThreads && kList % kThreads == 0, "a part of a range per thread");
+static_assert(kWords * kSub * 4 <= kHistBytes + kListBytes, "a range's sums lie over the counts and the first list");
 
 __device__ __forceinline__ uint32_t ld_peer32(const void* p, uint32_t rank) {
   uint32_t v;
@@ -381,8 +382,9 @@ struct Row {
     }
     sync_row();
   }
+  template <int N = kBins>
   __device__ __forceinline__ void clear_hist() const {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < N; i += kThreads) hist[i] = 0;
     __syncthreads();
   }
 
@@ -509,22 +511,21 @@ struct Row {
   // ------------------------------------------------------- ranges by parts
   // The rank key of the last of the ranking's first tokens, of those that `stays`, whose f sums to
   // `need` (at least 1, and reached): the range of keys is divided until one value is left.  `above`
-  // is the sum above the range; where the end is not in it, all begins again with all keys.
+  // is the sum above the range; where the end is not in it, all begins again with all keys, once: 0
+  // if it is not among those, which no exact sums lead to.
   template <class S, class F>
   __device__ __forceinline__ uint64_t select(uint32_t klo, uint32_t khi, uint64_t above, S stays, F f, uint64_t need) {
-    for (;;) {
+    for (bool again = false;;) {
       const int shift = max(32 - __clz(static_cast<int>(khi - klo)) - 9, 0);  // kSub = 2^9
       const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
-      clear_hist();
+      clear_hist<kWords * kSub>();
       each([&](float v, int i) {
         if (v >= v_lo && v <= v_hi && i >= off && i < off + n && stays(v, i)) {
-          const uint64_t w = f(v);  // by 15 bits in three words
+          const uint64_t w = f(v);
           const uint32_t part = (khi - order_key(v + 0.0f)) >> shift;
-          atomicAdd(&hist[part], static_cast<uint32_t>(w) & 0x7fffu);
-          if (w >> 15) {
-            atomicAdd(&hist[kSub + part], static_cast<uint32_t>(w >> 15) & 0x7fffu);
-            atomicAdd(&hist[2 * kSub + part], static_cast<uint32_t>(w >> 30));
-          }
+#pragma unroll
+          for (int j = 0; j < kWords; ++j)
+            if (word_of(w, j)) atomicAdd(&hist[j * kSub + part], word_of(w, j));
         }
       });
       turn ^= 1;
@@ -534,15 +535,16 @@ struct Row {
         uint64_t v = 0, all;
 #pragma unroll
         for (int r0 = 0; r0 < kMaxCtas; r0 += 4) {
-          uint32_t o[4][3] = {};
+          uint32_t o[4][kWords] = {};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
+            for (int j = 0; j < kWords; ++j)
               if (r0 + u < C) o[u][j] = ld_peer32(hist + j * kSub + t, r0 + u);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            v += o[u][0] + (static_cast<uint64_t>(o[u][1]) << 15) + (static_cast<uint64_t>(o[u][2]) << 30);
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) v += of_word(o[u][j], j);
         }
         const uint64_t at = above + scan(v, &all);
         if (at < need && at + v >= need) {
@@ -554,6 +556,8 @@ struct Row {
       tell(2);
       const uint32_t t = static_cast<uint32_t>(sh.said[turn][0]);
       if (t == kSub) {
+        if (again) return 0;
+        again = true;
         klo = order_key(kNegInf), khi = order_key(INFINITY);
         above = 0;
         continue;
@@ -1017,6 +1021,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
   float v_cut = kNegInf;
   const auto stays = [&](float v, int i) { return v > v_cut || (v == v_cut && R::key_of(v, r.first + i) >= cut); };
   const auto any = [](float, int) { return true; };
+  const auto lost = [&] {  // (a border that was not found: no token, the same in every CTA)
+    if (rank == 0 && threadIdx.x == 0) {
+      *token = -1;
+      if (logprob) *logprob = NAN;
+    }
+  };
   const auto set_cut = [&](uint64_t key) {
     cut = key;
     v_cut = value_of_key(key);
@@ -1085,6 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
       }
       if (m < 0 || cut == 0)
         set_cut(r.select(klo, khi, above, any, [](float) { return static_cast<uint64_t>(1); }, k));
+      if (cut == 0) return lost();
     }
     if (by_p) {
       if (by_k) {
@@ -1157,10 +1168,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
                 const int o = static_cast<int>((reinterpret_cast<uintptr_t>(g) / sizeof(T) + c * per) % kVec);
                 const int its = min(a.V, (c + 1) * per) - c * per;
                 const int pw = ((o + its + kVec - 1) / kVec + kWarps - 1) / kWarps;
-                const int at3 = 3 * (c * kWarps + (at - c * per + o) / kVec / pw);  // by 15 bits, as no
-                atomicAdd(&r.hist[at3], static_cast<uint32_t>(w[j]) & 0x7fffu);    // 64-bit sums are made there
-                atomicAdd(&r.hist[at3 + 1], static_cast<uint32_t>(w[j] >> 15) & 0x7fffu);
-                atomicAdd(&r.hist[at3 + 2], static_cast<uint32_t>(w[j] >> 30));
+                const int of = kWords * (c * kWarps + (at - c * per + o) / kVec / pw);  // in words, as no
+#pragma unroll
+                for (int u = 0; u < kWords; ++u) atomicAdd(&r.hist[of + u], word_of(w[j], u));  // 64-bit sums are made there
               }
             }
             before += w[j];
@@ -1168,9 +1178,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
           __syncthreads();
           // the warp that has the token drawn
           const int regions = C * kWarps;
-          if (static_cast<int>(threadIdx.x) < regions)
-            keep = sh.region[threadIdx.x] + r.hist[3 * threadIdx.x] + (static_cast<uint64_t>(r.hist[3 * threadIdx.x + 1]) << 15) +
-                   (static_cast<uint64_t>(r.hist[3 * threadIdx.x + 2]) << 30);
+          if (static_cast<int>(threadIdx.x) < regions) {
+            keep = sh.region[threadIdx.x];
+#pragma unroll
+            for (int u = 0; u < kWords; ++u) keep += of_word(r.hist[kWords * threadIdx.x + u], u);
+          }
           const uint64_t from = r.scan(keep, &all);
           const uint64_t target = times_fraction(all, ask.u);
           if (target >= from && target < from + keep) {
@@ -1192,6 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
       }
       if (m < 0 || sh.said[r.turn][0] == 0) {
         set_cut(r.select(klo, khi, above, stays, [&](float v) { return r.weight(v); }, need));
+        if (cut == 0) return lost();
         if (v_cut <= v_hi) {  // all above the window stay, and were added up
           known = high;
           v_known = v_hi;
@@ -1269,7 +1282,7 @@ using namespace moe;
 extern "C" moe_status_t moe_sample(const moe_sampling_t* s, void* stream) {
   if (!s) return set_error(MOE_ERR_INVALID_ARG, "moe_sampling_t is NULL");
   if (s->B < 0 || s->V < 1) return set_error(MOE_ERR_INVALID_ARG, "B must be >= 0 and V >= 1");
-  if (s->V > kMaxV) return set_error(MOE_ERR_UNSUPPORTED, "V must be at most %d", kMaxV);
+  if (s->V > kMaxLogits) return set_error(MOE_ERR_UNSUPPORTED, "V must be at most %d", kMaxLogits);
   if (s->B > (1 << 24)) return set_error(MOE_ERR_UNSUPPORTED, "B must be at most 2^24");
   if (s->dtype != MOE_F16 && s->dtype != MOE_BF16 && s->dtype != MOE_F32)
     return set_error(MOE_ERR_UNSUPPORTED, "dtype must be MOE_F16, MOE_BF16 or MOE_F32");
