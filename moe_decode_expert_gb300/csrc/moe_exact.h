@@ -71,4 +71,18 @@ MOE_HD uint32_t word_of(uint64_t weight, int j) {
 }
 MOE_HD uint64_t of_word(uint32_t sum, int j) { return static_cast<uint64_t>(sum) << (kWordBits * j); }
 
+// Ranges of order keys (order_key() of a value, -0 as 0) are divided by 512: the shift that does so,
+// and the part of a key in [lo, hi], from hi downwards.  Always below 512; comparing values in place
+// of keys lets a +0 into a range that ends at the key of -0.
+MOE_HD int part_shift(uint32_t lo, uint32_t hi) {
+#ifdef __CUDA_ARCH__
+  const int bits = 32 - __clz(static_cast<int>(hi - lo));
+#else
+  const int bits = hi == lo ? 0 : 32 - __builtin_clz(hi - lo);
+#endif
+  return bits > 9 ? bits - 9 : 0;
+}
+MOE_HD bool in_range(uint32_t key, uint32_t lo, uint32_t hi) { return key - lo <= hi - lo; }
+MOE_HD uint32_t part_of(uint32_t key, uint32_t hi, int shift) { return (hi - key) >> shift; }
+
 }  // namespace moe

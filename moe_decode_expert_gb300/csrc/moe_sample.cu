@@ -393,7 +393,8 @@ struct Row {
     if (wt.infinite || n == INFINITY) return order_key(INFINITY);
     if (n == -INFINITY) return order_key(kNegInf);
     const float x = n / wt.hi, v = wt.base + x;
-    return order_key(fmaf(fabsf(wt.base) + fabsf(x), room, v + room * 1e-30f));
+    // (-0 as 0, as the tokens' keys have it; past the largest float: infinity, not a number's key)
+    return min(order_key(fmaf(fabsf(wt.base) + fabsf(x), room, v + room * 1e-30f) + 0.0f), order_key(INFINITY));
   }
   // The least value that a token with some weight, down to bin b, has.
   __device__ __forceinline__ float least_of(int b) const {
@@ -510,19 +511,21 @@ struct Row {
 
   // ------------------------------------------------------- ranges by parts
   // The rank key of the last of the ranking's first tokens, of those that `stays`, whose f sums to
-  // `need` (at least 1, and reached): the range of keys is divided until one value is left.  `above`
+  // `need` (at least 1, and reached): the range of keys, between those of the infinities, is divided
+  // until one value is left.  `above`
   // is the sum above the range; where the end is not in it, all begins again with all keys, once: 0
   // if it is not among those, which no exact sums lead to.
   template <class S, class F>
   __device__ __forceinline__ uint64_t select(uint32_t klo, uint32_t khi, uint64_t above, S stays, F f, uint64_t need) {
     for (bool again = false;;) {
-      const int shift = max(32 - __clz(static_cast<int>(khi - klo)) - 9, 0);  // kSub = 2^9
-      const float v_lo = value_of_order(klo), v_hi = value_of_order(khi);
+      const int shift = part_shift(klo, khi);
+      static_assert(kSub == 512, "what part_shift() divides by");
       clear_hist<kWords * kSub>();
       each([&](float v, int i) {
-        if (v >= v_lo && v <= v_hi && i >= off && i < off + n && stays(v, i)) {
+        const uint32_t key = order_key(v + 0.0f);
+        if (in_range(key, klo, khi) && i >= off && i < off + n && stays(v, i)) {
           const uint64_t w = f(v);
-          const uint32_t part = (khi - order_key(v + 0.0f)) >> shift;
+          const uint32_t part = part_of(key, khi, shift);
 #pragma unroll
           for (int j = 0; j < kWords; ++j)
             if (word_of(w, j)) atomicAdd(&hist[j * kSub + part], word_of(w, j));
@@ -570,7 +573,7 @@ struct Row {
     // one value is left: by index
     const auto tie = [&](float v, int i) {
       const uint32_t key = order_key(v + 0.0f);
-      return v == v && key >= klo && key <= khi && i >= off && i < off + n && stays(v, i) ? f(v) : 0ull;
+      return in_range(key, klo, khi) && i >= off && i < off + n && stays(v, i) ? f(v) : 0ull;
     };
     sum(tie);
     locate(tie, need - above - 1, [&](float v, int i) {
