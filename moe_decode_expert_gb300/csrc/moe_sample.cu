@@ -915,8 +915,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(moe_sampling_t a, i
         }
         if constexpr (HELD) s[i] = raw;
         else reinterpret_cast<T*>(&sh.edge[e])[threadIdx.x & (kVec - 1)] = raw;
-        mine_edge = f;
-        i_edge = i;
+        if (!e || chunks > 1) {  // (of one chunk alone each token is one thread's)
+          mine_edge = f;
+          i_edge = i;
+        }
       }
     }
   }
