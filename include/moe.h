@@ -420,9 +420,9 @@ MOE_API moe_status_t moe_quantize_e4m3(const moe_quant_t* q, void* stream);
  * out_dtype.  Results do not depend on timing.
  * Any M, N >= 0, K >= 1; x and w begin on 16 bytes and their row strides are
  * multiples of 16 elements; what lies between the rows is not
- * read.  out has any strides >= N between rows.  Scales are any floats: a NaN
- * or infinity in a row, a weight row or a scale reaches only what it is a
- * factor of.  Limit: ceil(M / 16) * ceil(N / 128) below 2^28.
+ * read.  out has any strides >= N between rows.  Scales are any floats (two whose
+ * product is no normal fp32 number are applied one after the other): a NaN or
+ * infinity in a row, a weight row or a scale reaches only what it is a factor of.  Limit: ceil(M / 16) * ceil(N / 128) below 2^28.
  * ws: any workspace of this library (only its status word is used: a wait that
  * ran out is recorded there, MOE_ERR_TIMEOUT from moe_query_status). */
 typedef struct moe_linear {

@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 
 #ifdef __CUDACC__
@@ -57,6 +58,25 @@ struct Quotient {
     }
   }
 };
+
+// Two scales of a block's sum p of e4m3 products are applied as their product where that is a normal
+// number, else one after the other, the larger first where neither is zero: |p| is 0 or from 2^-18 to
+// 2^25, so p times the larger has all its bits unless the whole is infinite or zero in fp32 itself.
+MOE_HD bool normal(float s) {
+  uint32_t b;
+#ifdef __CUDA_ARCH__
+  b = __float_as_uint(s);
+#else
+  std::memcpy(&b, &s, 4);
+#endif
+  return 2u * b - 0x01000000u < 0xfe000000u;
+}
+constexpr float kNearScale = 0x1p-63f;  // two scales from this to below its reciprocal have a normal product
+MOE_HD float add_scaled(float sum, float p, float a, float b) {
+  if (normal(a * b) || a == 0.0f || b == 0.0f) return fmaf(p, a * b, sum);
+  const bool swap = fabsf(a) < fabsf(b);
+  return fmaf(p * (swap ? b : a), swap ? a : b, sum);
+}
 
 // Sums of the draw's weights in 32-bit words, kWordBits of every weight in each: a CTA may have every
 // token of the longest row, all in one sum.

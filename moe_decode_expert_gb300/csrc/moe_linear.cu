@@ -8,7 +8,9 @@
 // tensor memory that starts at zero; an epilogue warp reads it and adds it, times
 // its two scales, to fp32 sums in registers while the next block's product is made
 // in another accumulator.  A block of K is 128 bytes, one row of the 128-byte
-// swizzle, so a stage of the ring is one block of both operands.
+// swizzle, so a stage of the ring is one block of both operands.  The two scales
+// are applied as their product; a chunk of blocks in which some product is no
+// normal number is summed by another loop, which applies them one after the other.
 //
 // Few rows stream the weight: 8 x 151936 x 2048 51 us, 6150 GB/s, 92 % of the copy;
 // one row x 5120 x 2048 3.9 us in a graph, launch and latency.  Many rows are bound by
@@ -18,6 +20,7 @@
 #include <algorithm>
 
 #include "moe_common.cuh"
+#include "moe_exact.h"
 #include "moe_internal.h"
 #include "moe_tc.cuh"
 
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(192, 2)
   float* scales = reinterpret_cast<float*>(smem + stages * F::kStage);
   __shared__ __align__(8) uint64_t full[F::kMaxStages], empty[F::kMaxStages], tfull[F::kAcc], tempty[F::kAcc], done, inbox;
   __shared__ uint32_t tmem_base_s;
-  __shared__ volatile int s_abort;
+  __shared__ volatile int s_abort, s_odd[2];
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x % S);
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(192, 2)
     mbar_init(&done, 1);
     mbar_init(&inbox, 1);
     mbar_fence_init();
-    s_abort = 0;
+    s_abort = s_odd[0] = s_odd[1] = 0;
     // (others' sums of this CTA's columns, fours or twos with a token)
     if (S > 1)
       mbar_arrive_expect_tx(&inbox, static_cast<uint32_t>((max(min(a.M - m0 - rank * width, width), 0) + vec - 1) / vec * (S - 1) * vec) * 512u);
@@ -234,63 +237,97 @@ __global__ void __launch_bounds__(192, 2)
     float next[kPer];
     // A chunk's blocks are 2^cb, of kChunk at most: where there are few, no thread asks for others.
     const int cb = min(32 - __clz(nkb - 1), kChunkBits), cmask = (1 << cb) - 1;
-    // products of both scales for blocks [c << cb, ..), zero beyond M and the last block
+    // products of both scales for blocks [c << cb, ..), anything normal beyond M and the last block
     const auto fetch = [&](int chunk) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int at = etid + 128 * u, t = at >> cb, i = (chunk << cb) + (at & cmask);
-        next[u] = 0.0f;
+        next[u] = 1.0f;
         if (t < NT && i < nkb && m0 + t < a.M)
           next[u] = a.x_scales[static_cast<int64_t>(m0 + t) * KB + kb0 + i] *
                     a.w_scales[static_cast<int64_t>(nt) * KB + kb0 + i];
       }
     };
-    const auto stage_scales = [&](int buf) {
+    // (s_odd says of a chunk whether some product is infinite or below the normal numbers)
+    const auto stage_scales = [&](int chunk) {
+      float least = 1.0f, most = 1.0f;
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int at = etid + 128 * u, t = at >> cb;
-        if (t < NT) scales[(buf * F::kChunk + (at & cmask)) * F::kPitch + t] = next[u];
+        least = fminf(least, fabsf(next[u]));
+        most = fmaxf(most, fabsf(next[u]));
+        if (t < NT) scales[((chunk & 1) * F::kChunk + (at & cmask)) * F::kPitch + t] = next[u];
       }
+      if (!normal(least) || !normal(most)) s_odd[chunk & 1] = chunk + 1;
+    };
+    bool ok = true;
+    // Waits for block i's sums (a wait that ran out leaves the loop running without it, so that all
+    // warps meet at the barriers); their address.
+    const auto begin = [&](int i) {
+      const int b = i % F::kAcc;
+      ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], (i / F::kAcc) & 1, timeout, &s_abort));
+      if (ok) tc_fence_after();
+      else s_abort = 1;
+      return tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * NT);
+    };
+    const auto release = [&](int i) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[i % F::kAcc]);
+    };
+    // Blocks [i0, i1), a chunk with such products: small code with the sums in local memory, as it
+    // seldom runs and lies between what does.
+    const auto add_odd = [&](int i0, int i1) {
+      float sum[NT];
+#pragma unroll
+      for (int c = 0; c < NT; ++c) sum[c] = acc[c];
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) {
+        const uint32_t ta = begin(i);
+        if (!ok) continue;
+#pragma unroll 1
+        for (int c = 0; c < NT && m0 + c < a.M; ++c)
+          sum[c] = add_scaled(sum[c], tmem_ld1(ta + c), a.x_scales[static_cast<int64_t>(m0 + c) * KB + kb0 + i],
+                              a.w_scales[static_cast<int64_t>(nt) * KB + kb0 + i]);
+        release(i);
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) acc[c] = sum[c];
     };
     fetch(0);
-    bool ok = true;
     for (int i = 0; i < nkb; ++i) {
       const int chunk = i >> cb, in = i & cmask;
       if (in == 0) {
-        stage_scales(chunk & 1);
+        stage_scales(chunk);
         named_bar_sync(1, 128);  // (also: every warp is past the chunk before the last, whose place this was)
-        if ((chunk + 1) << cb < nkb) fetch(chunk + 1);
-      }
-      const int b = i % F::kAcc;
-      // (a wait that ran out leaves the loop running without it, so that all warps meet at the barriers)
-      ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], (i / F::kAcc) & 1, timeout, &s_abort));
-      if (ok) {
-        tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(scales + ((chunk & 1) * F::kChunk + in) * F::kPitch);
-        const uint32_t ta = tbase + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * NT);
-#pragma unroll
-        for (int c0 = 0; c0 < NT; c0 += kStep) {
-          uint32_t v[kStep];
-          if constexpr (kStep == 32) tmem_ld32_issue(ta + c0, v);
-          else tmem_ld16_issue(ta + c0, v);
-          tmem_ld_wait();
-          tmem_ld_tie(v);
-          if (c0 + kStep == NT) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[b]);
-          }
-#pragma unroll
-          for (int j = 0; j < kStep / 4; ++j) {
-            const float4 s = sc[c0 / 4 + j];
-            acc[c0 + 4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[c0 + 4 * j]);
-            acc[c0 + 4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[c0 + 4 * j + 1]);
-            acc[c0 + 4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[c0 + 4 * j + 2]);
-            acc[c0 + 4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[c0 + 4 * j + 3]);
-          }
+        const int next_i = (chunk + 1) << cb;
+        const bool odd = s_odd[chunk & 1] == chunk + 1;
+        if (odd) add_odd(i, min(nkb, next_i));
+        if (next_i < nkb) fetch(chunk + 1);
+        if (odd) {
+          i = next_i - 1;
+          continue;
         }
-      } else {
-        s_abort = 1;
+      }
+      const uint32_t ta = begin(i);
+      if (!ok) continue;
+      const float4* sc = reinterpret_cast<const float4*>(scales + ((chunk & 1) * F::kChunk + in) * F::kPitch);
+#pragma unroll
+      for (int c0 = 0; c0 < NT; c0 += kStep) {
+        uint32_t v[kStep];
+        if constexpr (kStep == 32) tmem_ld32_issue(ta + c0, v);
+        else tmem_ld16_issue(ta + c0, v);
+        tmem_ld_wait();
+        tmem_ld_tie(v);
+        if (c0 + kStep == NT) release(i);
+#pragma unroll
+        for (int j = 0; j < kStep / 4; ++j) {
+          const float4 s = sc[c0 / 4 + j];
+          acc[c0 + 4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[c0 + 4 * j]);
+          acc[c0 + 4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[c0 + 4 * j + 1]);
+          acc[c0 + 4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[c0 + 4 * j + 2]);
+          acc[c0 + 4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[c0 + 4 * j + 3]);
+        }
       }
     }
     if (!ok && lane == 0) report_error(ctrl, kDevTimeoutCopy, blockIdx.x);
@@ -488,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
   __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], tfull[G::kAcc], tempty[G::kAcc], sfull[2], sempty[2],
       done[G::kIssuers];
   __shared__ uint32_t tmem_base_s;
-  __shared__ volatile int s_abort;
+  __shared__ volatile int s_abort, s_far[2];  // (of a chunk of scales: whether some are far from 1)
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x & 1u);  // in the pair; 0 issues the MMAs
@@ -602,18 +639,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
         ok = __all_sync(0xffffffffu, tc_wait_polled(&sempty[buf], phase ^ 1u, timeout, &s_abort));
         if (!ok) break;
         float* sc = scales + buf * G::kScales;
-        if (lane % G::kChunk + kb0 < KB && lane < N / 128 * G::kChunk)  // (past the last weight block: any)
-          sc[G::kChunk * 128 + lane] =
+        float least = 1.0f, most = 1.0f;  // magnitudes of this lane's scales
+        if (lane % G::kChunk + kb0 < KB && lane < N / 128 * G::kChunk) {  // (past the last weight block: any)
+          const float w =
               a.w_scales[static_cast<int64_t>(min(nb + lane / G::kChunk, (a.N - 1) / 128)) * KB + kb0 + lane % G::kChunk];
+          sc[G::kChunk * 128 + lane] = w;
+          least = most = fabsf(w);
+        }
 #pragma unroll 1
         for (int r = lane; r < 128; r += 32) {
           const float* from = a.x_scales + static_cast<int64_t>(min(m0 + r, a.M - 1)) * KB + kb0;
           float v[G::kChunk];
 #pragma unroll
-          for (int i = 0; i < G::kChunk; ++i) v[i] = kb0 + i < KB ? from[i] : 0.0f;
+          for (int i = 0; i < G::kChunk; ++i) v[i] = kb0 + i < KB ? from[i] : 1.0f;
 #pragma unroll
-          for (int i = 0; i < G::kChunk; ++i) sc[i * 128 + r] = v[i];
+          for (int i = 0; i < G::kChunk; ++i) {
+            sc[i * 128 + r] = v[i];
+            least = fminf(least, fabsf(v[i]));
+            most = fmaxf(most, fabsf(v[i]));
+          }
         }
+        const bool far = __any_sync(0xffffffffu, least < kNearScale || most >= 1.0f / kNearScale);
+        if (lane == 0) s_far[buf] = far;
         mbar_arrive(&sfull[buf]);
         buf ^= 1;
         phase ^= buf == 0;
@@ -630,49 +677,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Many<N>::kThreads, 1
     const uint32_t free_bar = peer_addr(smem_u32(&tempty[0]), 0);
     float* scales = reinterpret_cast<float*>(smem + G::kStages * G::kStage + G::kWarps * G::kTurn);
     uint8_t* turn = smem + G::kStages * G::kStage + (warp - 4) * G::kTurn;
-    int b = 0, buf = 0, in = 0;  // accumulator; chunk of scales and block in it
+    int b = 0, buf = 0;  // accumulator; chunk of scales
     uint32_t bphase = 0, sphase = 0;
     bool ok = true;
     for (int t = first; t < tiles; t += step) {
       float acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0.0f;
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb0 = 0; kb0 < KB; kb0 += G::kChunk) {
         // (a wait that ran out leaves the loops running without it, so that all warps end together)
-        if (in == 0) ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&sfull[buf], sphase, timeout, &s_abort));
+        ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&sfull[buf], sphase, timeout, &s_abort));
         const float* sc = scales + buf * G::kScales;
-        const float s = sc[in * 128 + 32 * q + lane] * sc[G::kChunk * (128 + (g >> 1)) + in];
-        if (++in == G::kChunk || kb + 1 == KB) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[buf]);
-          in = 0;
-          buf ^= 1;
-          sphase ^= buf == 0;
-        }
-        ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], bphase, timeout, &s_abort));
-        if (!ok) {
-          s_abort = 1;
-          continue;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 64; c += 32 * G::kLoads) {
-          uint32_t v[G::kLoads][32];
-#pragma unroll
-          for (int u = 0; u < G::kLoads; ++u) tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * N + c + 32 * u), v[u]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < G::kLoads; ++u) tmem_ld_tie(v[u]);
-          if (c + 32 * G::kLoads == 64) {
-            tc_fence_before();
+        const int n = min(G::kChunk, KB - kb0);
+        // Reads this row's scales, and waits for the block's sums.
+        const auto begin = [&](int in, float& sx, float& sw) {
+          sx = sc[in * 128 + 32 * q + lane], sw = sc[G::kChunk * (128 + (g >> 1)) + in];
+          if (in + 1 == n) {
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
+            if (lane == 0) mbar_arrive(&sempty[buf]);
+          }
+          ok = __all_sync(0xffffffffu, ok && tc_wait_polled(&tfull[b], bphase, timeout, &s_abort));
+          if (ok) tc_fence_after();
+          else s_abort = 1;
+        };
+        const auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(free_bar + static_cast<uint32_t>(8 * b));
+        };
+        if (!s_far[buf]) {
+          for (int in = 0; in < n; ++in) {
+            float s, sw;
+            begin(in, s, sw);
+            if (!ok) continue;
+            s *= sw;
+#pragma unroll
+            for (int c = 0; c < 64; c += 32 * G::kLoads) {
+              uint32_t v[G::kLoads][32];
+#pragma unroll
+              for (int u = 0; u < G::kLoads; ++u) tmem_ld32_issue(lane0 + static_cast<uint32_t>(b * N + c + 32 * u), v[u]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int u = 0; u < G::kLoads; ++u) tmem_ld_tie(v[u]);
+              if (c + 32 * G::kLoads == 64) release();
+#pragma unroll
+              for (int j = 0; j < 32 * G::kLoads; j += 2)
+                fma2(acc[c + j], acc[c + j + 1], v[j / 32][j % 32], v[j / 32][j % 32 + 1], s);
+            }
+            if (++b == G::kAcc) { b = 0; bphase ^= 1u; }
+          }
+        } else {  // (seldom: small code, with the sums in local memory)
+          float sum[64];
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sum[c] = acc[c];
+#pragma unroll 1
+          for (int in = 0; in < n; ++in) {
+            float sx, sw;
+            begin(in, sx, sw);
+            if (!ok) continue;
+#pragma unroll 1
+            for (int c = 0; c < 64; ++c)
+              sum[c] = add_scaled(sum[c], tmem_ld1(lane0 + static_cast<uint32_t>(b * N + c)), sx, sw);
+            release();
+            if (++b == G::kAcc) { b = 0; bphase ^= 1u; }
           }
 #pragma unroll
-          for (int j = 0; j < 32 * G::kLoads; j += 2)
-            fma2(acc[c + j], acc[c + j + 1], v[j / 32][j % 32], v[j / 32][j % 32 + 1], s);
+          for (int c = 0; c < 64; ++c) acc[c] = sum[c];
         }
-        if (++b == G::kAcc) { b = 0; bphase ^= 1u; }
+        buf ^= 1;
+        sphase ^= buf == 0;
       }
       if (!ok) continue;
       const int m0 = t % mtiles * 256 + rank * 128 + 32 * q, n0 = t / mtiles * N + 64 * g;
