@@ -167,16 +167,19 @@ def _bind_fast_call(lib):
     entries = (lib.moe_add_rmsnorm, lib.moe_rope_append, lib.moe_paged_attention)
     structs = (_NORM_T, _CACHE_T, _ROPE_T, _ATTN_T)
     at = lambda fs: (ctypes.cast(f, ctypes.c_void_p).value for f in fs)  # noqa: E731
+    warning = ("the compiled argument checks%s were built for another PyTorch or header and are not used: "
+               "build them with __graft_entry__.build()")
     if getattr(_fast_call, "built_for", None) != torch.__version__ or not _fast_call.bind(
             *at(entries), *(t.size for t in structs)):
-        warnings.warn("the compiled argument checks were built for another PyTorch or header and are not used: "
-                      "build them with __graft_entry__.build()")
+        warnings.warn(warning % "")
         return
     _fast = _fast_call
     bind = getattr(_fast_call, "bind_projections", None)
-    if bind is not None and bind(*at((lib.moe_quantize_e4m3, lib.moe_linear_e4m3, lib.moe_sample)), _QUANT_T.size,
-                                 _LINEAR_T.size, _SAMPLING_T.size):
-        _fast_projections = _fast_call
+    if bind is None or not bind(*at((lib.moe_quantize_e4m3, lib.moe_linear_e4m3, lib.moe_sample)), _QUANT_T.size,
+                                _LINEAR_T.size, _SAMPLING_T.size):
+        warnings.warn(warning % " of the 8-bit projections and the draw")
+        return
+    _fast_projections = _fast_call
 
 
 def library():
