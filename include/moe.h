@@ -487,7 +487,9 @@ MOE_API moe_status_t moe_get_stats(moe_stats_t* stats);
 MOE_API void moe_reset_stats(void);
 
 /* Upper bound, in nanoseconds of GPU global time, on every device-side wait
- * of later launches (default 2e9 = 2 s).  Values below 1000 are refused. */
+ * of later launches (default 2e9 = 2 s).  Values below 1000 are refused.  The
+ * tensor-core kernels (the grouped passes, moe_linear_e4m3) wait for up to 10 ms
+ * whatever is set: their copies in flight have to end before they may leave. */
 MOE_API moe_status_t moe_set_wait_timeout_ns(uint64_t ns);
 
 /* Test hook for the failure path: enqueues one kernel that waits, with the

@@ -996,7 +996,7 @@ static moe_status_t launch_tc_passes(const moe_cfg_t& c, const BlockPtrs& p, uin
   float* y = reinterpret_cast<float*>(ws + L.g_y);
   const float* glog = reinterpret_cast<const float*>(ws + L.r_logits);
   const int gate_stride = c.has_shared_gate ? E + 1 : E;
-  const uint64_t timeout = wait_timeout_ns();
+  const uint64_t timeout = tc_wait_timeout_ns();
 
   // M-tiles per W13 tile: two share every token stage (half the token
   // traffic), but when the pairs are few that leaves SMs idle, so a single
@@ -1132,7 +1132,7 @@ moe_status_t launch_tc_router(const moe_cfg_t& c, const void* x, const void* rou
   const int tiles = tiles0 * S;
   const int g = tiles < sms ? tiles : sms;
   launch_pdl(kern, dim3(g), dim3(kTcThreads), smem, st, mWr, mG, mX, T, H, E, E1, mE, nm, S,
-             S > 1 ? part : logits, ctrl, wait_timeout_ns());
+             S > 1 ? part : logits, ctrl, tc_wait_timeout_ns());
   if (moe_status_t s = check_launch("tc_router_kernel")) return s;
   stat_kernels(1);
   return MOE_OK;

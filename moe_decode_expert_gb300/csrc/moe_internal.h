@@ -90,6 +90,14 @@ void stat_kernels(uint64_t n);
 // Device properties cached per device.
 int sm_count();
 uint64_t wait_timeout_ns();
+// The limit of waits in kernels on tcgen05 and TMA: 10 ms at least.  Such a kernel leaves after a wait
+// that ran out only once its copies and MMAs in flight have ended, and in a pair of CTAs one learns
+// that the other has given up by its own waits: a limit of microseconds could end both before a
+// copy into their shared memory has.
+inline uint64_t tc_wait_timeout_ns() {
+  const uint64_t ns = wait_timeout_ns(), least = 10000000;
+  return ns < least ? least : ns;
+}
 
 // Pointers of one MoE block call.
 struct BlockPtrs {

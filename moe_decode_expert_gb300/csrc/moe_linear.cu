@@ -811,7 +811,7 @@ moe_status_t launch_few(const moe_linear_t& l, int KB, Control* ctrl, cudaStream
   attr[1].val.clusterDim = {static_cast<unsigned>(S), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, linear_few_kernel<NT>, mw, mx, l, KB, S, mtiles, stages, ctrl, wait_timeout_ns()) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, linear_few_kernel<NT>, mw, mx, l, KB, S, mtiles, stages, ctrl, tc_wait_timeout_ns()) != cudaSuccess)
     return check_launch("linear_few_kernel");
   stat_kernels(1);
   return MOE_OK;
@@ -835,7 +835,7 @@ moe_status_t launch_many(const moe_linear_t& l, int KB, Control* ctrl, cudaStrea
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (linear)");
   const int pairs = sm_count() / 2;
   if (launch_pdl(linear_many_kernel<N>, dim3(2 * (tiles < pairs ? tiles : pairs)), dim3(Many<N>::kThreads), Many<N>::kSmem,
-                 st, mx, mw, mo, l, KB, mtiles, tiles, bulk, ctrl, wait_timeout_ns()) != cudaSuccess)
+                 st, mx, mw, mo, l, KB, mtiles, tiles, bulk, ctrl, tc_wait_timeout_ns()) != cudaSuccess)
     return check_launch("linear_many_kernel");
   stat_kernels(1);
   return MOE_OK;
