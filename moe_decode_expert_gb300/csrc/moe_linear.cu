@@ -12,10 +12,10 @@
 // are applied as their product; a chunk of blocks in which some product is no
 // normal number is summed by another loop, which applies them one after the other.
 //
-// Few rows stream the weight: 8 x 151936 x 2048 51 us, 6150 GB/s, 92 % of the copy;
+// Few rows stream the weight: 8 x 151936 x 2048 51 us, 6200 GB/s, 93 % of the copy;
 // one row x 5120 x 2048 3.9 us in a graph, launch and latency.  Many rows are bound by
 // the sums: reading a 256 x 256 accumulator and adding it takes as long as the MMAs
-// that make it (8192 x 5120 x 4096 136 us, 2525 TFLOP/s; 116 with no accumulator read).
+// that make it (8192 x 5120 x 4096 136 us, 2530 TFLOP/s; 116 with no accumulator read).
 
 #include <algorithm>
 

@@ -18,7 +18,8 @@
 //
 // One row is a chain of latencies (151936 logits 9 us); many rows are bound by their
 // instructions, about 50 a warp for 32 tokens where weights are summed: 256 rows of
-// 131072, fp32, 81 us without filters, 154 with a top-p that ends among thousands.
+// 131072, fp32, 81 us without filters, 155 with a top-p that ends among thousands.
+// (64 registers, for two CTAs an SM, spill 56 to 96 bytes.)
 
 #include <algorithm>
 
